@@ -454,6 +454,184 @@ int32_t cfr_paged_decode_path(int32_t q_fmt, const cfr_kv_pool *kv, int32_t max_
 cfr_status cfr_wait_probe(int64_t limit_cycles, int32_t arrive, uint32_t *err_word,
                           uint32_t *result, void *stream);
 
+/*
+ * Norms of queries and keys, position rotation and cache write of a step's new
+ * tokens in one pass: what runs between the q/k/v projection and the decode.
+ * For every new token t (0 <= t < num_tokens), with y_h a query or key row of
+ * head_dim values widened to fp32:
+ *
+ *   y   <- y * rsqrt(mean(y^2) + eps) * weight           (skipped when weight is NULL)
+ *   (a, b) <- (a cos - b sin, b cos + a sin)              over the first rotary_dim values,
+ *             angle = rope_positions[t] * inv_freq[i], i < rotary_dim / 2
+ *
+ * where pair i is (y[i], y[i + rotary_dim / 2]), or (y[2i], y[2i + 1]) when
+ * `interleaved` is non-zero (RoPE; CFR-Atlas page, "RoPE/ALiBi positional
+ * policy").  Norm and rotation are taken in fp32, the angle's reduction in
+ * fp64, so far positions lose nothing; each result is rounded once, to the type
+ * it is stored in.  Rotated queries go to q_out.  Key and value rows become
+ * token token_ids[t] of sequence seq_ids[t] in its F32 or BF16 page, resolved
+ * as cfr_append_kv resolves it (values pass unchanged but for that rounding).
+ *
+ *  kv          host; the F32 and BF16 pools in it are WRITTEN; other pools are ignored.
+ *  page_table, page_fmt (or NULL + uniform_fmt F32/BF16), max_pages, batch: as
+ *              for cfr_append_kv.
+ *  q, k, v     device [num_tokens][num_q_heads | num_kv_heads][head_dim], F32 or
+ *              BF16 (in_fmt); heads and values of a token are contiguous, tokens
+ *              are q_stride, k_stride, v_stride VALUES apart (so the three may be
+ *              views of one packed projection): each stride is at least the
+ *              token's own values and a multiple of 16 bytes, each base 16-byte
+ *              aligned.
+ *  q_weight, k_weight  device float [head_dim], 16-byte aligned, or NULL: no norm.
+ *  eps         >= 0.
+ *  rope_positions  device int32 [num_tokens] (a drafted token's may differ from
+ *              its place in the cache); NULL only when rotary_dim is 0.
+ *  inv_freq    device double [rotary_dim / 2], radians per position; NULL only when
+ *              rotary_dim is 0.
+ *  rotary_dim  0 (no rotation) or a multiple of 16, at most head_dim.
+ *  q_out       device [num_tokens][num_q_heads][head_dim] of in_fmt, contiguous,
+ *              16-byte aligned, written; must not overlap q, k or v.
+ *  seq_ids, token_ids  device int32 [num_tokens].  A negative seq_ids[t] or
+ *              token_ids[t] writes no K and V (a padded row); its query row is
+ *              computed all the same.  No two tokens may name the same place.
+ * Device-side faults leave that token's K and V unwritten and set err_word bits:
+ * a sequence >= batch or a token at or past max_pages * page_tokens
+ * (CFR_DEVERR_SEQ_LEN), a page that is not F32 or BF16 or whose pool is NULL
+ * (CFR_DEVERR_PAGE_FMT), a slot outside its pool (CFR_DEVERR_PAGE_ID).
+ */
+cfr_status cfr_qk_norm_rope_append(const cfr_kv_pool *kv, const int32_t *page_table,
+                                   int32_t max_pages, const uint8_t *page_fmt,
+                                   int32_t uniform_fmt, int32_t batch, const void *q,
+                                   int64_t q_stride, const void *k, int64_t k_stride,
+                                   const void *v, int64_t v_stride, int32_t in_fmt,
+                                   int32_t num_tokens, int32_t num_q_heads,
+                                   const float *q_weight, const float *k_weight, float eps,
+                                   const int32_t *rope_positions, const double *inv_freq,
+                                   int32_t rotary_dim, int32_t interleaved, void *q_out,
+                                   const int32_t *seq_ids, const int32_t *token_ids,
+                                   uint32_t *err_word, void *stream);
+
+/*
+ * Cache write: stores a ragged chunk of new tokens (a prefill chunk, or one
+ * token a sequence) into pages of ANY storage format, quantising as it writes.
+ * Sequence b's rows row_offsets[b] .. row_offsets[b + 1] - 1 of k_new and v_new
+ * become its tokens starts[b], starts[b] + 1, ...  Values are stored as fp32
+ * (F32 pages) or rounded to the nearest bfloat16 (BF16 pages).  A quantised
+ * page that the chunk touches, per kv head and for K and V apart, gets
+ *
+ *   scale' = max(scale if the page keeps earlier tokens, max|x| / Q)   (fp32; Q as
+ *            for cfr_demote_pages; x the chunk's rows of that page)
+ *
+ * where the page keeps its earlier tokens when the chunk starts past its first
+ * row: those rows are re-encoded, code -> nearest(code * scale / scale'), when
+ * the scale has grown, and left alone when it has not.  A chunk that starts on a page's first row
+ * starts the page anew, whatever it held.  New rows get the codes that
+ * cfr_demote_pages defines (IEEE division, ties to even, NaN left out of
+ * max|x|).  Rows of a page behind the chunk's end are left as they were.
+ *
+ *  kv          host; the pools and scales in it are WRITTEN.
+ *  page_table, page_fmt (or NULL + uniform_fmt), max_pages, batch: as for
+ *              cfr_paged_decode.
+ *  row_offsets device int32 [batch + 1], non-decreasing, row_offsets[0] >= 0,
+ *              row_offsets[batch] <= num_rows; equal neighbours write nothing.
+ *  starts      device int32 [batch], >= 0.
+ *  k_new, v_new device [num_rows][num_kv_heads][head_dim], F32 or BF16 (new_fmt),
+ *              heads contiguous, tokens k_stride and v_stride VALUES apart (at
+ *              least num_kv_heads * head_dim, a multiple of 16 bytes; bases
+ *              16-byte aligned).
+ *  num_rows    rows that k_new and v_new hold.
+ * Device-side faults skip and set err_word bits: a sequence whose offsets are
+ * not in order or whose tokens pass max_pages * page_tokens
+ * (CFR_DEVERR_SEQ_LEN); a page of an unknown format (CFR_DEVERR_PAGE_FMT),
+ * without a pool (CFR_DEVERR_POOL) or with a slot outside it
+ * (CFR_DEVERR_PAGE_ID).  No two sequences may share a written page.
+ */
+cfr_status cfr_write_kv(const cfr_kv_pool *kv, const int32_t *page_table, int32_t max_pages,
+                        const uint8_t *page_fmt, int32_t uniform_fmt, int32_t batch,
+                        const int32_t *row_offsets, const int32_t *starts, const void *k_new,
+                        int64_t k_stride, const void *v_new, int64_t v_stride, int32_t new_fmt,
+                        int32_t num_rows, uint32_t *err_word, void *stream);
+
+/*
+ * Cache read-back: the counterpart of cfr_write_kv.  Tokens starts[b] ..
+ * starts[b] + row_offsets[b + 1] - row_offsets[b] - 1 of every sequence come
+ * back as dense rows row_offsets[b] .. of k_out and v_out, expanded from
+ * whatever format their pages have (code * scale in fp32), as fp32 or rounded to
+ * the nearest bfloat16 (out_fmt).
+ *
+ * Arguments as for cfr_write_kv, with k_out, v_out device
+ * [num_rows][num_kv_heads][head_dim] written.  Rows that no sequence names, and
+ * those of skipped sequences and pages (same err_word bits), are left as they were.
+ */
+cfr_status cfr_read_kv(const cfr_kv_pool *kv, const int32_t *page_table, int32_t max_pages,
+                       const uint8_t *page_fmt, int32_t uniform_fmt, int32_t batch,
+                       const int32_t *row_offsets, const int32_t *starts, void *k_out,
+                       int64_t k_stride, void *v_out, int64_t v_stride, int32_t out_fmt,
+                       int32_t num_rows, uint32_t *err_word, void *stream);
+
+/* Most drafted tokens of one sequence in cfr_paged_decode_tree. */
+#define CFR_TREE_MAX_QUERIES 64
+
+/*
+ * Bytes of device workspace that cfr_paged_decode_tree needs for these sizes on
+ * the current device (independent of the context length).  0 when the sizes
+ * are invalid.
+ */
+size_t cfr_paged_decode_tree_workspace_size(int32_t batch, int32_t num_queries,
+                                            int32_t num_q_heads, int32_t num_kv_heads,
+                                            int32_t head_dim);
+
+/*
+ * Attention of a tree of drafted tokens over the paged cache (the verification
+ * step of tree-structured speculative decoding), optionally with capped scores.
+ * The last c_b = q_lens[b] of the n_b = seq_lens[b] cached tokens of sequence b
+ * are its drafted tokens, their K and V already in the cache; draft i sits at
+ * token n_b - c_b + i.  Query row (i, h) attends to every token before the
+ * drafts and to the drafts k < c_b whose bit k is set in tree_mask[b][i]
+ * (normally its ancestors and itself):
+ *
+ *   s_ij = softmax_scale * q_ih . k_j
+ *   s_ij = logit_cap * tanh(s_ij / logit_cap)              when logit_cap > 0
+ *   s_ij = s_ij - alibi_slopes[h] * (pos_i - pos_j)        when alibi_slopes is given
+ *   out = softmax_j(s) V,  lse = log sum_j exp(s_ij)
+ *
+ * pos_j = j before the drafts; draft k has pos = n_b - c_b + depths[b][k].
+ * A single causal query per sequence with capped scores is num_queries = 1.
+ *
+ *  q           device [batch][num_queries][num_q_heads][head_dim], F32 or BF16 (q_fmt),
+ *              16-byte aligned.
+ *  num_queries 1 .. CFR_TREE_MAX_QUERIES (CFR_ERR_UNSUPPORTED above); num_q_heads at most 256.
+ *  q_lens      device int32 [batch], 0 <= q_lens[b] <= num_queries, or NULL: num_queries
+ *              each.  out and lse rows at or past q_lens[b] are left as they were.
+ *  tree_mask   device uint64 [batch][num_queries], or NULL: draft i sees drafts 0 .. i.
+ *              Bits at or past q_lens[b] are ignored.  A row that sees no token at
+ *              all gets out = 0 and lse = -inf.
+ *  depths      device int32 [batch][num_queries] or NULL: depths i (a chain); read
+ *              only with alibi_slopes.
+ *  head_map    host, as for cfr_paged_decode.
+ *  logit_cap   0 (none) or > 0, finite.
+ *  out         device [batch][num_queries][num_q_heads][head_dim], F32 or BF16 (out_fmt),
+ *              16-byte aligned, written; lse device float [batch][num_queries][num_q_heads]
+ *              or NULL.
+ *  workspace   device, >= cfr_paged_decode_tree_workspace_size(...) bytes, 256-byte
+ *              aligned; as for cfr_paged_decode.
+ * Everything else (pools, page table, formats, softmax_scale, err_word) as for
+ * cfr_paged_decode.  A sequence with q_lens[b] outside [0, num_queries] (taken as num_queries), or with
+ * n_b < q_lens[b], n_b < 1 or n_b > max_pages * page_tokens and drafts, gets out = 0 and
+ * lse = -inf in its drafts' rows and sets CFR_DEVERR_SEQ_LEN.  A drafted token's non-finite
+ * K or V reaches only the rows that see it.
+ */
+cfr_status cfr_paged_decode_tree(const void *q, int32_t q_fmt, const cfr_kv_pool *kv,
+                                 const int32_t *page_table, int32_t max_pages,
+                                 const int32_t *seq_lens, int32_t batch,
+                                 const uint8_t *page_fmt, int32_t uniform_fmt,
+                                 int32_t num_q_heads, int32_t num_queries,
+                                 const int32_t *q_lens, const uint64_t *tree_mask,
+                                 const int32_t *depths, const int32_t *head_map,
+                                 const float *alibi_slopes, float softmax_scale,
+                                 float logit_cap, void *out, int32_t out_fmt, float *lse,
+                                 void *workspace, size_t workspace_bytes, uint32_t *err_word,
+                                 void *stream);
+
 /* Static description of a status code. */
 const char *cfr_status_str(cfr_status status);
 

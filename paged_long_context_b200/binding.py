@@ -30,7 +30,9 @@ EXPORTS = ["cfr_paged_decode_workspace_size", "cfr_paged_decode", "cfr_paged_dec
            "cfr_merge_partials",
            "cfr_schedule_splits", "cfr_gather_pages", "cfr_paged_decode_path", "cfr_status_str",
            "cfr_paged_decode_static_workspace", "cfr_demote_pages", "cfr_append_kv",
-           "cfr_paged_decode_sink_window", "cfr_paged_decode_multi", "cfr_wait_probe"]
+           "cfr_paged_decode_sink_window", "cfr_paged_decode_multi", "cfr_wait_probe",
+           "cfr_qk_norm_rope_append", "cfr_write_kv", "cfr_read_kv",
+           "cfr_paged_decode_tree_workspace_size", "cfr_paged_decode_tree"]
 FMT_COUNT = 5
 
 
@@ -109,6 +111,22 @@ def lib():
         L.cfr_append_kv.restype = ctypes.c_int
         L.cfr_append_kv.argtypes = [ctypes.POINTER(KvPool), _VP, _I32, _VP, _I32, _VP, _I32,
                                     _VP, _VP, _I32, _VP, _VP]
+        L.cfr_qk_norm_rope_append.restype = ctypes.c_int
+        L.cfr_qk_norm_rope_append.argtypes = [ctypes.POINTER(KvPool), _VP, _I32, _VP, _I32, _I32,
+                                              _VP, _I64, _VP, _I64, _VP, _I64, _I32, _I32, _I32,
+                                              _VP, _VP, _F32, _VP, _VP, _I32, _I32, _VP, _VP, _VP,
+                                              _VP, _VP]
+        L.cfr_write_kv.restype = ctypes.c_int
+        L.cfr_write_kv.argtypes = [ctypes.POINTER(KvPool), _VP, _I32, _VP, _I32, _I32, _VP, _VP,
+                                   _VP, _I64, _VP, _I64, _I32, _I32, _VP, _VP]
+        L.cfr_read_kv.restype = ctypes.c_int
+        L.cfr_read_kv.argtypes = L.cfr_write_kv.argtypes
+        L.cfr_paged_decode_tree_workspace_size.restype = _SZ
+        L.cfr_paged_decode_tree_workspace_size.argtypes = [_I32] * 5
+        L.cfr_paged_decode_tree.restype = ctypes.c_int
+        L.cfr_paged_decode_tree.argtypes = [_VP, _I32, ctypes.POINTER(KvPool), _VP, _I32, _VP, _I32,
+                                            _VP, _I32, _I32, _I32, _VP, _VP, _VP, _VP, _VP, _F32,
+                                            _F32, _VP, _I32, _VP, _VP, _SZ, _VP, _VP]
         L.cfr_wait_probe.restype = ctypes.c_int
         L.cfr_wait_probe.argtypes = [_I64, _I32, _VP, _VP, _VP]
         L.cfr_status_str.restype = ctypes.c_char_p
@@ -298,3 +316,138 @@ def append_kv(pool: KvPool, page_table, page_fmt, uniform_fmt: int, positions, k
                                    _p(page_fmt), uniform_fmt, _p(positions),
                                    int(positions.numel()), _p(k_new), _p(v_new), new_fmt, _p(err),
                                    _stream(stream)))
+
+
+def _want(name: str, t, dtypes, shape=None, strided_tokens=False, none_ok=False):
+    """Checks what the C ABI cannot see of a tensor argument: its type, shape, layout and
+    device.  strided_tokens: rows may be any distance apart, each row is contiguous."""
+    if t is None:
+        if none_ok:
+            return
+        raise ValueError(f"{name}: a tensor is required")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: {t.dtype} where {' or '.join(map(str, dtypes))} is wanted")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)} where {tuple(shape)} is wanted")
+    if strided_tokens:
+        if t.dim() != 3 or (t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]))):
+            raise ValueError(f"{name}: each token's [heads][head_dim] values must be contiguous")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, while device {torch.cuda.current_device()} is current")
+
+
+_INT32 = (torch.int32,)
+_HOT = (torch.float32, torch.bfloat16)
+
+
+def _fmt_of(t) -> int:
+    return synth.F32 if t.dtype == torch.float32 else synth.BF16
+
+
+def _token_stride(t) -> int:
+    """Values from one token's row to the next (a single row's stride is free: its own size)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _want_table(page_table, page_fmt):
+    _want("page_table", page_table, _INT32)
+    if page_table.dim() != 2:
+        raise ValueError("page_table: [batch][max_pages] is wanted")
+    _want("page_fmt", page_fmt, (torch.uint8,), page_table.shape, none_ok=True)
+
+
+def qk_norm_rope_append(pool: KvPool, q, k, v, rope_positions, inv_freq, q_out, page_table, page_fmt,
+                        uniform_fmt: int, seq_ids, token_ids, q_weight=None, k_weight=None,
+                        eps: float = 1e-6, interleaved: bool = False, err=None, stream=None) -> int:
+    """cfr_qk_norm_rope_append: norm and rotate a step's queries and keys, and write its K and V
+    into F32 / BF16 pages; q, k, v are [tokens][heads][head_dim] (views of a packed projection are
+    fine); returns the status."""
+    n, d = q.shape[0], pool.head_dim
+    _want_table(page_table, page_fmt)
+    _want("q", q, _HOT, (n, q.shape[1], d), strided_tokens=True)
+    for name, t in (("k", k), ("v", v)):
+        _want(name, t, (q.dtype,), (n, pool.num_kv_heads, d), strided_tokens=True)
+    _want("q_out", q_out, (q.dtype,), q.shape)
+    for name, t in (("seq_ids", seq_ids), ("token_ids", token_ids)):
+        _want(name, t, _INT32, (n,))
+    _want("rope_positions", rope_positions, _INT32, (n,), none_ok=inv_freq is None)
+    _want("inv_freq", inv_freq, (torch.float64,), none_ok=True)
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        _want(name, t, (torch.float32,), (d,), none_ok=True)
+    _want("err", err, _INT32, none_ok=True)
+    rot = 0 if inv_freq is None else 2 * int(inv_freq.numel())
+    return int(lib().cfr_qk_norm_rope_append(
+        ctypes.byref(pool), _p(page_table), int(page_table.shape[1]), _p(page_fmt), uniform_fmt,
+        int(page_table.shape[0]), _p(q), _token_stride(q), _p(k), _token_stride(k), _p(v),
+        _token_stride(v), _fmt_of(q), n, int(q.shape[1]), _p(q_weight), _p(k_weight), float(eps),
+        _p(rope_positions), _p(inv_freq), rot, 1 if interleaved else 0, _p(q_out), _p(seq_ids),
+        _p(token_ids), _p(err), _stream(stream)))
+
+
+def _chunk_args(pool, page_table, page_fmt, uniform_fmt, row_offsets, starts, a, b, names, err):
+    batch = int(page_table.shape[0])
+    _want_table(page_table, page_fmt)
+    _want("row_offsets", row_offsets, _INT32, (batch + 1,))
+    _want("starts", starts, _INT32, (batch,))
+    _want(names[0], a, _HOT, (a.shape[0], pool.num_kv_heads, pool.head_dim), strided_tokens=True)
+    _want(names[1], b, (a.dtype,), a.shape, strided_tokens=True)
+    _want("err", err, _INT32, none_ok=True)
+    return (ctypes.byref(pool), _p(page_table), int(page_table.shape[1]), _p(page_fmt), uniform_fmt,
+            batch, _p(row_offsets), _p(starts), _p(a), _token_stride(a), _p(b), _token_stride(b),
+            _fmt_of(a), int(a.shape[0]), _p(err))
+
+
+def write_kv(pool: KvPool, page_table, page_fmt, uniform_fmt: int, row_offsets, starts, k_new, v_new,
+             err=None, stream=None) -> int:
+    """cfr_write_kv: store a ragged chunk of new tokens into pages of any format, quantising as it
+    writes; k_new, v_new are [rows][kv heads][head_dim]; returns the status."""
+    args = _chunk_args(pool, page_table, page_fmt, uniform_fmt, row_offsets, starts, k_new, v_new,
+                       ("k_new", "v_new"), err)
+    return int(lib().cfr_write_kv(*args, _stream(stream)))
+
+
+def read_kv(pool: KvPool, page_table, page_fmt, uniform_fmt: int, row_offsets, starts, k_out, v_out,
+            err=None, stream=None) -> int:
+    """cfr_read_kv: cached tokens back as dense fp32 or bf16 rows; returns the status."""
+    args = _chunk_args(pool, page_table, page_fmt, uniform_fmt, row_offsets, starts, k_out, v_out,
+                       ("k_out", "v_out"), err)
+    return int(lib().cfr_read_kv(*args, _stream(stream)))
+
+
+def tree_workspace_size(batch, num_queries, num_q_heads, num_kv_heads, head_dim) -> int:
+    return int(lib().cfr_paged_decode_tree_workspace_size(batch, num_queries, num_q_heads,
+                                                          num_kv_heads, head_dim))
+
+
+def paged_decode_tree(pool: KvPool, q, page_table, seq_lens, out, lse, workspace, page_fmt=None,
+                      uniform_fmt: int = synth.BF16, q_lens=None, tree_mask=None, depths=None,
+                      head_map=None, alibi_slopes=None, softmax_scale: float = 0.0,
+                      logit_cap: float = 0.0, err=None, stream=None) -> int:
+    """cfr_paged_decode_tree: attention of drafted tokens (q is [batch][queries][heads][head_dim])
+    over the cache, under a tree mask of int64 bit rows [batch][queries]; returns the status.
+    head_map is a host int32 tensor."""
+    _want("q", q, _HOT)
+    if q.dim() != 4 or q.shape[3] != pool.head_dim:
+        raise ValueError("q: [batch][queries][heads][head_dim] is wanted")
+    batch, nq, hq, d = q.shape
+    _want_table(page_table, page_fmt)
+    _want("page_table", page_table, _INT32, (batch, page_table.shape[1]))
+    _want("seq_lens", seq_lens, _INT32, (batch,))
+    _want("out", out, _HOT, q.shape)
+    _want("lse", lse, (torch.float32,), (batch, nq, hq), none_ok=True)
+    _want("workspace", workspace, (torch.uint8,))
+    _want("q_lens", q_lens, _INT32, (batch,), none_ok=True)
+    _want("tree_mask", tree_mask, (torch.int64, torch.uint64), (batch, nq), none_ok=True)
+    _want("depths", depths, _INT32, (batch, nq), none_ok=True)
+    _want("alibi_slopes", alibi_slopes, (torch.float32,), (hq,), none_ok=True)
+    _want("err", err, _INT32, none_ok=True)
+    _want("head_map", head_map, _INT32, (hq,), none_ok=True)
+    if head_map is not None and head_map.is_cuda:
+        raise ValueError("head_map: a host tensor is wanted")
+    return int(lib().cfr_paged_decode_tree(
+        _p(q), _fmt_of(q), ctypes.byref(pool), _p(page_table), int(page_table.shape[1]), _p(seq_lens),
+        batch, _p(page_fmt), uniform_fmt, hq, nq, _p(q_lens), _p(tree_mask), _p(depths), _p(head_map),
+        _p(alibi_slopes), float(softmax_scale), float(logit_cap), _p(out), _fmt_of(out), _p(lse),
+        _p(workspace), int(workspace.numel()), _p(err), _stream(stream)))
