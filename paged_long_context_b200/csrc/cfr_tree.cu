@@ -19,6 +19,11 @@
 #include "cfr_tree.cuh"
 
 namespace cfr {
+
+bool tree_tc_supported(const TreeParams &p);
+int tree_tc_rows(int most_rows);
+cudaError_t launch_tree_tc(const TreeParams &p, int rb, cudaStream_t s);
+
 namespace {
 
 constexpr int kGenTT = 64, kGenRB = 32, kGenThreads = 256;
@@ -327,17 +332,29 @@ TreeWs tree_ws(int slots, int rb, int d) {
   return w;
 }
 
+// Scratch of the larger of the two kernels' cuts: the general one (two CTAs an SM,
+// 32 rows) or the tensor-core one (one CTA an SM, 128 or 256 rows).  `rows`: the
+// most rows that a kv head can have.
+TreeWs tree_scratch(int sms, int rows, int d) {
+  const TreeWs a = tree_ws(2 * general_grid(sms), kGenRB, d), b = tree_ws(2 * sms, tree_tc_rows(rows), d);
+  return a.total > b.total ? a : b;
+}
+
+template <int TT, int RB>
+cudaError_t launch_tree_merge(const TreeParams &p, cudaStream_t s) {
+  const dim3 grid(p.grid - 1, RB / 8);
+  return p.D == 128 ? launch_after_previous(tree_merge_kernel<TT, RB, 128>, grid, dim3(256), 0, s, p)
+                    : launch_after_previous(tree_merge_kernel<TT, RB, 64>, grid, dim3(256), 0, s, p);
+}
+
 template <int D>
-cudaError_t launch_general(TreeParams &p, int sms, cudaStream_t s) {
-  p.grid = general_grid(sms);
+cudaError_t launch_general(const TreeParams &p, cudaStream_t s) {
   const size_t smem = sizeof(GenSmem<D>);
   cudaError_t e = cudaFuncSetAttribute(tree_general_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   tree_general_kernel<D><<<p.grid, kGenThreads, smem, s>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  return launch_after_previous(tree_merge_kernel<kGenTT, kGenRB, D>, dim3(p.grid - 1, kGenRB / 8), dim3(256), 0, s, p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -356,7 +373,7 @@ size_t cfr_paged_decode_tree_workspace_size(int32_t batch, int32_t num_queries,
     return 0;
   const int sms = tree_sms();
   if (sms <= 0) return 0;
-  return tree_ws(2 * general_grid(sms), kGenRB, head_dim).total;
+  return tree_scratch(sms, num_queries * num_q_heads, head_dim).total;
 }
 
 cfr_status cfr_paged_decode_tree(const void *q, int32_t q_fmt, const cfr_kv_pool *kv,
@@ -401,12 +418,9 @@ cfr_status cfr_paged_decode_tree(const void *q, int32_t q_fmt, const cfr_kv_pool
   }
   const int sms = tree_sms();
   if (sms <= 0) return CFR_ERR_CUDA;
-  const TreeWs w = tree_ws(2 * general_grid(sms), kGenRB, kv->head_dim);
-  if (!workspace || !ptr_aligned(workspace, 256) || workspace_bytes < w.total) return CFR_ERR_WORKSPACE;
-  uint8_t *ws = static_cast<uint8_t *>(workspace);
-  p.part_m = reinterpret_cast<float *>(ws + w.part_m);
-  p.part_l = reinterpret_cast<float *>(ws + w.part_l);
-  p.part_acc = reinterpret_cast<float *>(ws + w.part_acc);
+  if (!workspace || !ptr_aligned(workspace, 256) ||
+      workspace_bytes < tree_scratch(sms, num_queries * num_q_heads, kv->head_dim).total)
+    return CFR_ERR_WORKSPACE;
   for (int f = 0; f < kFmtCount; ++f) {
     p.k_pool[f] = c.k_pool[f];
     p.v_pool[f] = c.v_pool[f];
@@ -437,7 +451,21 @@ cfr_status cfr_paged_decode_tree(const void *q, int32_t q_fmt, const cfr_kv_pool
   p.sigma = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf(static_cast<float>(kv->head_dim));
   p.cap = logit_cap;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = kv->head_dim == 128 ? launch_general<128>(p, sms, s) : launch_general<64>(p, sms, s);
+  int most = 0;
+  for (int g = 0; g < kv->num_kv_heads; ++g) most = count[g] > most ? count[g] : most;
+  const bool tc = tree_tc_supported(p);
+  const int rb = tc ? tree_tc_rows(most * num_queries) : kGenRB;
+  p.grid = tc ? sms : general_grid(sms);
+  const TreeWs w = tree_ws(2 * p.grid, rb, p.D);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  p.part_m = reinterpret_cast<float *>(ws + w.part_m);
+  p.part_l = reinterpret_cast<float *>(ws + w.part_l);
+  p.part_acc = reinterpret_cast<float *>(ws + w.part_acc);
+  cudaError_t e = tc ? launch_tree_tc(p, rb, s) : p.D == 128 ? launch_general<128>(p, s) : launch_general<64>(p, s);
+  if (e != cudaSuccess) return CFR_ERR_CUDA;
+  e = !tc ? launch_tree_merge<kGenTT, kGenRB>(p, s)
+      : rb == 128 ? launch_tree_merge<128, 128>(p, s)
+                  : launch_tree_merge<128, 256>(p, s);
   return e == cudaSuccess ? CFR_OK : CFR_ERR_CUDA;
 }
 

@@ -1,0 +1,1083 @@
+// cfr_tree_tc.cu -- attention of a tree of drafted tokens on the 5th-generation
+// tensor cores (tcgen05, accumulators and probabilities in TMEM) for bf16
+// queries over bf16, FP8, int8 and int4 pages.
+//
+// A work item's query rows (drafts x query heads of one kv head) are the M
+// dimension, 128 rows a tile; one 128-token tile of the cache is
+//   S[128 rows x 128 tokens] = Q . K^T     (A, B from shared memory, K-major)
+//   O[128 rows x D] += P . V               (A = P from TMEM, B = V, MN-major)
+// Rows as M (the one-token decode has tokens as M) because a tree brings tens to
+// hundreds of rows to a kv head: a thread then owns a whole row of S, so the
+// maximum, the sum and the mask of a row need no exchange between threads, and P goes back
+// to TMEM without touching shared memory.
+//
+// Online softmax with a lazy reference: a row's exponentials are taken against m_ref,
+// which is moved (O and l rescaled) only when the row's maximum has passed it
+// by more than 8 (a factor of 256, which bf16 and fp32 hold without loss), so
+// O stays in TMEM for nearly every tile.  P is rounded to bf16, the type of V as
+// an MMA operand; l sums the unrounded values in fp32.
+//
+// Quantised pages: codes are expanded to bf16 in shared memory (int8, int4 and
+// E4M3 codes are all exact there); the K scale multiplies the fp32 score of its
+// token, the V scale its probability.
+//
+// NM = 1 (up to 128 rows of a kv head): S is double-buffered, the scores of the
+// next tile are computed under the softmax of this one.  NM = 2 (more rows): two
+// row tiles of one K/V tile, each with a softmax warpgroup, take turns on the
+// tensor cores; K and V are read once for 256 rows.
+//
+// Warps: warpgroup 0 = K producer (warp 0), MMA issuer (1), V producer (2), V
+// repair (3); then NM softmax warpgroups; with quantised pools one more that
+// expands codes.  K and V tiles go through one ring of slots, K of tile t in
+// place 2t, V in place 2t + 1.
+//  - bf16 rows are brought by TMA boxes straight into the 128-byte-swizzled
+//    operand layout, quantised rows by bulk copies into their own rows' place
+//    and expanded there.
+//  - A V tile that reaches the drafts or the sequence's end is repaired before
+//    the MMA sees it: rows that hold no token become zeros, and non-finite
+//    values of drafts are taken out (they would reach, as 0 * NaN, rows that do
+//    not see the draft) and added back at the end to the rows that see it.
+//
+// Bound by HBM up to about 128 rows (K and V once); beyond that the 128 x 128
+// exponentials of a tile (16 a clock and SM) and the MMAs come near it.
+#include <cuda_bf16.h>
+
+#include <cstring>
+
+#include "cfr_cells.cuh"
+#include "cfr_tc.cuh"
+#include "cfr_tmap.cuh"
+#include "cfr_tree.cuh"
+
+namespace cfr {
+namespace {
+
+constexpr int TT = 128;        // tokens of a tile
+constexpr int META_RING = 8;   // tiles whose description is kept (see tt_producer)
+constexpr int MAX_PIECES = 17; // pages (of 8 tokens or more) that a tile can touch
+constexpr float RESCALE_STEP = 8.f;
+
+template <int D, int NM, bool QUANT>
+struct TtCfg {
+  static constexpr int RB = 128 * NM;
+  static constexpr int ROW_TILE = 128 * D * 2;   // bytes of 128 bf16 rows: a Q tile, a K or V slot
+  // slots that fit beside the queries (227 KB in all); heads of 64 have slots of half the size
+  static constexpr int NS = (D == 128 ? 1 : 2) * (QUANT ? (NM == 1 ? 5 : 4) : (NM == 1 ? 6 : D == 128 ? 5 : 6));
+  static constexpr int WGS = 1 + NM + (QUANT ? 1 : 0);
+  static constexpr int THREADS = 128 * WGS;
+  static constexpr int SOFTMAX_T0 = 128;
+  static constexpr int LOADER_T0 = 128 * (1 + NM);
+  // registers: what the block is launched with (65536 over its threads, a multiple of 8, at
+  // most 255), and the split over its warpgroups
+  static constexpr int REGS_LAUNCH = NM == 1 && !QUANT ? 255 : 65536 / THREADS / 8 * 8;
+  static constexpr bool SPLIT = !(NM == 1 && !QUANT);
+  static constexpr int REGS_IO = QUANT ? (NM == 1 ? 96 : 72) : 88;
+  static constexpr int REGS_SOFTMAX = QUANT ? (NM == 1 ? 232 : 176) : 208;
+  static constexpr int REGS_LOADER = QUANT ? (NM == 1 ? 176 : 88) : 0;
+  static_assert(!SPLIT || REGS_IO + NM * REGS_SOFTMAX + REGS_LOADER <= WGS * REGS_LAUNCH,
+                "the split must fit the registers the block was launched with");
+  static constexpr int TMEM_COLS = 512;
+  static constexpr int S_COL = 0, O_COL = 256;   // S (two of 128 columns), O (NM of 128)
+};
+
+struct TtMeta {
+  uint32_t valid[4];          // tokens of the tile that take part
+  int tin0, scaled;           // row of the first token in its page; any quantised page
+  uint8_t fmt[MAX_PIECES + 3];
+  float ks[MAX_PIECES], vs[MAX_PIECES];
+};
+
+template <int NS, bool QUANT>
+struct TtSmem {
+  uint64_t slot_full[NS], slot_empty[NS], raw_full[NS];
+  uint64_t s_full[2], p_full[2], pv_done[2], q_full[2], o_free[2];
+  uint64_t meta_full[META_RING], drain;
+  uint32_t tmem_base;
+  int flag[NS];
+  unsigned long long nonfinite[META_RING];  // of item k & 7: drafts whose V was repaired
+  uint32_t v_valid[META_RING][4];
+  int direct[NS];                           // the slot's tile needs no expansion or repair
+  TreeScratch scratch;
+  TtMeta meta[QUANT ? META_RING : 1];
+  uint32_t valid[META_RING][4];
+  alignas(16) float2 tok[QUANT ? META_RING : 1][QUANT ? TT : 2];  // K and V scale of each token
+};
+
+template <int N>
+__device__ __forceinline__ void tt_setmaxnreg(bool inc) {
+  if (inc)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// D[128 x N] (+)= A (TMEM) . B (shared memory)
+__device__ __forceinline__ void tt_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tt_ld32(uint32_t taddr, float *v) {
+  uint32_t *r = reinterpret_cast<uint32_t *>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tt_st32(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tt_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+      " mul.rn.f32x2 w, x, y;\n mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+      " add.rn.f32x2 w, x, y;\n mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// int8 codes 2i, 2i + 1 of a word -> bf16 pair: 128 + (c & 127) less 128, or less 256 where the sign bit
+// is set (both terms share the exponent trick: 0x4300 is 128, 0x4380 is 256)
+__device__ __forceinline__ uint32_t bf2_sub(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t i8x2_to_bf2(uint32_t w, uint32_t sel) {
+  const uint32_t t = prmt(w, 0u, sel);  // (byte, 0, byte, 0)
+  return bf2_sub((t & 0x007F007Fu) | 0x43004300u, (t & 0x00800080u) | 0x43004300u);
+}
+// int4 codes of byte i of a word whose nibbles were xored with 8: lo, hi = its low
+// and high nibbles, one a byte -> bf16 pair (128 + nibble less 136)
+__device__ __forceinline__ uint32_t i4x2_to_bf2(uint32_t lo, uint32_t hi, uint32_t sel) {
+  return bf2_sub((prmt(lo, hi, sel) & 0x000F000Fu) | 0x43004300u, 0x43084308u);
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_bf2(uint32_t w, int i) {
+  const uint32_t h = e4m3x2_to_h2(w, i);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+  return pack_bf16(f.x, f.y);
+}
+
+// 16 bytes of codes as bf16 words: 8 words (int8, E4M3) or 16 (int4)
+template <int N>
+__device__ __forceinline__ void expand16(int fmt, uint4 v, uint32_t (&o)[N]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (N == 16) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t x = w[q] ^ 0x88888888u;
+      const uint32_t lo = x & 0x0F0F0F0Fu, hi = (x >> 4) & 0x0F0F0F0Fu;
+      o[4 * q + 0] = i4x2_to_bf2(lo, hi, 0x4400u);
+      o[4 * q + 1] = i4x2_to_bf2(lo, hi, 0x5511u);
+      o[4 * q + 2] = i4x2_to_bf2(lo, hi, 0x6622u);
+      o[4 * q + 3] = i4x2_to_bf2(lo, hi, 0x7733u);
+    }
+  } else if (fmt == CFR_FMT_I8) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      o[2 * q] = i8x2_to_bf2(w[q], 0x4140u);
+      o[2 * q + 1] = i8x2_to_bf2(w[q], 0x4342u);
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      o[2 * q] = e4m3x2_to_bf2(w[q], 0);
+      o[2 * q + 1] = e4m3x2_to_bf2(w[q], 1);
+    }
+  }
+}
+
+// clears the non-finite bf16 values of a word; true when there was one
+__device__ __forceinline__ bool repair_word(uint32_t &w) {
+  bool bad = false;
+  if ((w & 0x7F80u) == 0x7F80u) {
+    w &= 0xFFFF0000u;
+    bad = true;
+  }
+  if ((w & 0x7F800000u) == 0x7F800000u) {
+    w &= 0x0000FFFFu;
+    bad = true;
+  }
+  return bad;
+}
+__device__ __forceinline__ bool repair16(uint4 &v) {
+  const bool a = repair_word(v.x), b = repair_word(v.y), c = repair_word(v.z), d = repair_word(v.w);
+  return a || b || c || d;
+}
+
+template <int D, int NM, bool QUANT>
+struct TtCtx {
+  using Cfg = TtCfg<D, NM, QUANT>;
+  using Smem = TtSmem<Cfg::NS, QUANT>;
+  const TreeParams &p;
+  const CUtensorMap &kmap, &vmap;
+  Smem &S;
+  uint8_t *q, *slots;
+  int box;  // rows of a TMA box: the largest power of two that divides P, at most 128
+  __device__ __forceinline__ uint8_t *slot(int s) const { return slots + s * Cfg::ROW_TILE; }
+};
+
+// place in the ring of slots
+template <int NS>
+struct Ring {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void step(int n) {
+    s += n;
+    if (s >= NS) {
+      s -= NS;
+      ph ^= 1u;
+    }
+  }
+};
+
+// ---- producers -----------------------------------------------------------------
+
+// One of the tile's pages, as lane `lane` of a producer sees it.
+struct Piece {
+  long long id;
+  int fmt;
+};
+
+__device__ __forceinline__ Piece tt_fetch(const TreeParams &p, const TreeItem &it, int t, int lane) {
+  Piece x{-1, 0};
+  const int j0 = t * TT, rows = min(TT, it.n - j0);
+  const int pg = j0 / p.P + lane;
+  if (t < it.t1 && rows > 0 && static_cast<long long>(pg) * p.P < j0 + rows) {
+    const long long cell = static_cast<long long>(it.b) * p.max_pages + pg;
+    x.id = p.page_table[cell];
+    x.fmt = p.page_fmt ? p.page_fmt[cell] : p.uniform_fmt;
+  }
+  return x;
+}
+
+// K (KV = 0) or V (KV = 1) of every tile, by one warp.  Page-table entries are
+// read two tiles ahead and scales one, so that neither is waited for.
+//
+// The description of tile t is kept in place t & 7.  It may be overwritten by
+// tile t + 8 because K's slot of tile t + 8 is free only when the scores of a
+// tile t + 2 or later were issued (a ring has at most 12 slots, 6 tiles), which is after the softmax of
+// tile t handed over its P.
+template <int D, int NM, bool QUANT, int KV>
+__device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_out) {
+  using Cfg = TtCfg<D, NM, QUANT>;
+  const TreeParams &p = c.p;
+  const int lane = threadIdx.x & 31;
+  Ring<Cfg::NS> r;
+  r.step(KV);
+  uint32_t raw_mask = 0, used = 0;   // slots filled through raw_full; slots filled at all
+  uint32_t phase_of = 0;             // the phase each was filled in
+  uint32_t tile = 0;
+  TreeItem it;
+  while (!*timed_out && tree_next<TT, Cfg::RB>(p, cur, it)) {
+    if (KV == 0 && lane == 0 && it.bad) set_err(p.err, CFR_DEVERR_SEQ_LEN);
+    const int pre = it.n - it.c;
+    Piece now = tt_fetch(p, it, it.t0, lane), next = tt_fetch(p, it, it.t0 + 1, lane);
+    for (int t = it.t0; t < it.t1; ++t, ++tile) {
+      const Piece after = tt_fetch(p, it, t + 2, lane);
+      const int j0 = t * TT, rows = max(0, min(TT, it.n - j0));
+      const int tin0 = j0 % p.P;
+      const int npiece = rows > 0 ? (tin0 + rows + p.P - 1) / p.P : 0;
+      bool ok = false;
+      int fmt = now.fmt;
+      if (lane < npiece) {
+        const bool known = fmt < kFmtCount;
+        const bool pool = known && p.k_pool[known ? fmt : 0];
+        ok = pool && now.id >= 0 && now.id < p.pool_pages[known ? fmt : 0];
+        if (!ok && KV == 0)
+          set_err(p.err, !known ? CFR_DEVERR_PAGE_FMT : !pool ? CFR_DEVERR_POOL : CFR_DEVERR_PAGE_ID);
+      }
+      const uint32_t okb = __ballot_sync(0xffffffffu, ok);
+      const bool quant = QUANT && ok && is_quantised(fmt);
+      const bool any_quant = QUANT && __any_sync(0xffffffffu, quant);
+      float2 sc = make_float2(1.f, 1.f);
+      if (QUANT && KV == 0 && quant)
+        sc = *reinterpret_cast<const float2 *>(p.scales[fmt] + (now.id * p.Hkv + it.g) * 2);
+      // tokens of valid pages, 32 a ballot
+      uint32_t valid[4];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const int row = 32 * w + lane;
+        valid[w] = __ballot_sync(0xffffffffu, row < rows && ((okb >> ((tin0 + row) / p.P)) & 1u));
+      }
+      // this lane's page: tile rows [a, z)
+      const int a = lane == 0 ? 0 : min(rows, lane * p.P - tin0);
+      const int z = min(rows, (lane + 1) * p.P - tin0);
+      const int boxes = (z - a + c.box - 1) / c.box;
+      const uint32_t mine = !ok ? 0u : quant ? static_cast<uint32_t>((z - a) * row_bytes(fmt, D))
+                                             : static_cast<uint32_t>(boxes * c.box * D * 2);
+      const uint32_t bytes = __reduce_add_sync(0xffffffffu, mine);
+      const bool full = (valid[0] & valid[1] & valid[2] & valid[3]) == 0xFFFFFFFFu;
+      const bool direct = !any_quant && (KV == 0 || (full && j0 + TT <= pre));
+      int go = 1;
+      if (lane == 0) go = mbar_wait(&c.S.slot_empty[r.s], r.ph ^ 1u, p.err, timed_out) ? 1 : 0;
+      if (!__shfl_sync(0xffffffffu, go, 0)) {
+        *timed_out = true;
+        break;
+      }
+      uint64_t *done = direct ? &c.S.slot_full[r.s] : &c.S.raw_full[r.s];
+      const int mi = tile & (META_RING - 1);
+      if (KV == 0 && QUANT && lane < npiece) {
+        c.S.meta[mi].fmt[lane] = ok ? static_cast<uint8_t>(fmt) : 255;
+        c.S.meta[mi].ks[lane] = sc.x;
+        c.S.meta[mi].vs[lane] = sc.y;
+      }
+      if (lane < 4) (KV == 0 ? c.S.valid : c.S.v_valid)[mi][lane] = lane == 0 ? valid[0] : lane == 1 ? valid[1] : lane == 2 ? valid[2] : valid[3];
+      if (lane == 0) {
+        if (QUANT && KV == 0) {
+          c.S.meta[mi].tin0 = tin0;
+          c.S.meta[mi].scaled = any_quant;
+        }
+        c.S.direct[r.s] = direct;
+      }
+      __syncwarp();
+      if (lane == 0) {
+        if (KV == 0 && !QUANT) mbar_arrive(&c.S.meta_full[mi]);
+        // a tile that needs nothing is shown to the expanding or repairing warps all the same, in order:
+        // a slot holds K and V in turn, and its barriers have one phase for each
+        if (direct) mbar_arrive(&c.S.raw_full[r.s]);
+        mbar_arrive_expect_tx(done, bytes);
+      }
+      __syncwarp();
+      used |= 1u << r.s;
+      raw_mask = direct ? raw_mask & ~(1u << r.s) : raw_mask | (1u << r.s);
+      phase_of = r.ph ? phase_of | (1u << r.s) : phase_of & ~(1u << r.s);
+      if (ok) {
+        uint8_t *dst = c.slot(r.s) + a * 128;
+        const int in_page = lane == 0 ? tin0 : 0;
+        if (quant) {
+          const int rb = row_bytes(fmt, D);
+          const uint8_t *pool = KV ? p.v_pool[fmt] : p.k_pool[fmt];
+          bulk_g2s(dst, pool + ((now.id * p.Hkv + it.g) * p.P + in_page) * rb, mine, done);
+        } else {
+          const int y = static_cast<int>((now.id * p.Hkv + it.g) * p.P + in_page);
+          for (int x = 0; x < boxes; ++x)
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half)
+              tma_load_2d(dst + half * (TT * 128) + x * c.box * 128, KV ? &c.vmap : &c.kmap, half * 64,
+                          y + x * c.box, done);
+        }
+      }
+      now = next;
+      next = after;
+      r.step(2);
+    }
+  }
+  if (*timed_out && lane == 0) {
+    // leave no copy in flight
+    for (int s = 0; s < Cfg::NS; ++s) {
+      bool late = false;
+      if ((used >> s) & 1u)
+        mbar_wait((raw_mask >> s) & 1u ? &c.S.raw_full[s] : &c.S.slot_full[s], (phase_of >> s) & 1u, p.err, &late);
+    }
+  }
+}
+
+// ---- repair and expansion -------------------------------------------------------
+
+// Row i of a V tile before the MMA: zeros where it holds no token; non-finite
+// values of a draft taken out and the draft noted.
+template <int D>
+__device__ __forceinline__ void tt_repair_row(uint8_t *v, int i, bool valid, int draft, unsigned long long *noted) {
+  bool bad = false;
+#pragma unroll 4
+  for (int ch = 0; ch < D / 8; ++ch) {
+    uint4 *at = reinterpret_cast<uint4 *>(v + (ch >> 3) * (TT * 128) + sw128(i, ch & 7));
+    if (!valid) {
+      *at = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+      uint4 w = *at;
+      if (repair16(w)) {
+        *at = w;
+        bad = true;
+      }
+    }
+  }
+  if (bad) atomicOr(noted, 1ull << draft);
+}
+
+// V repair of caches of bf16 pages only, one warp.  It takes part in the release
+// of every slot, so that it is never a phase behind a slot's barrier.
+template <int D, int NM>
+__device__ void tt_repair(TtCtx<D, NM, false> &c, TreeCursor cur, bool *timed_out) {
+  using Cfg = TtCfg<D, NM, false>;
+  const TreeParams &p = c.p;
+  const int lane = threadIdx.x & 31;
+  Ring<Cfg::NS> r;
+  uint32_t tile = 0, k = 0;
+  TreeItem it;
+  for (; !*timed_out && tree_next<TT, Cfg::RB>(p, cur, it); ++k) {
+    const int pre = it.n - it.c;
+    if (lane == 0) c.S.nonfinite[k & (META_RING - 1)] = 0ull;
+    __syncwarp();
+    for (int t2 = 2 * it.t0; t2 < 2 * it.t1; ++t2) {
+      int go = 1;
+      if (lane == 0) go = mbar_wait(&c.S.raw_full[r.s], r.ph, p.err, timed_out) ? 1 : 0;
+      if (!__shfl_sync(0xffffffffu, go, 0)) {
+        *timed_out = true;
+        break;
+      }
+      (void)mbar_try_wait(&c.S.raw_full[r.s], r.ph);
+      const bool is_v = t2 & 1;
+      if (is_v && !c.S.direct[r.s]) {
+        const int j0 = (t2 >> 1) * TT;
+        for (int i = lane; i < TT; i += 32) {
+          const bool valid = (c.S.v_valid[tile & (META_RING - 1)][i >> 5] >> (i & 31)) & 1u;
+          if (!valid || j0 + i >= pre)
+            tt_repair_row<D>(c.slot(r.s), i, valid, j0 + i - pre, &c.S.nonfinite[k & (META_RING - 1)]);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c.S.slot_full[r.s]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c.S.slot_empty[r.s]);
+      if (is_v) ++tile;
+      r.step(1);
+    }
+  }
+}
+
+// Expansion (and V repair) of caches with quantised pages: thread i owns row i.
+// It takes part in the release of every slot, as the repair warp above does.
+template <int D, int NM>
+__device__ void tt_expand(TtCtx<D, NM, true> &c, TreeCursor cur, bool *timed_out) {
+  using Cfg = TtCfg<D, NM, true>;
+  const TreeParams &p = c.p;
+  const int i = threadIdx.x - Cfg::LOADER_T0;
+  constexpr int C8 = D / 16, C4 = D / 32;   // 16-byte pieces of an 8-bit and a 4-bit row
+  Ring<Cfg::NS> r;
+  uint32_t tile = 0, k = 0;
+  TreeItem it;
+  for (; tree_next<TT, Cfg::RB>(p, cur, it); ++k) {
+    const int pre = it.n - it.c;
+    if (i == 0) c.S.nonfinite[k & (META_RING - 1)] = 0ull;
+    for (int t = it.t0; t < it.t1; ++t, ++tile) {
+      const int mi = tile & (META_RING - 1);
+      const TtMeta &m = c.S.meta[mi];
+      int fmt = 255, a = 0;
+      bool valid = false;
+      for (int kv = 0; kv < 2; ++kv) {
+        // one thread waits, the barrier hands on its outcome
+        if (i == 0) c.S.flag[r.s] = mbar_wait(&c.S.raw_full[r.s], r.ph, p.err, timed_out) ? 1 : 0;
+        named_sync(1, 128);
+        if (!c.S.flag[r.s]) {
+          *timed_out = true;
+          return;
+        }
+        (void)mbar_try_wait(&c.S.raw_full[r.s], r.ph);
+        const bool direct = c.S.direct[r.s];
+        if (kv == 0) {
+          valid = (c.S.valid[mi][i >> 5] >> (i & 31)) & 1u;
+          const int pc = (m.tin0 + i) / p.P;
+          fmt = valid ? m.fmt[pc] : 255;
+          a = pc == 0 ? 0 : pc * p.P - m.tin0;
+          c.S.tok[mi][i] = valid ? make_float2(m.ks[pc], m.vs[pc]) : make_float2(0.f, 0.f);
+        }
+        if (!direct) {
+          uint8_t *op = c.slot(r.s);
+          const bool eight = fmt == CFR_FMT_I8 || fmt == CFR_FMT_FP8, four = fmt == CFR_FMT_I4;
+          uint4 raw[C8];
+          // rows are read in an order that spreads a warp's lanes over the banks
+          if (eight) {
+            const uint8_t *src = op + a * 128 + (i - a) * D;
+#pragma unroll
+            for (int x = 0; x < C8; ++x) raw[x] = *reinterpret_cast<const uint4 *>(src + 16 * ((x + (D == 128 ? i : i >> 1)) & (C8 - 1)));
+          } else if (four) {
+            const uint8_t *src = op + a * 128 + (i - a) * (D / 2);
+#pragma unroll
+            for (int x = 0; x < C4; ++x) raw[x] = *reinterpret_cast<const uint4 *>(src + 16 * ((x + (D == 128 ? i >> 1 : i >> 2)) & (C4 - 1)));
+          }
+          named_sync(1, 128);  // every row is in registers before any is written
+          const int draft = t * TT + i - pre;
+          bool bad = false;
+          if (eight) {
+#pragma unroll
+            for (int x = 0; x < C8; ++x) {
+              const int ci = (x + (D == 128 ? i : i >> 1)) & (C8 - 1);
+              uint32_t o[8];
+              expand16<8>(fmt, raw[x], o);
+              uint4 u = make_uint4(o[0], o[1], o[2], o[3]), v = make_uint4(o[4], o[5], o[6], o[7]);
+              if (kv == 1 && fmt == CFR_FMT_FP8 && draft >= 0) bad = repair16(u) | repair16(v) | bad;
+              uint8_t *hb = op + (ci >> 2) * (TT * 128);
+              *reinterpret_cast<uint4 *>(hb + sw128(i, (2 * ci) & 7)) = u;
+              *reinterpret_cast<uint4 *>(hb + sw128(i, (2 * ci + 1) & 7)) = v;
+            }
+          } else if (four) {
+#pragma unroll
+            for (int x = 0; x < C4; ++x) {
+              const int ci = (x + (D == 128 ? i >> 1 : i >> 2)) & (C4 - 1);
+              uint32_t o[16];
+              expand16<16>(fmt, raw[x], o);
+              uint8_t *hb = op + (ci >> 1) * (TT * 128);
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                *reinterpret_cast<uint4 *>(hb + sw128(i, (4 * ci + y) & 7)) =
+                    make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+            }
+          } else if (kv == 1 && (!valid || draft >= 0)) {
+            tt_repair_row<D>(op, i, valid, draft, &c.S.nonfinite[k & (META_RING - 1)]);
+          }
+          if (bad) atomicOr(&c.S.nonfinite[k & (META_RING - 1)], 1ull << draft);
+          fence_async_smem();
+        }
+        named_sync(1, 128);
+        if (i == 0) {
+          if (!direct) mbar_arrive(&c.S.slot_full[r.s]);
+          if (kv == 0) mbar_arrive(&c.S.meta_full[mi]);
+          mbar_arrive(&c.S.slot_empty[r.s]);
+        }
+        r.step(1);
+      }
+    }
+  }
+}
+
+// ---- MMA issue ------------------------------------------------------------------
+
+template <int D, int NM, bool QUANT>
+__device__ void tt_issue(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_out) {
+  using Cfg = TtCfg<D, NM, QUANT>;
+  const TreeParams &p = c.p;
+  const uint32_t tmem = c.S.tmem_base;
+  const uint32_t qa = smem_u32(c.q), sa = smem_u32(c.slots);
+  constexpr uint32_t qk_desc = tc_idesc(1, 0, 0, TT), pv_desc = tc_idesc(1, 0, 1, D);
+  Ring<Cfg::NS> kr, vr;
+  vr.step(1);
+  uint32_t cnt[2] = {0, 0}, items[2] = {0, 0};   // tiles and items of each row tile so far
+  const auto sbuf = [&](int m, uint32_t n) { return NM == 1 ? static_cast<int>(n & 1) : m; };
+  const auto spar = [&](uint32_t n) { return NM == 1 ? (n >> 1) & 1u : n & 1u; };
+  const auto scores = [&](int m, uint32_t n) {   // S of row tile m's n-th tile, from the K slot
+    const uint32_t d = tmem + Cfg::S_COL + sbuf(m, n) * 128;
+    const uint32_t a = qa + m * Cfg::ROW_TILE, b = sa + kr.s * Cfg::ROW_TILE;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      const uint32_t off = (k >> 2) * (TT * 128) + (k & 3) * 32;
+      tc_mma(d, tc_sdesc(a + off, 16, 1024, 2), tc_sdesc(b + off, 16, 1024, 2), qk_desc, k > 0 ? 1u : 0u);
+    }
+    tc_commit(&c.S.s_full[sbuf(m, n)]);
+  };
+  TreeItem it;
+  while (!*timed_out && tree_next<TT, Cfg::RB>(p, cur, it)) {
+    const int ms = NM == 2 && it.rows > 128 ? 2 : 1;
+    const int T = it.t1 - it.t0;
+    if (!mbar_wait(&c.S.slot_full[kr.s], kr.ph, p.err, timed_out)) break;
+    for (int m = 0; m < ms; ++m)
+      if (!mbar_wait(&c.S.q_full[m], items[m] & 1u, p.err, timed_out)) break;
+    if (*timed_out) break;
+    tc_fence_after();
+    for (int m = 0; m < ms; ++m) scores(m, cnt[m]);
+    tc_commit(&c.S.slot_empty[kr.s]);
+    kr.step(2);
+    for (int t = 0; t < T; ++t) {
+      if (NM == 1 && t + 1 < T) {
+        if (!mbar_wait(&c.S.slot_full[kr.s], kr.ph, p.err, timed_out)) break;
+        tc_fence_after();
+        scores(0, cnt[0] + 1);
+        tc_commit(&c.S.slot_empty[kr.s]);
+        kr.step(2);
+      }
+      if (!mbar_wait(&c.S.slot_full[vr.s], vr.ph, p.err, timed_out)) break;
+      for (int m = 0; m < ms; ++m) {
+        const int sb = sbuf(m, cnt[m]);
+        if (t == 0 && !mbar_wait(&c.S.o_free[m], (items[m] & 1u) ^ 1u, p.err, timed_out)) break;
+        if (!mbar_wait(&c.S.p_full[sb], spar(cnt[m]), p.err, timed_out)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + Cfg::O_COL + m * 128, a = tmem + Cfg::S_COL + sb * 128;
+        const uint32_t b = sa + vr.s * Cfg::ROW_TILE;
+#pragma unroll
+        for (int k = 0; k < TT / 16; ++k)
+          tt_mma_ts(d, a + k * 8, tc_sdesc(b + k * 2048, TT * 128, 1024, 2), pv_desc, t > 0 || k > 0 ? 1u : 0u);
+        tc_commit(&c.S.pv_done[m]);
+        ++cnt[m];
+        if (NM == 2 && t + 1 < T) {
+          if (m == 0 && !mbar_wait(&c.S.slot_full[kr.s], kr.ph, p.err, timed_out)) break;
+          tc_fence_after();
+          scores(m, cnt[m]);
+        }
+      }
+      if (*timed_out) break;
+      tc_commit(&c.S.slot_empty[vr.s]);
+      vr.step(2);
+      if (NM == 2 && t + 1 < T) {
+        tc_commit(&c.S.slot_empty[kr.s]);
+        kr.step(2);
+      }
+    }
+    for (int m = 0; m < ms; ++m) ++items[m];
+  }
+  // nothing of the tensor cores may be in flight when TMEM is freed
+  tc_commit(&c.S.drain);
+  bool late = false;
+  mbar_wait(&c.S.drain, 0, p.err, &late);
+}
+
+// ---- softmax ---------------------------------------------------------------------
+
+template <int D, int NM, bool QUANT, bool GENERAL>
+struct TtRow {
+  unsigned long long bits;   // drafts that the row sees
+  long long out_row;
+  float slope;               // times log2 e
+  int pos;
+  bool real;
+};
+
+template <int D, int NM, bool QUANT, bool GENERAL>
+__device__ __forceinline__ void tt_row(TtCtx<D, NM, QUANT> &c, const TreeItem &it, int m, int r,
+                                       TtRow<D, NM, QUANT, GENERAL> &w) {
+  const TreeParams &p = c.p;
+  const int row = m * 128 + r;
+  w.real = row < it.rows;
+  w.bits = 0;
+  w.out_row = 0;
+  w.slope = 0.f;
+  w.pos = 0;
+  // the row's query as the A operand; rows past the item's are zeros
+  uint8_t *q = c.q + m * TtCfg<D, NM, QUANT>::ROW_TILE;
+  const uint4 *src = nullptr;
+  if (w.real) {
+    int i, h;
+    tree_row(p, it, it.row0 + row, i, h);
+    w.bits = tree_bits(p, it.b, i, it.c);
+    w.out_row = tree_out_row(p, it.b, i, h);
+    if (GENERAL && p.slopes) {
+      w.slope = p.slopes[h] * kLog2e;
+      w.pos = it.n - it.c + (p.depths ? p.depths[static_cast<long long>(it.b) * p.nq + i] : i);
+    }
+    src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.q) + w.out_row * (D * 2));
+  }
+#pragma unroll
+  for (int ch = 0; ch < D / 8; ++ch)
+    *reinterpret_cast<uint4 *>(q + (ch >> 3) * (TT * 128) + sw128(r, ch & 7)) =
+        w.real ? src[ch] : make_uint4(0u, 0u, 0u, 0u);
+  fence_async_smem();
+  mbar_arrive(&c.S.q_full[m]);
+}
+
+template <int D, int NM, bool QUANT, bool GENERAL>
+__device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_out) {
+  using Cfg = TtCfg<D, NM, QUANT>;
+  const TreeParams &p = c.p;
+  const int m = NM == 2 ? (threadIdx.x - Cfg::SOFTMAX_T0) >> 7 : 0;
+  const int r = threadIdx.x & 127;
+  const uint32_t lanes = static_cast<uint32_t>(r & 96) << 16;   // this warp's TMEM lanes
+  const uint32_t o_at = c.S.tmem_base + lanes + Cfg::O_COL + m * 128;
+  const float scale = p.sigma * kLog2e;
+  uint32_t cnt = 0, tile = 0, k = 0;   // tiles of this row tile, of the CTA, items of the CTA
+  // every wait's outcome is the warp's: TMEM instructions are for whole warps
+  const auto wait = [&](uint64_t *bar, uint32_t par) {
+    mbar_wait(bar, par, p.err, timed_out);
+    if (__any_sync(0xffffffffu, *timed_out)) *timed_out = true;
+    return !*timed_out;
+  };
+  // the next item that has rows for this row tile
+  const auto advance = [&](TreeItem &it) {
+    while (tree_next<TT, Cfg::RB>(p, cur, it)) {
+      if (m * 128 < it.rows) return true;
+      tile += it.t1 - it.t0;
+      ++k;
+    }
+    return false;
+  };
+  TreeItem it;
+  TtRow<D, NM, QUANT, GENERAL> row;
+  bool more = advance(it);
+  if (more) tt_row<D, NM, QUANT, GENERAL>(c, it, m, r, row);
+  while (more) {
+    const int pre = it.n - it.c;
+    float ref = -INFINITY, l = 0.f;
+    for (int t = it.t0; t < it.t1; ++t, ++tile, ++cnt) {
+      const int sb = NM == 1 ? cnt & 1 : m;
+      const uint32_t s_at = c.S.tmem_base + lanes + Cfg::S_COL + sb * 128;
+      const int mi = tile & (META_RING - 1);
+      if (!wait(&c.S.meta_full[mi], (tile / META_RING) & 1u)) return;
+      if (!wait(&c.S.s_full[sb], NM == 1 ? (cnt >> 1) & 1u : cnt & 1u)) return;
+      tc_fence_after();
+      float x[TT];
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) tt_ld32(s_at + 32 * ch, x + 32 * ch);
+      tc_wait_ld();
+      const int j0 = t * TT;
+      uint32_t seen[4];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) seen[w] = c.S.valid[mi][w];
+      const bool masked = j0 + TT > pre || (seen[0] & seen[1] & seen[2] & seen[3]) != 0xFFFFFFFFu;
+      const bool scaled = QUANT && c.S.meta[QUANT ? mi : 0].scaled;
+      float sc = scale;   // what x still has to be multiplied by
+      if (QUANT && scaled) {
+#pragma unroll
+        for (int i = 0; i < TT; i += 2) {
+          const float4 s2 = *reinterpret_cast<const float4 *>(&c.S.tok[QUANT ? mi : 0][i]);
+          const float2 y = mul2(make_float2(x[i], x[i + 1]), mul2(make_float2(s2.x, s2.z), make_float2(sc, sc)));
+          x[i] = y.x;
+          x[i + 1] = y.y;
+        }
+        sc = 1.f;
+      }
+      if (GENERAL) {
+        if (p.cap > 0.f) {
+          // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)), in units of log2 e
+          const float k1 = (sc == 1.f ? 1.f / kLog2e : p.sigma) * 2.f * kLog2e / p.cap;
+          const float c2 = p.cap * kLog2e;
+#pragma unroll
+          for (int i = 0; i < TT; ++i) x[i] = fmaf(-2.f * c2, rcp_approx(1.f + exp2_approx(x[i] * k1)), c2);
+          sc = 1.f;
+        }
+        if (p.slopes) {
+          const float base = row.slope * static_cast<float>(j0 - row.pos);
+          if (!masked) {
+#pragma unroll
+            for (int i = 0; i < TT; ++i) x[i] = fmaf(x[i], sc, fmaf(row.slope, static_cast<float>(i), base));
+          } else {
+#pragma unroll
+            for (int i = 0; i < TT; ++i) {
+              const int d = j0 + i - pre;   // draft
+              int far = j0 + i - row.pos;
+              if (d >= 0 && d < it.c && p.depths) far = pre + p.depths[static_cast<long long>(it.b) * p.nq + d] - row.pos;
+              x[i] = fmaf(x[i], sc, row.slope * static_cast<float>(far));
+            }
+          }
+          sc = 1.f;
+        }
+      }
+      if (masked) {
+        // tokens before the drafts, and the drafts of the row's bits
+        const int off = pre - j0;
+        uint32_t can[4] = {0u, 0u, 0u, 0u};
+        mask_set_range(can, 0, min(off, TT));
+        unsigned long long lo = 0, hi = 0;
+        if (off <= 0)
+          lo = off > -64 ? row.bits >> -off : 0ull;
+        else if (off < 64) {
+          lo = row.bits << off;
+          hi = row.bits >> (64 - off);
+        } else if (off < 128)
+          hi = row.bits << (off - 64);
+        can[0] |= static_cast<uint32_t>(lo);
+        can[1] |= static_cast<uint32_t>(lo >> 32);
+        can[2] |= static_cast<uint32_t>(hi);
+        can[3] |= static_cast<uint32_t>(hi >> 32);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) seen[w] &= can[w];
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+          if (!((seen[i >> 5] >> (i & 31)) & 1u)) x[i] = -INFINITY;
+      }
+      float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+      for (int i = 4; i < TT; i += 4)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], x[i + y]);
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+      if (t == it.t0) {
+        ref = top;
+      } else if (__any_sync(0xffffffffu, top > ref + RESCALE_STEP)) {
+        // O of the tiles so far moves to the new reference
+        if (!wait(&c.S.pv_done[m], (cnt - 1) & 1u)) return;
+        tc_fence_after();
+        const float to = fmaxf(ref, top);
+        const float f = to == -INFINITY ? 1.f : exp2_approx(ref - to);
+        l *= f;
+        ref = to;
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          float o[32];
+          tt_ld32(o_at + 32 * ch, o);
+          tc_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= f;
+          tt_st32(o_at + 32 * ch, reinterpret_cast<const uint32_t *>(o));
+        }
+        tt_wait_st();
+      }
+      const float2 less = make_float2(ref == -INFINITY ? 0.f : -ref, ref == -INFINITY ? 0.f : -ref);
+      const float2 sc2 = make_float2(sc, sc);
+      float2 sum[4] = {};
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) {
+          const int j = half * 64 + i;
+          const float2 y = fma2(make_float2(x[j], x[j + 1]), sc2, less);
+          float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+          sum[(i >> 1) & 3] = add2(sum[(i >> 1) & 3], e);
+          if (QUANT && scaled) {
+            const float4 s2 = *reinterpret_cast<const float4 *>(&c.S.tok[QUANT ? mi : 0][j]);
+            e = mul2(e, make_float2(s2.y, s2.w));
+            if (masked) {   // an unseen token stays out whatever its page's scale
+              if (!((seen[j >> 5] >> (j & 31)) & 1u)) e.x = 0.f;
+              if (!((seen[j >> 5] >> ((j & 31) + 1)) & 1u)) e.y = 0.f;
+            }
+          }
+          w[i >> 1] = pack_bf16(e.x, e.y);
+        }
+        tt_st32(s_at + 32 * half, w);
+      }
+      const float2 s01 = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+      l += s01.x + s01.y;
+      tt_wait_st();
+      tc_fence_before();
+      mbar_arrive(&c.S.p_full[sb]);
+    }
+    // the next item's queries go in before this one's rows are written out
+    const TreeItem done = it;
+    const TtRow<D, NM, QUANT, GENERAL> mine = row;
+    const uint32_t noted_at = k & (META_RING - 1);
+    ++k;
+    more = advance(it);
+    if (more) tt_row<D, NM, QUANT, GENERAL>(c, it, m, r, row);
+    if (!wait(&c.S.pv_done[m], (cnt - 1) & 1u)) return;
+    tc_fence_after();
+    unsigned long long noted = mine.real ? c.S.nonfinite[noted_at] & mine.bits : 0ull;
+    const long long slot = (2LL * blockIdx.x + (done.t0 > 0 ? 0 : 1)) * Cfg::RB + m * 128 + r;
+    const bool whole = done.whole();
+    const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+#pragma unroll 1
+    for (int ch = 0; ch < D / 32; ++ch) {
+      float o[32];
+      tt_ld32(o_at + 32 * ch, o);
+      tc_wait_ld();
+      if (noted) {   // values of drafts that the MMA was not shown
+        for (int d = 0; d < 64; ++d) {
+          if (!((noted >> d) & 1ull)) continue;
+          const int j = done.n - done.c + d;
+          const long long cell = static_cast<long long>(done.b) * p.max_pages + j / p.P;
+          const int fmt = p.page_fmt ? p.page_fmt[cell] : p.uniform_fmt;
+          const uint8_t *v = p.v_pool[fmt] +
+                             ((p.page_table[cell] * static_cast<long long>(p.Hkv) + done.g) * p.P + j % p.P) * row_bytes(fmt, D);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float y = fmt == CFR_FMT_BF16
+                                ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(v)[32 * ch + i]) << 16)
+                                : e4m3_at(v[32 * ch + i], 0);
+            if (!(fabsf(y) < INFINITY)) o[i] += y;
+          }
+        }
+      }
+      if (mine.real) {
+        if (!whole) {
+          float4 *dst = reinterpret_cast<float4 *>(p.part_acc + slot * D + 32 * ch);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        } else {
+          if (l == 0.f) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+          }
+          if (p.out_fmt == CFR_FMT_F32) {
+            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + mine.out_row * D + 32 * ch);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+          } else {
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + mine.out_row * D + 32 * ch);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                  pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+          }
+        }
+      }
+    }
+    tc_fence_before();
+    mbar_arrive(&c.S.o_free[m]);
+    if (mine.real) {
+      if (!whole) {
+        p.part_m[slot] = ref;
+        p.part_l[slot] = l;
+      } else if (p.lse) {
+        p.lse[mine.out_row] = l == 0.f ? -INFINITY : (ref + log2f(l)) / kLog2e;
+      }
+    }
+  }
+}
+
+// ---- kernel ------------------------------------------------------------------------
+
+template <int D, int NM, bool QUANT>
+constexpr size_t tt_head() {
+  return (sizeof(TtSmem<TtCfg<D, NM, QUANT>::NS, QUANT>) + 1023) / 1024 * 1024;
+}
+template <int D, int NM, bool QUANT>
+constexpr size_t tt_smem() {
+  using Cfg = TtCfg<D, NM, QUANT>;
+  return tt_head<D, NM, QUANT>() + static_cast<size_t>(NM + Cfg::NS) * Cfg::ROW_TILE + 1024;
+}
+
+template <int D, int NM, bool QUANT, bool GENERAL>
+__global__ void __launch_bounds__((TtCfg<D, NM, QUANT>::THREADS), 1)
+    tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap) {
+  using Cfg = TtCfg<D, NM, QUANT>;
+  using Smem = TtSmem<Cfg::NS, QUANT>;
+  static_assert(tt_smem<D, NM, QUANT>() <= 227 * 1024, "shared memory of a block");
+  extern __shared__ uint8_t raw[];
+  uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) / 1024 * 1024);
+  Smem &S = *reinterpret_cast<Smem *>(base);
+  const int warp = threadIdx.x >> 5;
+  TtCtx<D, NM, QUANT> c{p, kmap, vmap, S, base + tt_head<D, NM, QUANT>(),
+                        base + tt_head<D, NM, QUANT>() + NM * Cfg::ROW_TILE, min(128, p.P & -p.P)};
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Cfg::NS; ++i) {
+      mbar_init(&S.slot_full[i], 1);
+      mbar_init(&S.slot_empty[i], 2);   // the MMAs' reads, and the repairing or expanding warps
+      mbar_init(&S.raw_full[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.p_full[i], 128);
+      mbar_init(&S.pv_done[i], 1);
+      mbar_init(&S.q_full[i], 128);
+      mbar_init(&S.o_free[i], 128);
+    }
+    for (int i = 0; i < META_RING; ++i) mbar_init(&S.meta_full[i], 1);
+    mbar_init(&S.drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&S.tmem_base)),
+                 "r"(Cfg::TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  TreeCursor cur;
+  const long long W = tree_find<TT, Cfg::RB>(
+      p, S.scratch, threadIdx.x, Cfg::THREADS,
+      [&](long long w) { return tree_start(w, blockIdx.x, p.grid); }, cur);
+  cur.end = tree_start(W, blockIdx.x + 1, p.grid);
+  tc_fence_after();   // (tree_find synchronises the block)
+  bool timed_out = false;
+  const int wg = warp >> 2;
+  if (wg == 0) {
+    if (Cfg::SPLIT) tt_setmaxnreg<Cfg::SPLIT ? Cfg::REGS_IO : 24>(false);
+    if (warp == 0) {
+      tt_producer<D, NM, QUANT, 0>(c, cur, &timed_out);
+    } else if (warp == 2) {
+      tt_producer<D, NM, QUANT, 1>(c, cur, &timed_out);
+    } else if (warp == 1) {
+      if ((threadIdx.x & 31) == 0) tt_issue<D, NM, QUANT>(c, cur, &timed_out);
+    } else if constexpr (!QUANT) {
+      tt_repair<D, NM>(c, cur, &timed_out);
+    }
+  } else if (wg <= NM) {
+    if (Cfg::SPLIT) tt_setmaxnreg<Cfg::SPLIT ? Cfg::REGS_SOFTMAX : 24>(true);
+    tt_softmax<D, NM, QUANT, GENERAL>(c, cur, &timed_out);
+  } else if constexpr (QUANT) {
+    tt_setmaxnreg<Cfg::REGS_LOADER>(Cfg::REGS_LOADER > Cfg::REGS_LAUNCH);
+    tt_expand<D, NM>(c, cur, &timed_out);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(S.tmem_base), "r"(Cfg::TMEM_COLS) : "memory");
+  }
+}
+
+template <int D, int NM, bool QUANT, bool GENERAL>
+cudaError_t launch(const TreeParams &p, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t s) {
+  using Cfg = TtCfg<D, NM, QUANT>;
+  auto kernel = tree_tc_kernel<D, NM, QUANT, GENERAL>;
+  static bool checked[64];   // per device: the kernel has the registers its split counts on
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !checked[dev]) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(tt_smem<D, NM, QUANT>()));
+    if (e != cudaSuccess) return e;
+    cudaFuncAttributes a;
+    e = cudaFuncGetAttributes(&a, kernel);
+    if (e != cudaSuccess) return e;
+    if (Cfg::SPLIT && a.numRegs != Cfg::REGS_LAUNCH) return cudaErrorInvalidConfiguration;
+    if (dev < 64) checked[dev] = true;
+  }
+  kernel<<<p.grid, Cfg::THREADS, tt_smem<D, NM, QUANT>(), s>>>(p, k, v);
+  return cudaGetLastError();
+}
+
+template <int D, int NM, bool QUANT>
+cudaError_t launch_general_or_plain(const TreeParams &p, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t s) {
+  return p.cap > 0.f || p.slopes ? launch<D, NM, QUANT, true>(p, k, v, s) : launch<D, NM, QUANT, false>(p, k, v, s);
+}
+
+}  // namespace
+
+// Whether the tensor-core kernel takes the call: bf16 queries, no fp32 pages, pages a multiple of 8 tokens.
+bool tree_tc_supported(const TreeParams &p) {
+  if (p.q_fmt != CFR_FMT_BF16 || p.P % 8 != 0 || p.P > (1 << 24)) return false;
+  if (p.page_fmt ? p.k_pool[CFR_FMT_F32] != nullptr : p.uniform_fmt == CFR_FMT_F32) return false;
+  return p.pool_pages[CFR_FMT_BF16] * p.Hkv <= 0x7fffffffLL / p.P;   // rows of a tensor map
+}
+
+// Rows of a work item: the rows of one kv head, up to 256.
+int tree_tc_rows(int most_rows) { return most_rows > 128 ? 256 : 128; }
+
+cudaError_t launch_tree_tc(const TreeParams &p, int rb, cudaStream_t s) {
+  CUtensorMap k, v;
+  std::memset(&k, 0, sizeof(k));
+  std::memset(&v, 0, sizeof(v));
+  const int box = p.P & -p.P;
+  if (p.k_pool[CFR_FMT_BF16] && p.pool_pages[CFR_FMT_BF16] > 0) {
+    const long long rows = p.pool_pages[CFR_FMT_BF16] * p.Hkv * p.P;
+    if (!encode_pool_map(&k, p.k_pool[CFR_FMT_BF16], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, p.D, box < 128 ? box : 128) ||
+        !encode_pool_map(&v, p.v_pool[CFR_FMT_BF16], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, rows, p.D, box < 128 ? box : 128))
+      return cudaErrorInvalidValue;
+  }
+  bool quant = !p.page_fmt && is_quantised(p.uniform_fmt);
+  if (p.page_fmt) quant = p.k_pool[CFR_FMT_I8] || p.k_pool[CFR_FMT_I4] || p.k_pool[CFR_FMT_FP8];
+  if (p.D == 128) {
+    if (rb == 128)
+      return quant ? launch_general_or_plain<128, 1, true>(p, k, v, s) : launch_general_or_plain<128, 1, false>(p, k, v, s);
+    return quant ? launch_general_or_plain<128, 2, true>(p, k, v, s) : launch_general_or_plain<128, 2, false>(p, k, v, s);
+  }
+  if (rb == 128)
+    return quant ? launch_general_or_plain<64, 1, true>(p, k, v, s) : launch_general_or_plain<64, 1, false>(p, k, v, s);
+  return quant ? launch_general_or_plain<64, 2, true>(p, k, v, s) : launch_general_or_plain<64, 2, false>(p, k, v, s);
+}
+
+}  // namespace cfr

@@ -308,3 +308,32 @@ def test_offsets_beyond_32_bits():
     assert got.run() == 0
     torch.cuda.synchronize()
     assert torch.equal(want.out, got.out) and torch.equal(want.lse, got.lse)
+
+
+# long enough for a CTA to walk many tiles of an item, several items and their borders
+@pytest.mark.parametrize("Q", [3, 40], ids=["12rows", "160rows"])
+@pytest.mark.parametrize("name", ["bf16-p16", "bf16-p16-d64", "bf16-p24", "i8-p16", "i8-p256", "i4-p32", "fp8-p8-d64", "tiered-p16",
+                                  "tiered-p128", "tiered-p256-d64", "f32-p16"])
+def test_long_sequences(name, Q):
+    lens = (9001, 18303, 130, 5120)
+    cfg = {**CONFIGS[name], "Hq": 8, "Hkv": 2}
+    case = tree_case(lens, Q, **cfg)
+    masks, depths = trees(len(lens), Q, 21)
+    call = TreeCall(case, masks, depths, q_lens=[Q, Q - 1, Q, Q // 2])
+    assert call.run() == 0
+    call.check()
+    assert int(call.err.item()) == 0
+    again = TreeCall(case, masks, depths, q_lens=[Q, Q - 1, Q, Q // 2])
+    assert again.run() == 0
+    torch.cuda.synchronize()
+    assert torch.equal(again.out, call.out) and torch.equal(again.lse, call.lse)
+
+
+@pytest.mark.parametrize("name", ["bf16-p16", "tiered-p128", "f32-p16"])
+def test_scores_that_grow_along_the_sequence(name):
+    # each tile's maximum passes the last one's by more than the step at which the running reference moves
+    case = tree_case((9001, 2100), 3, softmax_scale=1.0, alibi=True, **CONFIGS[name])
+    case.alibi_slopes[:] = torch.tensor([0.2, 0.11, 0.05, 0.02, 0.5, 1.0, 0.3, 0.07], device="cuda")
+    call = TreeCall(case)
+    assert call.run() == 0
+    call.check()
