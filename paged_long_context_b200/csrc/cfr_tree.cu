@@ -333,7 +333,7 @@ TreeWs tree_ws(int slots, int rb, int d) {
 }
 
 // Scratch of the larger of the two kernels' cuts: the general one (two CTAs an SM,
-// 32 rows) or the tensor-core one (one CTA an SM, 128 or 256 rows).  `rows`: the
+// 32 rows) or the tensor-core one (one CTA an SM, 64 or 256 rows).  `rows`: the
 // most rows that a kv head can have.
 TreeWs tree_scratch(int sms, int rows, int d) {
   const TreeWs a = tree_ws(2 * general_grid(sms), kGenRB, d), b = tree_ws(2 * sms, tree_tc_rows(rows), d);
@@ -464,7 +464,7 @@ cfr_status cfr_paged_decode_tree(const void *q, int32_t q_fmt, const cfr_kv_pool
   cudaError_t e = tc ? launch_tree_tc(p, rb, s) : p.D == 128 ? launch_general<128>(p, s) : launch_general<64>(p, s);
   if (e != cudaSuccess) return CFR_ERR_CUDA;
   e = !tc ? launch_tree_merge<kGenTT, kGenRB>(p, s)
-      : rb == 128 ? launch_tree_merge<128, 128>(p, s)
+      : rb == 64 ? launch_tree_merge<128, 64>(p, s)
                   : launch_tree_merge<128, 256>(p, s);
   return e == cudaSuccess ? CFR_OK : CFR_ERR_CUDA;
 }

@@ -21,10 +21,17 @@
 // E4M3 codes are all exact there); the K scale multiplies the fp32 score of its
 // token, the V scale its probability.
 //
-// NM = 1 (up to 128 rows of a kv head): S is double-buffered, the scores of the
-// next tile are computed under the softmax of this one.  NM = 2 (more rows): two
-// row tiles of one K/V tile, each with a softmax warpgroup, take turns on the
-// tensor cores; K and V are read once for 256 rows.
+// Two variants.
+//  - Narrow (NM = 1): up to 64 rows of a kv head.  128 rows of Q would leave half
+//    the tensor core's lanes and softmax threads idle, so the rows stand in Q
+//    twice (or four times, up to 32 rows), and copy i of a row takes the i-th
+//    half (quarter) of every tile's tokens: its own maximum, sum and O, with
+//    zeros in P for the other tokens.  All four schedulers of the SM then share
+//    the exponentials, and the copies are joined when an item ends.
+//  - Wide (NM = 2): two row tiles of one K/V tile, each with a softmax warpgroup; K
+//    and V are read once for 256 rows.  TMEM holds two S buffers of 64 tokens
+//    for each row tile beside the two O, so a tile is taken in two steps.
+// Either way the scores of a step are computed while the one before is in the softmax.
 //
 // Warps: warpgroup 0 = K producer (warp 0), MMA issuer (1), V producer (2), V
 // repair (3); then NM softmax warpgroups; with quantised pools one more that
@@ -59,25 +66,22 @@ constexpr float RESCALE_STEP = 8.f;
 
 template <int D, int NM, bool QUANT>
 struct TtCfg {
-  static constexpr int RB = 128 * NM;
+  static constexpr int RB = NM == 1 ? 64 : 256;  // rows of an item
+  static constexpr int STEP = 128 / NM;          // tokens of a step
+  static constexpr int STEPS = NM;               // steps of a tile
   static constexpr int ROW_TILE = 128 * D * 2;   // bytes of 128 bf16 rows: a Q tile, a K or V slot
   // slots that fit beside the queries (227 KB in all); heads of 64 have slots of half the size
-  static constexpr int NS = (D == 128 ? 1 : 2) * (QUANT ? (NM == 1 ? 5 : 4) : (NM == 1 ? 6 : D == 128 ? 5 : 6));
+  static constexpr int NS = (D == 128 ? 1 : 2) * (NM == 2 && QUANT ? 4 : 5);
   static constexpr int WGS = 1 + NM + (QUANT ? 1 : 0);
   static constexpr int THREADS = 128 * WGS;
   static constexpr int SOFTMAX_T0 = 128;
   static constexpr int LOADER_T0 = 128 * (1 + NM);
-  // registers: what the block is launched with (65536 over its threads, a multiple of 8, at
-  // most 255), and the split over its warpgroups
-  static constexpr int REGS_LAUNCH = NM == 1 && !QUANT ? 255 : 65536 / THREADS / 8 * 8;
-  static constexpr bool SPLIT = !(NM == 1 && !QUANT);
-  static constexpr int REGS_IO = QUANT ? (NM == 1 ? 96 : 72) : 88;
-  static constexpr int REGS_SOFTMAX = QUANT ? (NM == 1 ? 232 : 176) : 208;
-  static constexpr int REGS_LOADER = QUANT ? (NM == 1 ? 176 : 88) : 0;
-  static_assert(!SPLIT || REGS_IO + NM * REGS_SOFTMAX + REGS_LOADER <= WGS * REGS_LAUNCH,
-                "the split must fit the registers the block was launched with");
+  // TMEM columns: S, two buffers of STEP for each row tile; O, 128 for each; narrow: P, two
+  // buffers of its own, so that the zeros of other copies' tokens stay (wide: P over its S)
   static constexpr int TMEM_COLS = 512;
-  static constexpr int S_COL = 0, O_COL = 256;   // S (two of 128 columns), O (NM of 128)
+  static constexpr int S_COL = 0, O_COL = 256, P_COL = 384;
+  __device__ static __forceinline__ uint32_t s_col(int m, int b) { return S_COL + (2 * m + b) * STEP; }
+  __device__ static __forceinline__ uint32_t p_col(int m, int b) { return NM == 1 ? P_COL + 64 * b : s_col(m, b); }
 };
 
 struct TtMeta {
@@ -87,11 +91,13 @@ struct TtMeta {
   float ks[MAX_PIECES], vs[MAX_PIECES];
 };
 
-template <int NS, bool QUANT>
+template <int NS, int NM, bool QUANT>
 struct TtSmem {
   uint64_t slot_full[NS], slot_empty[NS], raw_full[NS];
-  uint64_t s_full[2], p_full[2], pv_done[2], q_full[2], o_free[2];
-  uint64_t meta_full[META_RING], drain;
+  // by row tile and, where two steps can be under way, by the step's parity: a wait by
+  // parity must begin no earlier than one phase before the one it is for
+  uint64_t s_full[2 * NM], p_full[2 * NM], pv_done[2 * NM], q_full[NM], o_free[NM];
+  uint64_t meta_full[META_RING], drain, meet;
   uint32_t tmem_base;
   int flag[NS];
   unsigned long long nonfinite[META_RING];  // of item k & 7: drafts whose V was repaired
@@ -101,15 +107,10 @@ struct TtSmem {
   TtMeta meta[QUANT ? META_RING : 1];
   uint32_t valid[META_RING][4];
   alignas(16) float2 tok[QUANT ? META_RING : 1][QUANT ? TT : 2];  // K and V scale of each token
+  // joining of the copies (narrow): 16 columns of O of every row, its maximum and sum
+  alignas(16) float join[NM == 1 ? 128 : 1][20];
+  float2 join_ml[NM == 1 ? 128 : 1];
 };
-
-template <int N>
-__device__ __forceinline__ void tt_setmaxnreg(bool inc) {
-  if (inc)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-  else
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
 
 // D[128 x N] (+)= A (TMEM) . B (shared memory)
 __device__ __forceinline__ void tt_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
@@ -134,14 +135,21 @@ __device__ __forceinline__ void tt_ld32(uint32_t taddr, float *v) {
       : "memory");
 }
 
-__device__ __forceinline__ void tt_st32(uint32_t taddr, const uint32_t *r) {
+__device__ __forceinline__ void tt_ld16(uint32_t taddr, float *v) {
+  uint32_t *r = reinterpret_cast<uint32_t *>(v);
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tt_st16(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tt_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -249,7 +257,7 @@ __device__ __forceinline__ bool repair16(uint4 &v) {
 template <int D, int NM, bool QUANT>
 struct TtCtx {
   using Cfg = TtCfg<D, NM, QUANT>;
-  using Smem = TtSmem<Cfg::NS, QUANT>;
+  using Smem = TtSmem<Cfg::NS, NM, QUANT>;
   const TreeParams &p;
   const CUtensorMap &kmap, &vmap;
   Smem &S;
@@ -582,67 +590,61 @@ __device__ void tt_issue(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_out
   const TreeParams &p = c.p;
   const uint32_t tmem = c.S.tmem_base;
   const uint32_t qa = smem_u32(c.q), sa = smem_u32(c.slots);
-  constexpr uint32_t qk_desc = tc_idesc(1, 0, 0, TT), pv_desc = tc_idesc(1, 0, 1, D);
+  constexpr uint32_t qk_desc = tc_idesc(1, 0, 0, Cfg::STEP), pv_desc = tc_idesc(1, 0, 1, D);
+  constexpr int STEP_BYTES = Cfg::STEP * 128;     // of a step's rows in each 64-column half of a slot
   Ring<Cfg::NS> kr, vr;
   vr.step(1);
-  uint32_t cnt[2] = {0, 0}, items[2] = {0, 0};   // tiles and items of each row tile so far
-  const auto sbuf = [&](int m, uint32_t n) { return NM == 1 ? static_cast<int>(n & 1) : m; };
-  const auto spar = [&](uint32_t n) { return NM == 1 ? (n >> 1) & 1u : n & 1u; };
-  const auto scores = [&](int m, uint32_t n) {   // S of row tile m's n-th tile, from the K slot
-    const uint32_t d = tmem + Cfg::S_COL + sbuf(m, n) * 128;
-    const uint32_t a = qa + m * Cfg::ROW_TILE, b = sa + kr.s * Cfg::ROW_TILE;
+  uint32_t cnt[2] = {0, 0}, items[2] = {0, 0};    // steps and items of each row tile so far
+  const auto scores = [&](int m, uint32_t n, int h) {   // S of row tile m's n-th step, from the K slot
+    const uint32_t d = tmem + Cfg::s_col(m, n & 1);
+    const uint64_t a = tc_sdesc(qa + m * Cfg::ROW_TILE, 16, 1024, 2);
+    const uint64_t b = tc_sdesc(sa + kr.s * Cfg::ROW_TILE + h * STEP_BYTES, 16, 1024, 2);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-      const uint32_t off = (k >> 2) * (TT * 128) + (k & 3) * 32;
-      tc_mma(d, tc_sdesc(a + off, 16, 1024, 2), tc_sdesc(b + off, 16, 1024, 2), qk_desc, k > 0 ? 1u : 0u);
+      const uint64_t off = ((k >> 2) * (TT * 128) + (k & 3) * 32) >> 4;
+      tc_mma(d, a + off, b + off, qk_desc, k > 0 ? 1u : 0u);
     }
-    tc_commit(&c.S.s_full[sbuf(m, n)]);
+    tc_commit(&c.S.s_full[2 * m + (n & 1)]);
   };
   TreeItem it;
   while (!*timed_out && tree_next<TT, Cfg::RB>(p, cur, it)) {
     const int ms = NM == 2 && it.rows > 128 ? 2 : 1;
-    const int T = it.t1 - it.t0;
-    if (!mbar_wait(&c.S.slot_full[kr.s], kr.ph, p.err, timed_out)) break;
+    const int steps = (it.t1 - it.t0) * Cfg::STEPS;
     for (int m = 0; m < ms; ++m)
       if (!mbar_wait(&c.S.q_full[m], items[m] & 1u, p.err, timed_out)) break;
     if (*timed_out) break;
-    tc_fence_after();
-    for (int m = 0; m < ms; ++m) scores(m, cnt[m]);
-    tc_commit(&c.S.slot_empty[kr.s]);
-    kr.step(2);
-    for (int t = 0; t < T; ++t) {
-      if (NM == 1 && t + 1 < T) {
-        if (!mbar_wait(&c.S.slot_full[kr.s], kr.ph, p.err, timed_out)) break;
+    // step -1 only issues the scores of step 0
+    for (int s = -1; s < steps; ++s) {
+      if (s + 1 < steps) {
+        const int h = (s + 1) % Cfg::STEPS;
+        if (h == 0 && !mbar_wait(&c.S.slot_full[kr.s], kr.ph, p.err, timed_out)) break;
         tc_fence_after();
-        scores(0, cnt[0] + 1);
-        tc_commit(&c.S.slot_empty[kr.s]);
-        kr.step(2);
-      }
-      if (!mbar_wait(&c.S.slot_full[vr.s], vr.ph, p.err, timed_out)) break;
-      for (int m = 0; m < ms; ++m) {
-        const int sb = sbuf(m, cnt[m]);
-        if (t == 0 && !mbar_wait(&c.S.o_free[m], (items[m] & 1u) ^ 1u, p.err, timed_out)) break;
-        if (!mbar_wait(&c.S.p_full[sb], spar(cnt[m]), p.err, timed_out)) break;
-        tc_fence_after();
-        const uint32_t d = tmem + Cfg::O_COL + m * 128, a = tmem + Cfg::S_COL + sb * 128;
-        const uint32_t b = sa + vr.s * Cfg::ROW_TILE;
-#pragma unroll
-        for (int k = 0; k < TT / 16; ++k)
-          tt_mma_ts(d, a + k * 8, tc_sdesc(b + k * 2048, TT * 128, 1024, 2), pv_desc, t > 0 || k > 0 ? 1u : 0u);
-        tc_commit(&c.S.pv_done[m]);
-        ++cnt[m];
-        if (NM == 2 && t + 1 < T) {
-          if (m == 0 && !mbar_wait(&c.S.slot_full[kr.s], kr.ph, p.err, timed_out)) break;
-          tc_fence_after();
-          scores(m, cnt[m]);
+        for (int m = 0; m < ms; ++m) scores(m, cnt[m] + (s < 0 ? 0 : 1), h);
+        if (h == Cfg::STEPS - 1) {
+          tc_commit(&c.S.slot_empty[kr.s]);
+          kr.step(2);
         }
       }
+      if (s < 0) continue;
+      const int h = s % Cfg::STEPS;
+      if (h == 0 && !mbar_wait(&c.S.slot_full[vr.s], vr.ph, p.err, timed_out)) break;
+      for (int m = 0; m < ms; ++m) {
+        const int b = cnt[m] & 1;
+        if (s == 0 && !mbar_wait(&c.S.o_free[m], (items[m] & 1u) ^ 1u, p.err, timed_out)) break;
+        if (!mbar_wait(&c.S.p_full[2 * m + b], (cnt[m] >> 1) & 1u, p.err, timed_out)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + Cfg::O_COL + m * 128, a = tmem + Cfg::p_col(m, b);
+        const uint64_t v = tc_sdesc(sa + vr.s * Cfg::ROW_TILE + h * STEP_BYTES, TT * 128, 1024, 2);
+#pragma unroll
+        for (int k = 0; k < Cfg::STEP / 16; ++k)
+          tt_mma_ts(d, a + k * 8, v + static_cast<uint64_t>(k * 2048 >> 4), pv_desc, s > 0 || k > 0 ? 1u : 0u);
+        tc_commit(&c.S.pv_done[2 * m + b]);
+        ++cnt[m];
+      }
       if (*timed_out) break;
-      tc_commit(&c.S.slot_empty[vr.s]);
-      vr.step(2);
-      if (NM == 2 && t + 1 < T) {
-        tc_commit(&c.S.slot_empty[kr.s]);
-        kr.step(2);
+      if (h == Cfg::STEPS - 1) {
+        tc_commit(&c.S.slot_empty[vr.s]);
+        vr.step(2);
       }
     }
     for (int m = 0; m < ms; ++m) ++items[m];
@@ -655,31 +657,40 @@ __device__ void tt_issue(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_out
 
 // ---- softmax ---------------------------------------------------------------------
 
-template <int D, int NM, bool QUANT, bool GENERAL>
 struct TtRow {
   unsigned long long bits;   // drafts that the row sees
   long long out_row;
   float slope;               // times log2 e
   int pos;
+  int row, copy, width;      // row of the item, its copy, tokens of a step that the copy takes
   bool real;
 };
 
+// This thread's row of the item, and its query as the A operand (rows past the item's
+// are zeros).
 template <int D, int NM, bool QUANT, bool GENERAL>
-__device__ __forceinline__ void tt_row(TtCtx<D, NM, QUANT> &c, const TreeItem &it, int m, int r,
-                                       TtRow<D, NM, QUANT, GENERAL> &w) {
+__device__ __forceinline__ void tt_row(TtCtx<D, NM, QUANT> &c, const TreeItem &it, int m, int r, TtRow &w) {
   const TreeParams &p = c.p;
-  const int row = m * 128 + r;
-  w.real = row < it.rows;
+  if (NM == 1) {
+    const int lg = it.rows <= 32 ? 5 : 6;   // four copies of 32 rows, or two of 64
+    w.row = r & ((1 << lg) - 1);
+    w.copy = r >> lg;
+    w.width = 1 << lg;
+  } else {
+    w.row = m * 128 + r;
+    w.copy = 0;
+    w.width = TtCfg<D, NM, QUANT>::STEP;
+  }
+  w.real = w.row < it.rows;
   w.bits = 0;
   w.out_row = 0;
   w.slope = 0.f;
   w.pos = 0;
-  // the row's query as the A operand; rows past the item's are zeros
   uint8_t *q = c.q + m * TtCfg<D, NM, QUANT>::ROW_TILE;
   const uint4 *src = nullptr;
   if (w.real) {
     int i, h;
-    tree_row(p, it, it.row0 + row, i, h);
+    tree_row(p, it, it.row0 + w.row, i, h);
     w.bits = tree_bits(p, it.b, i, it.c);
     w.out_row = tree_out_row(p, it.b, i, h);
     if (GENERAL && p.slopes) {
@@ -696,21 +707,64 @@ __device__ __forceinline__ void tt_row(TtCtx<D, NM, QUANT> &c, const TreeItem &i
   mbar_arrive(&c.S.q_full[m]);
 }
 
+// values of drafts that the MMA was not shown, back into 16 columns of O
+template <int D>
+__device__ __forceinline__ void tt_add_back(const TreeParams &p, const TreeItem &it, unsigned long long noted, int col,
+                                            float (&o)[16]) {
+#pragma unroll 1
+  for (int d = 0; d < 64; ++d) {
+    if (!((noted >> d) & 1ull)) continue;
+    const int j = it.n - it.c + d;
+    const long long cell = static_cast<long long>(it.b) * p.max_pages + j / p.P;
+    const int fmt = p.page_fmt ? p.page_fmt[cell] : p.uniform_fmt;
+    const uint8_t *v = p.v_pool[fmt] +
+                       ((p.page_table[cell] * static_cast<long long>(p.Hkv) + it.g) * p.P + j % p.P) * row_bytes(fmt, D);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float y = fmt == CFR_FMT_BF16
+                          ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(v)[col + i]) << 16)
+                          : e4m3_at(v[col + i], 0);
+      if (!(fabsf(y) < INFINITY)) o[i] += y;
+    }
+  }
+}
+
+// N finished output values of a row (or, where `part`, of its partial) from column col on
+template <int N>
+__device__ __forceinline__ void tt_put(const TreeParams &p, bool part, long long row, int col, const float *o) {
+  if (part || p.out_fmt == CFR_FMT_F32) {
+    float4 *dst = reinterpret_cast<float4 *>((part ? p.part_acc : static_cast<float *>(p.out)) + row * p.D + col);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+  } else {
+    uint2 *dst = reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + row * p.D + col);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) dst[i] = make_uint2(pack_bf16(o[4 * i], o[4 * i + 1]), pack_bf16(o[4 * i + 2], o[4 * i + 3]));
+  }
+}
+
 template <int D, int NM, bool QUANT, bool GENERAL>
 __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_out) {
   using Cfg = TtCfg<D, NM, QUANT>;
   const TreeParams &p = c.p;
   const int m = NM == 2 ? (threadIdx.x - Cfg::SOFTMAX_T0) >> 7 : 0;
   const int r = threadIdx.x & 127;
-  const uint32_t lanes = static_cast<uint32_t>(r & 96) << 16;   // this warp's TMEM lanes
-  const uint32_t o_at = c.S.tmem_base + lanes + Cfg::O_COL + m * 128;
+  const uint32_t lanes = c.S.tmem_base + (static_cast<uint32_t>(r & 96) << 16);   // this warp's TMEM lanes
+  const uint32_t o_at = lanes + Cfg::O_COL + m * 128;
   const float scale = p.sigma * kLog2e;
-  uint32_t cnt = 0, tile = 0, k = 0;   // tiles of this row tile, of the CTA, items of the CTA
+  uint32_t cnt = 0, tile = 0, k = 0;   // steps of this row tile, tiles and items of the CTA
+  uint32_t met = 0;                    // meetings of the warpgroup's threads so far
+  int zeroed = 0;                      // (narrow) the width for which P's other columns are zeros
   // every wait's outcome is the warp's: TMEM instructions are for whole warps
   const auto wait = [&](uint64_t *bar, uint32_t par) {
     mbar_wait(bar, par, p.err, timed_out);
     if (__any_sync(0xffffffffu, *timed_out)) *timed_out = true;
     return !*timed_out;
+  };
+  // all threads of the warpgroup (a named barrier would have no time limit)
+  const auto meet = [&]() {
+    mbar_arrive(&c.S.meet);
+    return wait(&c.S.meet, met++ & 1u);
   };
   // the next item that has rows for this row tile
   const auto advance = [&](TreeItem &it) {
@@ -722,214 +776,224 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_o
     return false;
   };
   TreeItem it;
-  TtRow<D, NM, QUANT, GENERAL> row;
+  TtRow row;
   bool more = advance(it);
   if (more) tt_row<D, NM, QUANT, GENERAL>(c, it, m, r, row);
   while (more) {
     const int pre = it.n - it.c;
+    const int first = row.copy * row.width;   // the copy's first token of a step
+    const bool wide = NM == 2 || row.width == 64;
+    const bool idle = !__any_sync(0xffffffffu, row.real);
     float ref = -INFINITY, l = 0.f;
-    for (int t = it.t0; t < it.t1; ++t, ++tile, ++cnt) {
-      const int sb = NM == 1 ? cnt & 1 : m;
-      const uint32_t s_at = c.S.tmem_base + lanes + Cfg::S_COL + sb * 128;
+    if (NM == 1 && zeroed != row.width) {
+      const uint32_t z[16] = {};
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) tt_st16(lanes + Cfg::P_COL + 16 * i, z);
+      tt_wait_st();
+      zeroed = row.width;
+    }
+    const int steps = (it.t1 - it.t0) * Cfg::STEPS;
+    for (int s = 0; s < steps; ++s, ++cnt) {
+      const int b = cnt & 1, h = s % Cfg::STEPS;
       const int mi = tile & (META_RING - 1);
-      if (!wait(&c.S.meta_full[mi], (tile / META_RING) & 1u)) return;
-      if (!wait(&c.S.s_full[sb], NM == 1 ? (cnt >> 1) & 1u : cnt & 1u)) return;
+      // (scores first: they say that the tile 8 before this one was described, whatever tiles this
+      // warpgroup passed over)
+      if (!wait(&c.S.s_full[2 * m + b], (cnt >> 1) & 1u)) return;
+      if (h == 0 && !wait(&c.S.meta_full[mi], (tile / META_RING) & 1u)) return;
       tc_fence_after();
-      float x[TT];
-#pragma unroll
-      for (int ch = 0; ch < 4; ++ch) tt_ld32(s_at + 32 * ch, x + 32 * ch);
-      tc_wait_ld();
-      const int j0 = t * TT;
-      uint32_t seen[4];
-#pragma unroll
-      for (int w = 0; w < 4; ++w) seen[w] = c.S.valid[mi][w];
-      const bool masked = j0 + TT > pre || (seen[0] & seen[1] & seen[2] & seen[3]) != 0xFFFFFFFFu;
+      if (idle) {   // a warp without rows: what it leaves in P reaches no other row
+        tc_fence_before();
+        mbar_arrive(&c.S.p_full[2 * m + b]);
+        if (h == Cfg::STEPS - 1) ++tile;
+        continue;
+      }
+      float x[64];
+      const uint32_t s_at = lanes + Cfg::s_col(m, b) + first;
+      tt_ld32(s_at, x);
+      if (wide) tt_ld32(s_at + 32, x + 32);
+      const int in_tile = h * Cfg::STEP + first;                // the copy's first token in the tile
+      const int off = pre - ((it.t0 + s / Cfg::STEPS) * TT + in_tile);  // its tokens before the drafts
+      unsigned long long seen = c.S.valid[mi][in_tile >> 5];
+      if (wide) seen |= static_cast<unsigned long long>(c.S.valid[mi][(in_tile >> 5) + 1]) << 32;
+      const bool masked = off < row.width || seen != (wide ? ~0ull : 0xFFFFFFFFull);
       const bool scaled = QUANT && c.S.meta[QUANT ? mi : 0].scaled;
-      float sc = scale;   // what x still has to be multiplied by
+      const float2 *tok = &c.S.tok[QUANT ? mi : 0][QUANT ? in_tile : 0];
+      tc_wait_ld();
+      // Scores as they enter the exponential, in units of log2 e: times the softmax scale
+      // (left to the exponential where nothing else is to be done), the pages' scales, capped, less the
+      // distance, -inf where the row does not see the token.
+      float sc = scale;
       if (QUANT && scaled) {
 #pragma unroll
-        for (int i = 0; i < TT; i += 2) {
-          const float4 s2 = *reinterpret_cast<const float4 *>(&c.S.tok[QUANT ? mi : 0][i]);
-          const float2 y = mul2(make_float2(x[i], x[i + 1]), mul2(make_float2(s2.x, s2.z), make_float2(sc, sc)));
+        for (int i = 0; i < 64; i += 2) {
+          if (i == 32 && !wide) break;
+          const float4 s2 = *reinterpret_cast<const float4 *>(tok + i);
+          const float2 y = mul2(make_float2(x[i], x[i + 1]), mul2(make_float2(s2.x, s2.z), make_float2(scale, scale)));
           x[i] = y.x;
           x[i + 1] = y.y;
         }
         sc = 1.f;
       }
-      if (GENERAL) {
-        if (p.cap > 0.f) {
-          // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)), in units of log2 e
-          const float k1 = (sc == 1.f ? 1.f / kLog2e : p.sigma) * 2.f * kLog2e / p.cap;
-          const float c2 = p.cap * kLog2e;
+      if (GENERAL && p.cap > 0.f) {
+        // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap))
+        const float k1 = (QUANT && scaled ? 1.f : scale) * 2.f / p.cap, c2 = p.cap * kLog2e;
 #pragma unroll
-          for (int i = 0; i < TT; ++i) x[i] = fmaf(-2.f * c2, rcp_approx(1.f + exp2_approx(x[i] * k1)), c2);
-          sc = 1.f;
+        for (int i = 0; i < 64; ++i) {
+          if (i == 32 && !wide) break;
+          x[i] = fmaf(-2.f * c2, rcp_approx(1.f + exp2_approx(x[i] * k1)), c2);
         }
-        if (p.slopes) {
-          const float base = row.slope * static_cast<float>(j0 - row.pos);
-          if (!masked) {
+        sc = 1.f;
+      }
+      if (GENERAL && p.slopes) {
+        const float base = row.slope * static_cast<float>(pre - off - row.pos);
 #pragma unroll
-            for (int i = 0; i < TT; ++i) x[i] = fmaf(x[i], sc, fmaf(row.slope, static_cast<float>(i), base));
-          } else {
+        for (int i = 0; i < 64; ++i) {
+          if (i == 32 && !wide) break;
+          x[i] = fmaf(x[i], sc, fmaf(row.slope, static_cast<float>(i), base));
+        }
+        if (masked && p.depths) {   // a draft stands at its depth
 #pragma unroll
-            for (int i = 0; i < TT; ++i) {
-              const int d = j0 + i - pre;   // draft
-              int far = j0 + i - row.pos;
-              if (d >= 0 && d < it.c && p.depths) far = pre + p.depths[static_cast<long long>(it.b) * p.nq + d] - row.pos;
-              x[i] = fmaf(x[i], sc, row.slope * static_cast<float>(far));
-            }
+          for (int i = 0; i < 64; ++i) {
+            const int d = i - off;
+            if (d >= 0 && d < it.c)
+              x[i] = fmaf(row.slope, static_cast<float>(p.depths[static_cast<long long>(it.b) * p.nq + d] - d), x[i]);
           }
-          sc = 1.f;
         }
+        sc = 1.f;
       }
       if (masked) {
         // tokens before the drafts, and the drafts of the row's bits
-        const int off = pre - j0;
-        uint32_t can[4] = {0u, 0u, 0u, 0u};
-        mask_set_range(can, 0, min(off, TT));
-        unsigned long long lo = 0, hi = 0;
-        if (off <= 0)
-          lo = off > -64 ? row.bits >> -off : 0ull;
-        else if (off < 64) {
-          lo = row.bits << off;
-          hi = row.bits >> (64 - off);
-        } else if (off < 128)
-          hi = row.bits << (off - 64);
-        can[0] |= static_cast<uint32_t>(lo);
-        can[1] |= static_cast<uint32_t>(lo >> 32);
-        can[2] |= static_cast<uint32_t>(hi);
-        can[3] |= static_cast<uint32_t>(hi >> 32);
+        seen &= off >= 64 ? ~0ull : off > 0 ? (row.bits << off) | ((1ull << off) - 1ull) : off > -64 ? row.bits >> -off : 0ull;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) seen[w] &= can[w];
-#pragma unroll
-        for (int i = 0; i < TT; ++i)
-          if (!((seen[i >> 5] >> (i & 31)) & 1u)) x[i] = -INFINITY;
+        for (int i = 0; i < 64; ++i)
+          if (!((seen >> i) & 1ull)) x[i] = -INFINITY;
       }
       float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-      for (int i = 4; i < TT; i += 4)
+      for (int i = 4; i < 64; i += 4) {
+        if (i == 32 && !wide) break;
 #pragma unroll
         for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], x[i + y]);
+      }
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-      if (t == it.t0) {
+      if (s == 0) {
         ref = top;
       } else if (__any_sync(0xffffffffu, top > ref + RESCALE_STEP)) {
-        // O of the tiles so far moves to the new reference
-        if (!wait(&c.S.pv_done[m], (cnt - 1) & 1u)) return;
+        // O of the steps so far moves to the new reference
+        if (!wait(&c.S.pv_done[2 * m + ((cnt - 1) & 1)], ((cnt - 1) >> 1) & 1u)) return;
         tc_fence_after();
         const float to = fmaxf(ref, top);
         const float f = to == -INFINITY ? 1.f : exp2_approx(ref - to);
         l *= f;
         ref = to;
 #pragma unroll 1
-        for (int ch = 0; ch < D / 32; ++ch) {
-          float o[32];
-          tt_ld32(o_at + 32 * ch, o);
+        for (int ch = 0; ch < D / 16; ++ch) {
+          float o[16];
+          tt_ld16(o_at + 16 * ch, o);
           tc_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= f;
-          tt_st32(o_at + 32 * ch, reinterpret_cast<const uint32_t *>(o));
+          for (int i = 0; i < 16; ++i) o[i] *= f;
+          tt_st16(o_at + 16 * ch, reinterpret_cast<const uint32_t *>(o));
         }
         tt_wait_st();
       }
-      const float2 less = make_float2(ref == -INFINITY ? 0.f : -ref, ref == -INFINITY ? 0.f : -ref);
-      const float2 sc2 = make_float2(sc, sc);
-      float2 sum[4] = {};
+      // p = 2^(s - ref), its sum, and P as the MMA's operand
+      const float less = ref == -INFINITY ? 0.f : -ref;
+      const float2 less2 = make_float2(less, less), sc2 = make_float2(sc, sc);
+      float2 sum[2] = {};
+      const uint32_t p_at = lanes + Cfg::p_col(m, b) + first / 2;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        uint32_t w[32];
+        if (half == 1 && !wide) break;
+        uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-          const int j = half * 64 + i;
-          const float2 y = fma2(make_float2(x[j], x[j + 1]), sc2, less);
+        for (int i = 0; i < 32; i += 2) {
+          const int j = half * 32 + i;
+          const float2 y = fma2(make_float2(x[j], x[j + 1]), sc2, less2);
           float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-          sum[(i >> 1) & 3] = add2(sum[(i >> 1) & 3], e);
+          sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], e);
           if (QUANT && scaled) {
-            const float4 s2 = *reinterpret_cast<const float4 *>(&c.S.tok[QUANT ? mi : 0][j]);
-            e = mul2(e, make_float2(s2.y, s2.w));
-            if (masked) {   // an unseen token stays out whatever its page's scale
-              if (!((seen[j >> 5] >> (j & 31)) & 1u)) e.x = 0.f;
-              if (!((seen[j >> 5] >> ((j & 31) + 1)) & 1u)) e.y = 0.f;
-            }
+            const float4 s2 = *reinterpret_cast<const float4 *>(tok + j);
+            // an unseen token stays out whatever its page's scale
+            e.x = e.x == 0.f ? 0.f : e.x * s2.y;
+            e.y = e.y == 0.f ? 0.f : e.y * s2.w;
           }
           w[i >> 1] = pack_bf16(e.x, e.y);
         }
-        tt_st32(s_at + 32 * half, w);
+        tt_st16(p_at + 16 * half, w);
       }
-      const float2 s01 = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+      const float2 s01 = add2(sum[0], sum[1]);
       l += s01.x + s01.y;
       tt_wait_st();
       tc_fence_before();
-      mbar_arrive(&c.S.p_full[sb]);
+      mbar_arrive(&c.S.p_full[2 * m + b]);
+      if (h == Cfg::STEPS - 1) ++tile;
     }
     // the next item's queries go in before this one's rows are written out
     const TreeItem done = it;
-    const TtRow<D, NM, QUANT, GENERAL> mine = row;
+    const TtRow mine = row;
     const uint32_t noted_at = k & (META_RING - 1);
     ++k;
     more = advance(it);
     if (more) tt_row<D, NM, QUANT, GENERAL>(c, it, m, r, row);
-    if (!wait(&c.S.pv_done[m], (cnt - 1) & 1u)) return;
+    if (!wait(&c.S.pv_done[2 * m + ((cnt - 1) & 1)], ((cnt - 1) >> 1) & 1u)) return;
     tc_fence_after();
-    unsigned long long noted = mine.real ? c.S.nonfinite[noted_at] & mine.bits : 0ull;
-    const long long slot = (2LL * blockIdx.x + (done.t0 > 0 ? 0 : 1)) * Cfg::RB + m * 128 + r;
+    const unsigned long long noted = c.S.nonfinite[noted_at] & mine.bits;
     const bool whole = done.whole();
-    const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-#pragma unroll 1
-    for (int ch = 0; ch < D / 32; ++ch) {
-      float o[32];
-      tt_ld32(o_at + 32 * ch, o);
-      tc_wait_ld();
-      if (noted) {   // values of drafts that the MMA was not shown
-        for (int d = 0; d < 64; ++d) {
-          if (!((noted >> d) & 1ull)) continue;
-          const int j = done.n - done.c + d;
-          const long long cell = static_cast<long long>(done.b) * p.max_pages + j / p.P;
-          const int fmt = p.page_fmt ? p.page_fmt[cell] : p.uniform_fmt;
-          const uint8_t *v = p.v_pool[fmt] +
-                             ((p.page_table[cell] * static_cast<long long>(p.Hkv) + done.g) * p.P + j % p.P) * row_bytes(fmt, D);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float y = fmt == CFR_FMT_BF16
-                                ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(v)[32 * ch + i]) << 16)
-                                : e4m3_at(v[32 * ch + i], 0);
-            if (!(fabsf(y) < INFINITY)) o[i] += y;
-          }
-        }
+    const long long slot = (2LL * blockIdx.x + (done.t0 > 0 ? 0 : 1)) * Cfg::RB + mine.row;
+    const long long to_row = whole ? mine.out_row : slot;
+    // the copies of a row meet at their common maximum
+    float f = 1.f, ref_all = ref, l_all = l;
+    const int copies = NM == 1 ? 128 / mine.width : 1;
+    if (NM == 1) {
+      c.S.join_ml[r] = make_float2(ref, l);
+      if (!meet()) return;
+      for (int i = 0; i < copies; ++i) ref_all = fmaxf(ref_all, c.S.join_ml[mine.row + i * mine.width].x);
+      l_all = 0.f;
+      for (int i = 0; i < copies; ++i) {
+        const float2 o = c.S.join_ml[mine.row + i * mine.width];
+        l_all += ref_all == -INFINITY ? o.y : o.y * exp2_approx(o.x - ref_all);
       }
-      if (mine.real) {
-        if (!whole) {
-          float4 *dst = reinterpret_cast<float4 *>(p.part_acc + slot * D + 32 * ch);
+      f = ref_all == -INFINITY ? 1.f : exp2_approx(ref - ref_all);
+    }
+    if (whole) f = l_all == 0.f ? 0.f : f / l_all;
+    const int share = 16 / copies;   // columns of 16 that a copy's thread puts together
+#pragma unroll 1
+    for (int ch = 0; ch < D / 16; ++ch) {
+      float o[16];
+      tt_ld16(o_at + 16 * ch, o);
+      tc_wait_ld();
+      if (noted && mine.copy == 0) tt_add_back<D>(p, done, noted, 16 * ch, o);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        } else {
-          if (l == 0.f) {
+      for (int i = 0; i < 16; ++i) o[i] = l_all == 0.f ? 0.f : o[i] * f;
+      if (NM == 2) {
+        if (mine.real) tt_put<16>(p, !whole, to_row, 16 * ch, o);
+      } else {
+        float4 *at = reinterpret_cast<float4 *>(c.S.join[r]);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+        for (int i = 0; i < 4; ++i) at[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        if (!meet()) return;
+        const int col = mine.copy * share;
+        for (int half = 0; half < share; half += 4) {
+          float4 t = *reinterpret_cast<const float4 *>(&c.S.join[mine.row][col + half]);
+          for (int i = 1; i < copies; ++i) {
+            const float4 y = *reinterpret_cast<const float4 *>(&c.S.join[mine.row + i * mine.width][col + half]);
+            t = make_float4(t.x + y.x, t.y + y.y, t.z + y.z, t.w + y.w);
           }
-          if (p.out_fmt == CFR_FMT_F32) {
-            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + mine.out_row * D + 32 * ch);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
-          } else {
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + mine.out_row * D + 32 * ch);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                  pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-          }
+          const float v[4] = {t.x, t.y, t.z, t.w};
+          if (mine.real) tt_put<4>(p, !whole, to_row, 16 * ch + col + half, v);
         }
+        if (!meet()) return;
       }
     }
     tc_fence_before();
     mbar_arrive(&c.S.o_free[m]);
-    if (mine.real) {
+    if (mine.real && mine.copy == 0) {
       if (!whole) {
-        p.part_m[slot] = ref;
-        p.part_l[slot] = l;
+        p.part_m[slot] = ref_all;
+        p.part_l[slot] = l_all;
       } else if (p.lse) {
-        p.lse[mine.out_row] = l == 0.f ? -INFINITY : (ref + log2f(l)) / kLog2e;
+        p.lse[mine.out_row] = l_all == 0.f ? -INFINITY : (ref_all + log2f(l_all)) / kLog2e;
       }
     }
   }
@@ -939,7 +1003,7 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_o
 
 template <int D, int NM, bool QUANT>
 constexpr size_t tt_head() {
-  return (sizeof(TtSmem<TtCfg<D, NM, QUANT>::NS, QUANT>) + 1023) / 1024 * 1024;
+  return (sizeof(TtSmem<TtCfg<D, NM, QUANT>::NS, NM, QUANT>) + 1023) / 1024 * 1024;
 }
 template <int D, int NM, bool QUANT>
 constexpr size_t tt_smem() {
@@ -952,7 +1016,7 @@ __global__ void __launch_bounds__((TtCfg<D, NM, QUANT>::THREADS), 1)
     tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap) {
   using Cfg = TtCfg<D, NM, QUANT>;
-  using Smem = TtSmem<Cfg::NS, QUANT>;
+  using Smem = TtSmem<Cfg::NS, NM, QUANT>;
   static_assert(tt_smem<D, NM, QUANT>() <= 227 * 1024, "shared memory of a block");
   extern __shared__ uint8_t raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) / 1024 * 1024);
@@ -966,15 +1030,18 @@ __global__ void __launch_bounds__((TtCfg<D, NM, QUANT>::THREADS), 1)
       mbar_init(&S.slot_empty[i], 2);   // the MMAs' reads, and the repairing or expanding warps
       mbar_init(&S.raw_full[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2 * NM; ++i) {
       mbar_init(&S.s_full[i], 1);
       mbar_init(&S.p_full[i], 128);
       mbar_init(&S.pv_done[i], 1);
+    }
+    for (int i = 0; i < NM; ++i) {
       mbar_init(&S.q_full[i], 128);
       mbar_init(&S.o_free[i], 128);
     }
     for (int i = 0; i < META_RING; ++i) mbar_init(&S.meta_full[i], 1);
     mbar_init(&S.drain, 1);
+    mbar_init(&S.meet, 128);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -993,7 +1060,6 @@ __global__ void __launch_bounds__((TtCfg<D, NM, QUANT>::THREADS), 1)
   bool timed_out = false;
   const int wg = warp >> 2;
   if (wg == 0) {
-    if (Cfg::SPLIT) tt_setmaxnreg<Cfg::SPLIT ? Cfg::REGS_IO : 24>(false);
     if (warp == 0) {
       tt_producer<D, NM, QUANT, 0>(c, cur, &timed_out);
     } else if (warp == 2) {
@@ -1004,10 +1070,8 @@ __global__ void __launch_bounds__((TtCfg<D, NM, QUANT>::THREADS), 1)
       tt_repair<D, NM>(c, cur, &timed_out);
     }
   } else if (wg <= NM) {
-    if (Cfg::SPLIT) tt_setmaxnreg<Cfg::SPLIT ? Cfg::REGS_SOFTMAX : 24>(true);
     tt_softmax<D, NM, QUANT, GENERAL>(c, cur, &timed_out);
   } else if constexpr (QUANT) {
-    tt_setmaxnreg<Cfg::REGS_LOADER>(Cfg::REGS_LOADER > Cfg::REGS_LAUNCH);
     tt_expand<D, NM>(c, cur, &timed_out);
   }
   __syncwarp();
@@ -1023,19 +1087,9 @@ template <int D, int NM, bool QUANT, bool GENERAL>
 cudaError_t launch(const TreeParams &p, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t s) {
   using Cfg = TtCfg<D, NM, QUANT>;
   auto kernel = tree_tc_kernel<D, NM, QUANT, GENERAL>;
-  static bool checked[64];   // per device: the kernel has the registers its split counts on
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(tt_smem<D, NM, QUANT>()));
   if (e != cudaSuccess) return e;
-  if (dev >= 64 || !checked[dev]) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(tt_smem<D, NM, QUANT>()));
-    if (e != cudaSuccess) return e;
-    cudaFuncAttributes a;
-    e = cudaFuncGetAttributes(&a, kernel);
-    if (e != cudaSuccess) return e;
-    if (Cfg::SPLIT && a.numRegs != Cfg::REGS_LAUNCH) return cudaErrorInvalidConfiguration;
-    if (dev < 64) checked[dev] = true;
-  }
   kernel<<<p.grid, Cfg::THREADS, tt_smem<D, NM, QUANT>(), s>>>(p, k, v);
   return cudaGetLastError();
 }
@@ -1054,8 +1108,8 @@ bool tree_tc_supported(const TreeParams &p) {
   return p.pool_pages[CFR_FMT_BF16] * p.Hkv <= 0x7fffffffLL / p.P;   // rows of a tensor map
 }
 
-// Rows of a work item: the rows of one kv head, up to 256.
-int tree_tc_rows(int most_rows) { return most_rows > 128 ? 256 : 128; }
+// Rows of a work item, which chooses the variant: narrow up to 64 rows of a kv head, else wide.
+int tree_tc_rows(int most_rows) { return most_rows > 64 ? 256 : 64; }
 
 cudaError_t launch_tree_tc(const TreeParams &p, int rb, cudaStream_t s) {
   CUtensorMap k, v;
@@ -1071,11 +1125,11 @@ cudaError_t launch_tree_tc(const TreeParams &p, int rb, cudaStream_t s) {
   bool quant = !p.page_fmt && is_quantised(p.uniform_fmt);
   if (p.page_fmt) quant = p.k_pool[CFR_FMT_I8] || p.k_pool[CFR_FMT_I4] || p.k_pool[CFR_FMT_FP8];
   if (p.D == 128) {
-    if (rb == 128)
+    if (rb == 64)
       return quant ? launch_general_or_plain<128, 1, true>(p, k, v, s) : launch_general_or_plain<128, 1, false>(p, k, v, s);
     return quant ? launch_general_or_plain<128, 2, true>(p, k, v, s) : launch_general_or_plain<128, 2, false>(p, k, v, s);
   }
-  if (rb == 128)
+  if (rb == 64)
     return quant ? launch_general_or_plain<64, 1, true>(p, k, v, s) : launch_general_or_plain<64, 1, false>(p, k, v, s);
   return quant ? launch_general_or_plain<64, 2, true>(p, k, v, s) : launch_general_or_plain<64, 2, false>(p, k, v, s);
 }
