@@ -300,15 +300,15 @@ __device__ __forceinline__ Piece tt_fetch(const TreeParams &p, const TreeItem &i
   return x;
 }
 
-// K (KV = 0) or V (KV = 1) of every tile, by one warp.  Page-table entries are
+// K (KV = 0) or V (KV = 1) of every tile, by one warp (one code for both: see the kernel).  Page-table entries are
 // read two tiles ahead and scales one, so that neither is waited for.
 //
 // The description of tile t is kept in place t & 7.  It may be overwritten by
 // tile t + 8 because K's slot of tile t + 8 is free only when the scores of a
 // tile t + 2 or later were issued (a ring has at most 12 slots, 6 tiles), which is after the softmax of
 // tile t handed over its P.
-template <int D, int NM, bool QUANT, int KV>
-__device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_out) {
+template <int D, int NM, bool QUANT>
+__device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_out, const int KV) {
   using Cfg = TtCfg<D, NM, QUANT>;
   const TreeParams &p = c.p;
   const int lane = threadIdx.x & 31;
@@ -427,7 +427,7 @@ __device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_
 // Row i of a V tile before the MMA: zeros where it holds no token; non-finite
 // values of a draft taken out and the draft noted.
 template <int D>
-__device__ __forceinline__ void tt_repair_row(uint8_t *v, int i, bool valid, int draft, unsigned long long *noted) {
+__device__ __noinline__ void tt_repair_row(uint8_t *v, int i, bool valid, int draft, unsigned long long *noted) {
   bool bad = false;
 #pragma unroll 4
   for (int ch = 0; ch < D / 8; ++ch) {
@@ -584,73 +584,90 @@ __device__ void tt_expand(TtCtx<D, NM, true> &c, TreeCursor cur, bool *timed_out
 
 // ---- MMA issue ------------------------------------------------------------------
 
+// The whole warp walks the steps and one lane issues: with control flow and
+// operands the same in every lane, descriptors stay in uniform registers (from a
+// lone lane each MMA took 80 to 100 cycles to issue, for 32 to 64 of tensor time).
 template <int D, int NM, bool QUANT>
 __device__ void tt_issue(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_out) {
   using Cfg = TtCfg<D, NM, QUANT>;
   const TreeParams &p = c.p;
-  const uint32_t tmem = c.S.tmem_base;
-  const uint32_t qa = smem_u32(c.q), sa = smem_u32(c.slots);
+  const auto same = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+  const uint32_t tmem = same(c.S.tmem_base);
+  const uint32_t qa = same(smem_u32(c.q)), sa = same(smem_u32(c.slots));
+  uint32_t lead;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(lead));
   constexpr uint32_t qk_desc = tc_idesc(1, 0, 0, Cfg::STEP), pv_desc = tc_idesc(1, 0, 1, D);
   constexpr int STEP_BYTES = Cfg::STEP * 128;     // of a step's rows in each 64-column half of a slot
   Ring<Cfg::NS> kr, vr;
   vr.step(1);
   uint32_t cnt[2] = {0, 0}, items[2] = {0, 0};    // steps and items of each row tile so far
+  const auto wait = [&](uint64_t *bar, uint32_t par) {
+    mbar_wait(bar, par, p.err, timed_out);
+    return __all_sync(0xffffffffu, !*timed_out) != 0;
+  };
   const auto scores = [&](int m, uint32_t n, int h) {   // S of row tile m's n-th step, from the K slot
     const uint32_t d = tmem + Cfg::s_col(m, n & 1);
     const uint64_t a = tc_sdesc(qa + m * Cfg::ROW_TILE, 16, 1024, 2);
     const uint64_t b = tc_sdesc(sa + kr.s * Cfg::ROW_TILE + h * STEP_BYTES, 16, 1024, 2);
+    if (lead) {
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const uint64_t off = ((k >> 2) * (TT * 128) + (k & 3) * 32) >> 4;
-      tc_mma(d, a + off, b + off, qk_desc, k > 0 ? 1u : 0u);
+      for (int k = 0; k < D / 16; ++k) {
+        const uint64_t off = ((k >> 2) * (TT * 128) + (k & 3) * 32) >> 4;
+        tc_mma(d, a + off, b + off, qk_desc, k > 0 ? 1u : 0u);
+      }
+      tc_commit(&c.S.s_full[2 * m + (n & 1)]);
     }
-    tc_commit(&c.S.s_full[2 * m + (n & 1)]);
   };
+  bool go = true;
   TreeItem it;
-  while (!*timed_out && tree_next<TT, Cfg::RB>(p, cur, it)) {
-    const int ms = NM == 2 && it.rows > 128 ? 2 : 1;
-    const int steps = (it.t1 - it.t0) * Cfg::STEPS;
-    for (int m = 0; m < ms; ++m)
-      if (!mbar_wait(&c.S.q_full[m], items[m] & 1u, p.err, timed_out)) break;
-    if (*timed_out) break;
+  while (go && tree_next<TT, Cfg::RB>(p, cur, it)) {
+    const int ms = NM == 2 && same(it.rows) > 128 ? 2 : 1;
+    const int steps = same((it.t1 - it.t0) * Cfg::STEPS);
+    for (int m = 0; m < ms && go; ++m) go = wait(&c.S.q_full[m], items[m] & 1u);
+    if (!go) break;
     // step -1 only issues the scores of step 0
     for (int s = -1; s < steps; ++s) {
       if (s + 1 < steps) {
         const int h = (s + 1) % Cfg::STEPS;
-        if (h == 0 && !mbar_wait(&c.S.slot_full[kr.s], kr.ph, p.err, timed_out)) break;
+        if (h == 0) go = wait(&c.S.slot_full[kr.s], kr.ph);
+        if (!go) break;
         tc_fence_after();
         for (int m = 0; m < ms; ++m) scores(m, cnt[m] + (s < 0 ? 0 : 1), h);
         if (h == Cfg::STEPS - 1) {
-          tc_commit(&c.S.slot_empty[kr.s]);
+          if (lead) tc_commit(&c.S.slot_empty[kr.s]);
           kr.step(2);
         }
       }
       if (s < 0) continue;
       const int h = s % Cfg::STEPS;
-      if (h == 0 && !mbar_wait(&c.S.slot_full[vr.s], vr.ph, p.err, timed_out)) break;
+      if (h == 0) go = wait(&c.S.slot_full[vr.s], vr.ph);
+      if (!go) break;
       for (int m = 0; m < ms; ++m) {
         const int b = cnt[m] & 1;
-        if (s == 0 && !mbar_wait(&c.S.o_free[m], (items[m] & 1u) ^ 1u, p.err, timed_out)) break;
-        if (!mbar_wait(&c.S.p_full[2 * m + b], (cnt[m] >> 1) & 1u, p.err, timed_out)) break;
+        if (s == 0) go = wait(&c.S.o_free[m], (items[m] & 1u) ^ 1u);
+        if (go) go = wait(&c.S.p_full[2 * m + b], (cnt[m] >> 1) & 1u);
+        if (!go) break;
         tc_fence_after();
         const uint32_t d = tmem + Cfg::O_COL + m * 128, a = tmem + Cfg::p_col(m, b);
         const uint64_t v = tc_sdesc(sa + vr.s * Cfg::ROW_TILE + h * STEP_BYTES, TT * 128, 1024, 2);
+        if (lead) {
 #pragma unroll
-        for (int k = 0; k < Cfg::STEP / 16; ++k)
-          tt_mma_ts(d, a + k * 8, v + static_cast<uint64_t>(k * 2048 >> 4), pv_desc, s > 0 || k > 0 ? 1u : 0u);
-        tc_commit(&c.S.pv_done[2 * m + b]);
+          for (int k = 0; k < Cfg::STEP / 16; ++k)
+            tt_mma_ts(d, a + k * 8, v + static_cast<uint64_t>(k * 2048 >> 4), pv_desc, s > 0 || k > 0 ? 1u : 0u);
+          tc_commit(&c.S.pv_done[2 * m + b]);
+        }
         ++cnt[m];
       }
-      if (*timed_out) break;
+      if (!go) break;
       if (h == Cfg::STEPS - 1) {
-        tc_commit(&c.S.slot_empty[vr.s]);
+        if (lead) tc_commit(&c.S.slot_empty[vr.s]);
         vr.step(2);
       }
     }
     for (int m = 0; m < ms; ++m) ++items[m];
   }
   // nothing of the tensor cores may be in flight when TMEM is freed
-  tc_commit(&c.S.drain);
+  if (lead) tc_commit(&c.S.drain);
   bool late = false;
   mbar_wait(&c.S.drain, 0, p.err, &late);
 }
@@ -743,6 +760,42 @@ __device__ __forceinline__ void tt_put(const TreeParams &p, bool part, long long
   }
 }
 
+// cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)), in units of log2 e; k1 takes x to 2 s / cap
+// in those units, c2 = cap log2 e
+__device__ __forceinline__ float tt_cap(float x, float k1, float c2) {
+  return fmaf(-2.f * c2, rcp_approx(1.f + exp2_approx(x * k1)), c2);
+}
+
+// Finishes, in TMEM, the scores of a step that has tokens which a row does not see.  Out
+// of line and rolled: the roles of the kernel share the SM's instruction cache, and
+// with these paths inside the loop its hit rate fell to 76 % and fetching
+// instructions bound the kernel (a step took 2.5 times as long).
+template <bool GENERAL>
+__device__ __noinline__ void tt_masked(const TreeParams &p, uint32_t s_at, int width, unsigned long long seen,
+                                       const float2 *tok, float scale, float slope, int pos, int pre, int off, int c, int b) {
+  const float k1 = 2.f / p.cap, c2 = p.cap * kLog2e;
+#pragma unroll 1
+  for (int ch = 0; ch < width; ch += 16) {
+    float x[16];
+    tt_ld16(s_at + ch, x);
+    tc_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int d = ch + i - off;   // draft
+      float y = x[i] * (tok ? tok[ch + i].x * scale : scale);
+      if (GENERAL && p.cap > 0.f) y = tt_cap(y, k1, c2);
+      if (GENERAL && p.slopes) {
+        int far = pre + d - pos;
+        if (d >= 0 && d < c && p.depths) far = pre + p.depths[static_cast<long long>(b) * p.nq + d] - pos;
+        y = fmaf(slope, static_cast<float>(far), y);
+      }
+      x[i] = (seen >> (ch + i)) & 1ull ? y : -INFINITY;
+    }
+    tt_st16(s_at + ch, reinterpret_cast<const uint32_t *>(x));
+  }
+  tt_wait_st();
+}
+
 template <int D, int NM, bool QUANT, bool GENERAL>
 __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_out) {
   using Cfg = TtCfg<D, NM, QUANT>;
@@ -775,16 +828,91 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_o
     }
     return false;
   };
-  TreeItem it;
-  TtRow row;
-  bool more = advance(it);
-  if (more) tt_row<D, NM, QUANT, GENERAL>(c, it, m, r, row);
-  while (more) {
+  TreeItem it, next;
+  TtRow row{}, next_row{};
+  float ref = -INFINITY, l = 0.f;
+  bool open = false;                   // an item whose rows are not written out yet
+  uint32_t item_of = 0;                // its number
+  // joins the copies and writes an item's rows, or its partials
+  const auto finish = [&]() {
+    if (!wait(&c.S.pv_done[2 * m + ((cnt - 1) & 1)], ((cnt - 1) >> 1) & 1u)) return false;
+    tc_fence_after();
+    const unsigned long long noted = c.S.nonfinite[item_of & (META_RING - 1)] & row.bits;
+    const bool whole = it.whole();
+    const long long slot = (2LL * blockIdx.x + (it.t0 > 0 ? 0 : 1)) * Cfg::RB + row.row;
+    const long long to_row = whole ? row.out_row : slot;
+    // the copies of a row meet at their common maximum
+    float f = 1.f, ref_all = ref, l_all = l;
+    const int copies = NM == 1 ? 128 / row.width : 1;
+    if (NM == 1) {
+      c.S.join_ml[r] = make_float2(ref, l);
+      if (!meet()) return false;
+      for (int i = 0; i < copies; ++i) ref_all = fmaxf(ref_all, c.S.join_ml[row.row + i * row.width].x);
+      l_all = 0.f;
+      for (int i = 0; i < copies; ++i) {
+        const float2 o = c.S.join_ml[row.row + i * row.width];
+        l_all += ref_all == -INFINITY ? o.y : o.y * exp2_approx(o.x - ref_all);
+      }
+      f = ref_all == -INFINITY ? 1.f : exp2_approx(ref - ref_all);
+    }
+    if (whole) f = l_all == 0.f ? 0.f : f / l_all;
+    const int share = 16 / copies;   // columns of 16 that a copy's thread puts together
+#pragma unroll 1
+    for (int ch = 0; ch < D / 16; ++ch) {
+      float o[16];
+      tt_ld16(o_at + 16 * ch, o);
+      tc_wait_ld();
+      if (noted && row.copy == 0) tt_add_back<D>(p, it, noted, 16 * ch, o);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] = l_all == 0.f ? 0.f : o[i] * f;
+      if (NM == 2) {
+        if (row.real) tt_put<16>(p, !whole, to_row, 16 * ch, o);
+      } else {
+        float4 *at = reinterpret_cast<float4 *>(c.S.join[r]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        if (!meet()) return false;
+        const int col = row.copy * share;
+        for (int half = 0; half < share; half += 4) {
+          float4 t = *reinterpret_cast<const float4 *>(&c.S.join[row.row][col + half]);
+          for (int i = 1; i < copies; ++i) {
+            const float4 y = *reinterpret_cast<const float4 *>(&c.S.join[row.row + i * row.width][col + half]);
+            t = make_float4(t.x + y.x, t.y + y.y, t.z + y.z, t.w + y.w);
+          }
+          const float v[4] = {t.x, t.y, t.z, t.w};
+          if (row.real) tt_put<4>(p, !whole, to_row, 16 * ch + col + half, v);
+        }
+        if (!meet()) return false;
+      }
+    }
+    tc_fence_before();
+    mbar_arrive(&c.S.o_free[m]);
+    if (row.real && row.copy == 0) {
+      if (!whole) {
+        p.part_m[slot] = ref_all;
+        p.part_l[slot] = l_all;
+      } else if (p.lse) {
+        p.lse[row.out_row] = l_all == 0.f ? -INFINITY : (ref_all + log2f(l_all)) / kLog2e;
+      }
+    }
+    return true;
+  };
+  for (;;) {
+    // the next item's queries go in before the last one's rows are written out
+    const bool more = advance(next);
+    if (more) tt_row<D, NM, QUANT, GENERAL>(c, next, m, r, next_row);
+    if (open && !finish()) return;
+    if (!more) return;
+    it = next;
+    row = next_row;
+    item_of = k++;
+    open = true;
     const int pre = it.n - it.c;
     const int first = row.copy * row.width;   // the copy's first token of a step
     const bool wide = NM == 2 || row.width == 64;
     const bool idle = !__any_sync(0xffffffffu, row.real);
-    float ref = -INFINITY, l = 0.f;
+    ref = -INFINITY;
+    l = 0.f;
     if (NM == 1 && zeroed != row.width) {
       const uint32_t z[16] = {};
 #pragma unroll 1
@@ -807,10 +935,7 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_o
         if (h == Cfg::STEPS - 1) ++tile;
         continue;
       }
-      float x[64];
       const uint32_t s_at = lanes + Cfg::s_col(m, b) + first;
-      tt_ld32(s_at, x);
-      if (wide) tt_ld32(s_at + 32, x + 32);
       const int in_tile = h * Cfg::STEP + first;                // the copy's first token in the tile
       const int off = pre - ((it.t0 + s / Cfg::STEPS) * TT + in_tile);  // its tokens before the drafts
       unsigned long long seen = c.S.valid[mi][in_tile >> 5];
@@ -818,12 +943,22 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_o
       const bool masked = off < row.width || seen != (wide ? ~0ull : 0xFFFFFFFFull);
       const bool scaled = QUANT && c.S.meta[QUANT ? mi : 0].scaled;
       const float2 *tok = &c.S.tok[QUANT ? mi : 0][QUANT ? in_tile : 0];
-      tc_wait_ld();
       // Scores as they enter the exponential, in units of log2 e: times the softmax scale
-      // (left to the exponential where nothing else is to be done), the pages' scales, capped, less the
-      // distance, -inf where the row does not see the token.
+      // (left to the exponential where nothing else is to be done), the pages' scales,
+      // capped, less the distance, -inf where the row does not see the token.  Steps with
+      // unseen tokens, one or two of an item, are finished out of line.
       float sc = scale;
-      if (QUANT && scaled) {
+      if (masked) {
+        // tokens before the drafts, and the drafts of the row's bits
+        seen &= off >= 64 ? ~0ull : off > 0 ? (row.bits << off) | ((1ull << off) - 1ull) : off > -64 ? row.bits >> -off : 0ull;
+        tt_masked<GENERAL>(p, s_at, row.width, seen, scaled ? tok : nullptr, scale, row.slope, row.pos, pre, off, it.c, it.b);
+        sc = 1.f;
+      }
+      float x[64];
+      tt_ld32(s_at, x);
+      if (wide) tt_ld32(s_at + 32, x + 32);
+      tc_wait_ld();
+      if (QUANT && scaled && !masked) {
 #pragma unroll
         for (int i = 0; i < 64; i += 2) {
           if (i == 32 && !wide) break;
@@ -834,39 +969,23 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_o
         }
         sc = 1.f;
       }
-      if (GENERAL && p.cap > 0.f) {
-        // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap))
+      if (GENERAL && p.cap > 0.f && !masked) {
         const float k1 = (QUANT && scaled ? 1.f : scale) * 2.f / p.cap, c2 = p.cap * kLog2e;
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
           if (i == 32 && !wide) break;
-          x[i] = fmaf(-2.f * c2, rcp_approx(1.f + exp2_approx(x[i] * k1)), c2);
+          x[i] = tt_cap(x[i], k1, c2);
         }
         sc = 1.f;
       }
-      if (GENERAL && p.slopes) {
+      if (GENERAL && p.slopes && !masked) {
         const float base = row.slope * static_cast<float>(pre - off - row.pos);
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
           if (i == 32 && !wide) break;
           x[i] = fmaf(x[i], sc, fmaf(row.slope, static_cast<float>(i), base));
         }
-        if (masked && p.depths) {   // a draft stands at its depth
-#pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            const int d = i - off;
-            if (d >= 0 && d < it.c)
-              x[i] = fmaf(row.slope, static_cast<float>(p.depths[static_cast<long long>(it.b) * p.nq + d] - d), x[i]);
-          }
-        }
         sc = 1.f;
-      }
-      if (masked) {
-        // tokens before the drafts, and the drafts of the row's bits
-        seen &= off >= 64 ? ~0ull : off > 0 ? (row.bits << off) | ((1ull << off) - 1ull) : off > -64 ? row.bits >> -off : 0ull;
-#pragma unroll
-        for (int i = 0; i < 64; ++i)
-          if (!((seen >> i) & 1ull)) x[i] = -INFINITY;
       }
       float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -928,73 +1047,6 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_o
       tc_fence_before();
       mbar_arrive(&c.S.p_full[2 * m + b]);
       if (h == Cfg::STEPS - 1) ++tile;
-    }
-    // the next item's queries go in before this one's rows are written out
-    const TreeItem done = it;
-    const TtRow mine = row;
-    const uint32_t noted_at = k & (META_RING - 1);
-    ++k;
-    more = advance(it);
-    if (more) tt_row<D, NM, QUANT, GENERAL>(c, it, m, r, row);
-    if (!wait(&c.S.pv_done[2 * m + ((cnt - 1) & 1)], ((cnt - 1) >> 1) & 1u)) return;
-    tc_fence_after();
-    const unsigned long long noted = c.S.nonfinite[noted_at] & mine.bits;
-    const bool whole = done.whole();
-    const long long slot = (2LL * blockIdx.x + (done.t0 > 0 ? 0 : 1)) * Cfg::RB + mine.row;
-    const long long to_row = whole ? mine.out_row : slot;
-    // the copies of a row meet at their common maximum
-    float f = 1.f, ref_all = ref, l_all = l;
-    const int copies = NM == 1 ? 128 / mine.width : 1;
-    if (NM == 1) {
-      c.S.join_ml[r] = make_float2(ref, l);
-      if (!meet()) return;
-      for (int i = 0; i < copies; ++i) ref_all = fmaxf(ref_all, c.S.join_ml[mine.row + i * mine.width].x);
-      l_all = 0.f;
-      for (int i = 0; i < copies; ++i) {
-        const float2 o = c.S.join_ml[mine.row + i * mine.width];
-        l_all += ref_all == -INFINITY ? o.y : o.y * exp2_approx(o.x - ref_all);
-      }
-      f = ref_all == -INFINITY ? 1.f : exp2_approx(ref - ref_all);
-    }
-    if (whole) f = l_all == 0.f ? 0.f : f / l_all;
-    const int share = 16 / copies;   // columns of 16 that a copy's thread puts together
-#pragma unroll 1
-    for (int ch = 0; ch < D / 16; ++ch) {
-      float o[16];
-      tt_ld16(o_at + 16 * ch, o);
-      tc_wait_ld();
-      if (noted && mine.copy == 0) tt_add_back<D>(p, done, noted, 16 * ch, o);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[i] = l_all == 0.f ? 0.f : o[i] * f;
-      if (NM == 2) {
-        if (mine.real) tt_put<16>(p, !whole, to_row, 16 * ch, o);
-      } else {
-        float4 *at = reinterpret_cast<float4 *>(c.S.join[r]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) at[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        if (!meet()) return;
-        const int col = mine.copy * share;
-        for (int half = 0; half < share; half += 4) {
-          float4 t = *reinterpret_cast<const float4 *>(&c.S.join[mine.row][col + half]);
-          for (int i = 1; i < copies; ++i) {
-            const float4 y = *reinterpret_cast<const float4 *>(&c.S.join[mine.row + i * mine.width][col + half]);
-            t = make_float4(t.x + y.x, t.y + y.y, t.z + y.z, t.w + y.w);
-          }
-          const float v[4] = {t.x, t.y, t.z, t.w};
-          if (mine.real) tt_put<4>(p, !whole, to_row, 16 * ch + col + half, v);
-        }
-        if (!meet()) return;
-      }
-    }
-    tc_fence_before();
-    mbar_arrive(&c.S.o_free[m]);
-    if (mine.real && mine.copy == 0) {
-      if (!whole) {
-        p.part_m[slot] = ref_all;
-        p.part_l[slot] = l_all;
-      } else if (p.lse) {
-        p.lse[mine.out_row] = l_all == 0.f ? -INFINITY : (ref_all + log2f(l_all)) / kLog2e;
-      }
     }
   }
 }
@@ -1060,12 +1112,10 @@ __global__ void __launch_bounds__((TtCfg<D, NM, QUANT>::THREADS), 1)
   bool timed_out = false;
   const int wg = warp >> 2;
   if (wg == 0) {
-    if (warp == 0) {
-      tt_producer<D, NM, QUANT, 0>(c, cur, &timed_out);
-    } else if (warp == 2) {
-      tt_producer<D, NM, QUANT, 1>(c, cur, &timed_out);
+    if (warp == 0 || warp == 2) {
+      tt_producer<D, NM, QUANT>(c, cur, &timed_out, warp >> 1);
     } else if (warp == 1) {
-      if ((threadIdx.x & 31) == 0) tt_issue<D, NM, QUANT>(c, cur, &timed_out);
+      tt_issue<D, NM, QUANT>(c, cur, &timed_out);
     } else if constexpr (!QUANT) {
       tt_repair<D, NM>(c, cur, &timed_out);
     }
