@@ -50,6 +50,7 @@
 #include <cuda_bf16.h>
 
 #include <cstring>
+#include <type_traits>
 
 #include "cfr_cells.cuh"
 #include "cfr_tc.cuh"
@@ -86,7 +87,7 @@ struct TtCfg {
 
 struct TtMeta {
   uint32_t valid[4];          // tokens of the tile that take part
-  int tin0, scaled;           // row of the first token in its page; any quantised page
+  int tin0, scaled;           // row of the first token in its page; bit 0: quantised pages, bit 1: int4 pages
   uint8_t fmt[MAX_PIECES + 3];
   float ks[MAX_PIECES], vs[MAX_PIECES];
 };
@@ -106,7 +107,8 @@ struct TtSmem {
   TreeScratch scratch;
   TtMeta meta[QUANT ? META_RING : 1];
   uint32_t valid[META_RING][4];
-  alignas(16) float2 tok[QUANT ? META_RING : 1][QUANT ? TT : 2];  // K and V scale of each token
+  // K scale (times softmax scale and log2 e) and V scale of each token
+  alignas(16) float ks[QUANT ? META_RING : 1][QUANT ? TT : 4], vs[QUANT ? META_RING : 1][QUANT ? TT : 4];
   // joining of the copies (narrow): 16 columns of O of every row, its maximum and sum
   alignas(16) float join[NM == 1 ? 128 : 1][20];
   float2 join_ml[NM == 1 ? 128 : 1];
@@ -266,6 +268,25 @@ struct TtCtx {
   __device__ __forceinline__ uint8_t *slot(int s) const { return slots + s * Cfg::ROW_TILE; }
 };
 
+// mbar_wait with its loop out of line, once for all roles
+__device__ __noinline__ bool tt_wait_long(uint64_t *bar, uint32_t parity, uint32_t *err) {
+  bool timed_out = false;
+  return mbar_wait(bar, parity, err, &timed_out);
+}
+__device__ __forceinline__ bool tt_wait(uint64_t *bar, uint32_t parity, uint32_t *err, bool *timed_out) {
+  if (*timed_out) return false;
+  if (mbar_try_wait(bar, parity)) return true;
+  if (tt_wait_long(bar, parity, err)) return true;
+  *timed_out = true;
+  return false;
+}
+
+// tree_next out of line, once for all roles
+template <int RB>
+__device__ __noinline__ bool tt_next_item(const TreeParams &p, TreeCursor &cur, TreeItem &it) {
+  return tree_next<TT, RB>(p, cur, it);
+}
+
 // place in the ring of slots
 template <int NS>
 struct Ring {
@@ -317,8 +338,9 @@ __device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_
   uint32_t raw_mask = 0, used = 0;   // slots filled through raw_full; slots filled at all
   uint32_t phase_of = 0;             // the phase each was filled in
   uint32_t tile = 0;
-  TreeItem it;
-  while (!*timed_out && tree_next<TT, Cfg::RB>(p, cur, it)) {
+  TreeItem item;
+  while (!*timed_out && tt_next_item<Cfg::RB>(p, cur, item)) {
+    const TreeItem it = item;
     if (KV == 0 && lane == 0 && it.bad) set_err(p.err, CFR_DEVERR_SEQ_LEN);
     const int pre = it.n - it.c;
     Piece now = tt_fetch(p, it, it.t0, lane), next = tt_fetch(p, it, it.t0 + 1, lane);
@@ -336,19 +358,12 @@ __device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_
         if (!ok && KV == 0)
           set_err(p.err, !known ? CFR_DEVERR_PAGE_FMT : !pool ? CFR_DEVERR_POOL : CFR_DEVERR_PAGE_ID);
       }
-      const uint32_t okb = __ballot_sync(0xffffffffu, ok);
       const bool quant = QUANT && ok && is_quantised(fmt);
       const bool any_quant = QUANT && __any_sync(0xffffffffu, quant);
+      const bool any4 = QUANT && __any_sync(0xffffffffu, quant && fmt == CFR_FMT_I4);
       float2 sc = make_float2(1.f, 1.f);
       if (QUANT && KV == 0 && quant)
         sc = *reinterpret_cast<const float2 *>(p.scales[fmt] + (now.id * p.Hkv + it.g) * 2);
-      // tokens of valid pages, 32 a ballot
-      uint32_t valid[4];
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const int row = 32 * w + lane;
-        valid[w] = __ballot_sync(0xffffffffu, row < rows && ((okb >> ((tin0 + row) / p.P)) & 1u));
-      }
       // this lane's page: tile rows [a, z)
       const int a = lane == 0 ? 0 : min(rows, lane * p.P - tin0);
       const int z = min(rows, (lane + 1) * p.P - tin0);
@@ -356,10 +371,18 @@ __device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_
       const uint32_t mine = !ok ? 0u : quant ? static_cast<uint32_t>((z - a) * row_bytes(fmt, D))
                                              : static_cast<uint32_t>(boxes * c.box * D * 2);
       const uint32_t bytes = __reduce_add_sync(0xffffffffu, mine);
-      const bool full = (valid[0] & valid[1] & valid[2] & valid[3]) == 0xFFFFFFFFu;
+      // tokens of valid pages: lane w holds those of 32 w on
+      uint32_t valid = 0;
+#pragma unroll 1
+      for (int w = 0; w < 4; ++w) {
+        const int lo = max(a - 32 * w, 0), hi = min(z - 32 * w, 32);
+        const uint32_t any = __reduce_or_sync(0xffffffffu, ok && lo < hi ? (0xFFFFFFFFu >> (32 - (hi - lo))) << lo : 0u);
+        if (lane == w) valid = any;
+      }
+      const bool full = __all_sync(0xffffffffu, lane >= 4 || valid == 0xFFFFFFFFu);
       const bool direct = !any_quant && (KV == 0 || (full && j0 + TT <= pre));
       int go = 1;
-      if (lane == 0) go = mbar_wait(&c.S.slot_empty[r.s], r.ph ^ 1u, p.err, timed_out) ? 1 : 0;
+      if (lane == 0) go = tt_wait(&c.S.slot_empty[r.s], r.ph ^ 1u, p.err, timed_out) ? 1 : 0;
       if (!__shfl_sync(0xffffffffu, go, 0)) {
         *timed_out = true;
         break;
@@ -371,11 +394,11 @@ __device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_
         c.S.meta[mi].ks[lane] = sc.x;
         c.S.meta[mi].vs[lane] = sc.y;
       }
-      if (lane < 4) (KV == 0 ? c.S.valid : c.S.v_valid)[mi][lane] = lane == 0 ? valid[0] : lane == 1 ? valid[1] : lane == 2 ? valid[2] : valid[3];
+      if (lane < 4) (KV == 0 ? c.S.valid : c.S.v_valid)[mi][lane] = valid;
       if (lane == 0) {
         if (QUANT && KV == 0) {
           c.S.meta[mi].tin0 = tin0;
-          c.S.meta[mi].scaled = any_quant;
+          c.S.meta[mi].scaled = any_quant ? (any4 ? 3 : 1) : 0;
         }
         c.S.direct[r.s] = direct;
       }
@@ -397,7 +420,8 @@ __device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_
         if (quant) {
           const int rb = row_bytes(fmt, D);
           const uint8_t *pool = KV ? p.v_pool[fmt] : p.k_pool[fmt];
-          bulk_g2s(dst, pool + ((now.id * p.Hkv + it.g) * p.P + in_page) * rb, mine, done);
+          // (places: see tt_expand)
+          bulk_g2s(D == 128 && fmt == CFR_FMT_I4 ? dst + TT * 128 : dst, pool + ((now.id * p.Hkv + it.g) * p.P + in_page) * rb, mine, done);
         } else {
           const int y = static_cast<int>((now.id * p.Hkv + it.g) * p.P + in_page);
           for (int x = 0; x < boxes; ++x)
@@ -417,7 +441,7 @@ __device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_
     for (int s = 0; s < Cfg::NS; ++s) {
       bool late = false;
       if ((used >> s) & 1u)
-        mbar_wait((raw_mask >> s) & 1u ? &c.S.raw_full[s] : &c.S.slot_full[s], (phase_of >> s) & 1u, p.err, &late);
+        tt_wait((raw_mask >> s) & 1u ? &c.S.raw_full[s] : &c.S.slot_full[s], (phase_of >> s) & 1u, p.err, &late);
     }
   }
 }
@@ -454,14 +478,15 @@ __device__ void tt_repair(TtCtx<D, NM, false> &c, TreeCursor cur, bool *timed_ou
   const int lane = threadIdx.x & 31;
   Ring<Cfg::NS> r;
   uint32_t tile = 0, k = 0;
-  TreeItem it;
-  for (; !*timed_out && tree_next<TT, Cfg::RB>(p, cur, it); ++k) {
+  TreeItem item;
+  for (; !*timed_out && tt_next_item<Cfg::RB>(p, cur, item); ++k) {
+    const TreeItem it = item;
     const int pre = it.n - it.c;
     if (lane == 0) c.S.nonfinite[k & (META_RING - 1)] = 0ull;
     __syncwarp();
     for (int t2 = 2 * it.t0; t2 < 2 * it.t1; ++t2) {
       int go = 1;
-      if (lane == 0) go = mbar_wait(&c.S.raw_full[r.s], r.ph, p.err, timed_out) ? 1 : 0;
+      if (lane == 0) go = tt_wait(&c.S.raw_full[r.s], r.ph, p.err, timed_out) ? 1 : 0;
       if (!__shfl_sync(0xffffffffu, go, 0)) {
         *timed_out = true;
         break;
@@ -494,11 +519,11 @@ __device__ void tt_expand(TtCtx<D, NM, true> &c, TreeCursor cur, bool *timed_out
   using Cfg = TtCfg<D, NM, true>;
   const TreeParams &p = c.p;
   const int i = threadIdx.x - Cfg::LOADER_T0;
-  constexpr int C8 = D / 16, C4 = D / 32;   // 16-byte pieces of an 8-bit and a 4-bit row
   Ring<Cfg::NS> r;
   uint32_t tile = 0, k = 0;
-  TreeItem it;
-  for (; tree_next<TT, Cfg::RB>(p, cur, it); ++k) {
+  TreeItem item;
+  for (; tt_next_item<Cfg::RB>(p, cur, item); ++k) {
+    const TreeItem it = item;
     const int pre = it.n - it.c;
     if (i == 0) c.S.nonfinite[k & (META_RING - 1)] = 0ull;
     for (int t = it.t0; t < it.t1; ++t, ++tile) {
@@ -508,7 +533,7 @@ __device__ void tt_expand(TtCtx<D, NM, true> &c, TreeCursor cur, bool *timed_out
       bool valid = false;
       for (int kv = 0; kv < 2; ++kv) {
         // one thread waits, the barrier hands on its outcome
-        if (i == 0) c.S.flag[r.s] = mbar_wait(&c.S.raw_full[r.s], r.ph, p.err, timed_out) ? 1 : 0;
+        if (i == 0) c.S.flag[r.s] = tt_wait(&c.S.raw_full[r.s], r.ph, p.err, timed_out) ? 1 : 0;
         named_sync(1, 128);
         if (!c.S.flag[r.s]) {
           *timed_out = true;
@@ -516,58 +541,87 @@ __device__ void tt_expand(TtCtx<D, NM, true> &c, TreeCursor cur, bool *timed_out
         }
         (void)mbar_try_wait(&c.S.raw_full[r.s], r.ph);
         const bool direct = c.S.direct[r.s];
+        const bool any4 = m.scaled & 2;   // 4-bit rows among the tile's
         if (kv == 0) {
           valid = (c.S.valid[mi][i >> 5] >> (i & 31)) & 1u;
           const int pc = (m.tin0 + i) / p.P;
           fmt = valid ? m.fmt[pc] : 255;
           a = pc == 0 ? 0 : pc * p.P - m.tin0;
-          c.S.tok[mi][i] = valid ? make_float2(m.ks[pc], m.vs[pc]) : make_float2(0.f, 0.f);
+          c.S.ks[mi][i] = valid ? m.ks[pc] * (p.sigma * kLog2e) : 0.f;
+          c.S.vs[mi][i] = valid ? m.vs[pc] : 0.f;
         }
         if (!direct) {
           uint8_t *op = c.slot(r.s);
           const bool eight = fmt == CFR_FMT_I8 || fmt == CFR_FMT_FP8, four = fmt == CFR_FMT_I4;
-          uint4 raw[C8];
-          // rows are read in an order that spreads a warp's lanes over the banks
-          if (eight) {
-            const uint8_t *src = op + a * 128 + (i - a) * D;
-#pragma unroll
-            for (int x = 0; x < C8; ++x) raw[x] = *reinterpret_cast<const uint4 *>(src + 16 * ((x + (D == 128 ? i : i >> 1)) & (C8 - 1)));
-          } else if (four) {
-            const uint8_t *src = op + a * 128 + (i - a) * (D / 2);
-#pragma unroll
-            for (int x = 0; x < C4; ++x) raw[x] = *reinterpret_cast<const uint4 *>(src + 16 * ((x + (D == 128 ? i >> 1 : i >> 2)) & (C4 - 1)));
-          }
-          named_sync(1, 128);  // every row is in registers before any is written
           const int draft = t * TT + i - pre;
-          bool bad = false;
-          if (eight) {
+          const bool look = kv == 1 && fmt == CFR_FMT_FP8 && draft >= 0;   // E4M3 has NaN
+          // 64 values at a time (a row of one half of the slot), so that the code stays small;
+          // rows are read in an order that spreads a warp's lanes over the banks
+          const auto put8 = [&](const uint4 (&raw)[4], int hh) {
 #pragma unroll
-            for (int x = 0; x < C8; ++x) {
-              const int ci = (x + (D == 128 ? i : i >> 1)) & (C8 - 1);
+            for (int x = 0; x < 4; ++x) {
+              const int ci = (x + i) & 3;   // codes 16 ci .. of the 64
               uint32_t o[8];
               expand16<8>(fmt, raw[x], o);
-              uint4 u = make_uint4(o[0], o[1], o[2], o[3]), v = make_uint4(o[4], o[5], o[6], o[7]);
-              if (kv == 1 && fmt == CFR_FMT_FP8 && draft >= 0) bad = repair16(u) | repair16(v) | bad;
-              uint8_t *hb = op + (ci >> 2) * (TT * 128);
-              *reinterpret_cast<uint4 *>(hb + sw128(i, (2 * ci) & 7)) = u;
-              *reinterpret_cast<uint4 *>(hb + sw128(i, (2 * ci + 1) & 7)) = v;
+              const uint4 u = make_uint4(o[0], o[1], o[2], o[3]), v = make_uint4(o[4], o[5], o[6], o[7]);
+              uint8_t *hb = op + hh * (TT * 128);
+              *reinterpret_cast<uint4 *>(hb + sw128(i, 2 * ci)) = u;
+              *reinterpret_cast<uint4 *>(hb + sw128(i, 2 * ci + 1)) = v;
             }
-          } else if (four) {
+          };
+          const auto put4 = [&](const uint4 (&raw)[2], int hh) {
 #pragma unroll
-            for (int x = 0; x < C4; ++x) {
-              const int ci = (x + (D == 128 ? i >> 1 : i >> 2)) & (C4 - 1);
+            for (int x = 0; x < 2; ++x) {
+              const int ci = (x + (i >> 1)) & 1;   // codes 32 ci .. of the 64
               uint32_t o[16];
               expand16<16>(fmt, raw[x], o);
-              uint8_t *hb = op + (ci >> 1) * (TT * 128);
+              uint8_t *hb = op + hh * (TT * 128);
 #pragma unroll
               for (int y = 0; y < 4; ++y)
-                *reinterpret_cast<uint4 *>(hb + sw128(i, (4 * ci + y) & 7)) =
+                *reinterpret_cast<uint4 *>(hb + sw128(i, 4 * ci + y)) =
                     make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
             }
-          } else if (kv == 1 && (!valid || draft >= 0)) {
-            tt_repair_row<D>(op, i, valid, draft, &c.S.nonfinite[k & (META_RING - 1)]);
+          };
+          if (D == 128) {
+            // 8-bit rows lie where the row's first half goes, so each thread overwrites its own; 4-bit rows
+            // lie in the second half's place of their page's rows, which is written once all were read
+            uint4 raw4[2];
+            if (eight) {
+#pragma unroll 1
+              for (int hh = 1; hh >= 0; --hh) {
+                uint4 raw[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  raw[x] = *reinterpret_cast<const uint4 *>(op + i * 128 + hh * 64 + 16 * ((x + i) & 3));
+                put8(raw, hh);
+              }
+            }
+            const uint8_t *src = op + TT * 128 + a * 128 + (i - a) * 64;
+#pragma unroll 1
+            for (int hh = 0; hh < 2; ++hh) {
+              if (four)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                  raw4[x] = *reinterpret_cast<const uint4 *>(src + hh * 32 + 16 * ((x + (i >> 1)) & 1));
+              if (hh == 1 && any4) named_sync(1, 128);
+              if (four) put4(raw4, hh);
+            }
+          } else {
+            uint4 raw[4], raw4[2];
+            const uint8_t *src = op + a * 128 + (i - a) * row_bytes(eight ? CFR_FMT_I8 : CFR_FMT_I4, D);
+            if (eight) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) raw[x] = *reinterpret_cast<const uint4 *>(src + 16 * ((x + i) & 3));
+            } else if (four) {
+#pragma unroll
+              for (int x = 0; x < 2; ++x) raw4[x] = *reinterpret_cast<const uint4 *>(src + 16 * ((x + (i >> 1)) & 1));
+            }
+            named_sync(1, 128);  // every row is in registers before any is written
+            if (eight) put8(raw, 0);
+            if (four) put4(raw4, 0);
           }
-          if (bad) atomicOr(&c.S.nonfinite[k & (META_RING - 1)], 1ull << draft);
+          if (kv == 1 && (eight || four ? look : !valid || draft >= 0))
+            tt_repair_row<D>(op, i, valid, draft, &c.S.nonfinite[k & (META_RING - 1)]);
           fence_async_smem();
         }
         named_sync(1, 128);
@@ -602,7 +656,7 @@ __device__ void tt_issue(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_out
   vr.step(1);
   uint32_t cnt[2] = {0, 0}, items[2] = {0, 0};    // steps and items of each row tile so far
   const auto wait = [&](uint64_t *bar, uint32_t par) {
-    mbar_wait(bar, par, p.err, timed_out);
+    tt_wait(bar, par, p.err, timed_out);
     return __all_sync(0xffffffffu, !*timed_out) != 0;
   };
   const auto scores = [&](int m, uint32_t n, int h) {   // S of row tile m's n-th step, from the K slot
@@ -619,8 +673,9 @@ __device__ void tt_issue(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_out
     }
   };
   bool go = true;
-  TreeItem it;
-  while (go && tree_next<TT, Cfg::RB>(p, cur, it)) {
+  TreeItem item;
+  while (go && tt_next_item<Cfg::RB>(p, cur, item)) {
+    const TreeItem it = item;
     const int ms = NM == 2 && same(it.rows) > 128 ? 2 : 1;
     const int steps = same((it.t1 - it.t0) * Cfg::STEPS);
     for (int m = 0; m < ms && go; ++m) go = wait(&c.S.q_full[m], items[m] & 1u);
@@ -669,7 +724,7 @@ __device__ void tt_issue(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_out
   // nothing of the tensor cores may be in flight when TMEM is freed
   if (lead) tc_commit(&c.S.drain);
   bool late = false;
-  mbar_wait(&c.S.drain, 0, p.err, &late);
+  tt_wait(&c.S.drain, 0, p.err, &late);
 }
 
 // ---- softmax ---------------------------------------------------------------------
@@ -772,7 +827,7 @@ __device__ __forceinline__ float tt_cap(float x, float k1, float c2) {
 // instructions bound the kernel (a step took 2.5 times as long).
 template <bool GENERAL>
 __device__ __noinline__ void tt_masked(const TreeParams &p, uint32_t s_at, int width, unsigned long long seen,
-                                       const float2 *tok, float scale, float slope, int pos, int pre, int off, int c, int b) {
+                                       const float *ks, float scale, float slope, int pos, int pre, int off, int c, int b) {
   const float k1 = 2.f / p.cap, c2 = p.cap * kLog2e;
 #pragma unroll 1
   for (int ch = 0; ch < width; ch += 16) {
@@ -782,7 +837,7 @@ __device__ __noinline__ void tt_masked(const TreeParams &p, uint32_t s_at, int w
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int d = ch + i - off;   // draft
-      float y = x[i] * (tok ? tok[ch + i].x * scale : scale);
+      float y = x[i] * (ks ? ks[ch + i] : scale);
       if (GENERAL && p.cap > 0.f) y = tt_cap(y, k1, c2);
       if (GENERAL && p.slopes) {
         int far = pre + d - pos;
@@ -810,7 +865,7 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_o
   int zeroed = 0;                      // (narrow) the width for which P's other columns are zeros
   // every wait's outcome is the warp's: TMEM instructions are for whole warps
   const auto wait = [&](uint64_t *bar, uint32_t par) {
-    mbar_wait(bar, par, p.err, timed_out);
+    tt_wait(bar, par, p.err, timed_out);
     if (__any_sync(0xffffffffu, *timed_out)) *timed_out = true;
     return !*timed_out;
   };
@@ -821,7 +876,9 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_o
   };
   // the next item that has rows for this row tile
   const auto advance = [&](TreeItem &it) {
-    while (tree_next<TT, Cfg::RB>(p, cur, it)) {
+    TreeItem item;
+    while (tt_next_item<Cfg::RB>(p, cur, item)) {
+      it = item;
       if (m * 128 < it.rows) return true;
       tile += it.t1 - it.t0;
       ++k;
@@ -910,6 +967,7 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_o
     const int pre = it.n - it.c;
     const int first = row.copy * row.width;   // the copy's first token of a step
     const bool wide = NM == 2 || row.width == 64;
+    const bool in_one = p.P % row.width == 0;   // a step's tokens are of one page
     const bool idle = !__any_sync(0xffffffffu, row.real);
     ref = -INFINITY;
     l = 0.f;
@@ -942,39 +1000,49 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_o
       if (wide) seen |= static_cast<unsigned long long>(c.S.valid[mi][(in_tile >> 5) + 1]) << 32;
       const bool masked = off < row.width || seen != (wide ? ~0ull : 0xFFFFFFFFull);
       const bool scaled = QUANT && c.S.meta[QUANT ? mi : 0].scaled;
-      const float2 *tok = &c.S.tok[QUANT ? mi : 0][QUANT ? in_tile : 0];
+      // scales of one page serve the whole step where it lies in one; the V scale then goes into the exponent
+      const float *ks = &c.S.ks[QUANT ? mi : 0][QUANT ? in_tile : 0], *vs = &c.S.vs[QUANT ? mi : 0][QUANT ? in_tile : 0];
+      const bool one_page = QUANT && scaled && in_one && ks[0] > 0.f && ks[0] < 1e30f && vs[0] > 1e-30f && vs[0] < 1e30f;
       // Scores as they enter the exponential, in units of log2 e: times the softmax scale
       // (left to the exponential where nothing else is to be done), the pages' scales,
       // capped, less the distance, -inf where the row does not see the token.  Steps with
       // unseen tokens, one or two of an item, are finished out of line.
-      float sc = scale;
+      float sc = one_page ? ks[0] : scale;
       if (masked) {
         // tokens before the drafts, and the drafts of the row's bits
         seen &= off >= 64 ? ~0ull : off > 0 ? (row.bits << off) | ((1ull << off) - 1ull) : off > -64 ? row.bits >> -off : 0ull;
-        tt_masked<GENERAL>(p, s_at, row.width, seen, scaled ? tok : nullptr, scale, row.slope, row.pos, pre, off, it.c, it.b);
+        tt_masked<GENERAL>(p, s_at, row.width, seen, scaled ? ks : nullptr, scale, row.slope, row.pos, pre, off, it.c, it.b);
         sc = 1.f;
       }
       float x[64];
       tt_ld32(s_at, x);
       if (wide) tt_ld32(s_at + 32, x + 32);
       tc_wait_ld();
-      if (QUANT && scaled && !masked) {
+      if (QUANT && scaled && !one_page && !masked) {
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) {
+        for (int i = 0; i < 64; i += 4) {
           if (i == 32 && !wide) break;
-          const float4 s2 = *reinterpret_cast<const float4 *>(tok + i);
-          const float2 y = mul2(make_float2(x[i], x[i + 1]), mul2(make_float2(s2.x, s2.z), make_float2(scale, scale)));
+          const float4 k4 = *reinterpret_cast<const float4 *>(ks + i);
+          const float2 y = mul2(make_float2(x[i], x[i + 1]), make_float2(k4.x, k4.y));
+          const float2 z = mul2(make_float2(x[i + 2], x[i + 3]), make_float2(k4.z, k4.w));
           x[i] = y.x;
           x[i + 1] = y.y;
+          x[i + 2] = z.x;
+          x[i + 3] = z.y;
         }
         sc = 1.f;
       }
       if (GENERAL && p.cap > 0.f && !masked) {
-        const float k1 = (QUANT && scaled ? 1.f : scale) * 2.f / p.cap, c2 = p.cap * kLog2e;
+        const float c2 = p.cap * kLog2e;
+        const float2 k1 = make_float2(sc * 2.f / p.cap, sc * 2.f / p.cap);
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
+        for (int i = 0; i < 64; i += 2) {
           if (i == 32 && !wide) break;
-          x[i] = tt_cap(x[i], k1, c2);
+          const float2 y = mul2(make_float2(x[i], x[i + 1]), k1);
+          const float2 z = add2(make_float2(exp2_approx(y.x), exp2_approx(y.y)), make_float2(1.f, 1.f));
+          const float2 w = fma2(make_float2(rcp_approx(z.x), rcp_approx(z.y)), make_float2(-2.f * c2, -2.f * c2), make_float2(c2, c2));
+          x[i] = w.x;
+          x[i + 1] = w.y;
         }
         sc = 1.f;
       }
@@ -1017,32 +1085,37 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_o
         tt_wait_st();
       }
       // p = 2^(s - ref), its sum, and P as the MMA's operand
-      const float less = ref == -INFINITY ? 0.f : -ref;
+      float less = ref == -INFINITY ? 0.f : -ref, back = 1.f;
+      if (QUANT && one_page) {
+        less += log2f(vs[0]);
+        back = 1.f / vs[0];
+      }
       const float2 less2 = make_float2(less, less), sc2 = make_float2(sc, sc);
       float2 sum[2] = {};
       const uint32_t p_at = lanes + Cfg::p_col(m, b) + first / 2;
+      const auto exps = [&](auto by_token) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (half == 1 && !wide) break;
-        uint32_t w[16];
+        for (int half = 0; half < 2; ++half) {
+          if (half == 1 && !wide) break;
+          uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const int j = half * 32 + i;
-          const float2 y = fma2(make_float2(x[j], x[j + 1]), sc2, less2);
-          float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-          sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], e);
-          if (QUANT && scaled) {
-            const float4 s2 = *reinterpret_cast<const float4 *>(tok + j);
-            // an unseen token stays out whatever its page's scale
-            e.x = e.x == 0.f ? 0.f : e.x * s2.y;
-            e.y = e.y == 0.f ? 0.f : e.y * s2.w;
+          for (int i = 0; i < 32; i += 2) {
+            const int j = half * 32 + i;
+            const float2 y = fma2(make_float2(x[j], x[j + 1]), sc2, less2);
+            float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+            sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], e);
+            if (decltype(by_token)::value) e = mul2(e, *reinterpret_cast<const float2 *>(vs + j));
+            w[i >> 1] = pack_bf16(e.x, e.y);
           }
-          w[i >> 1] = pack_bf16(e.x, e.y);
+          tt_st16(p_at + 16 * half, w);
         }
-        tt_st16(p_at + 16 * half, w);
-      }
+      };
+      if (QUANT && scaled && !one_page)
+        exps(std::true_type());
+      else
+        exps(std::false_type());
       const float2 s01 = add2(sum[0], sum[1]);
-      l += s01.x + s01.y;
+      l += (s01.x + s01.y) * back;
       tt_wait_st();
       tc_fence_before();
       mbar_arrive(&c.S.p_full[2 * m + b]);
