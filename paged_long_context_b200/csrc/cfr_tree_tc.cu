@@ -33,22 +33,22 @@
 //    for each row tile beside the two O, so a tile is taken in two steps.
 // Either way the scores of a step are computed while the one before is in the softmax.
 //
-// Warps: warpgroup 0 = K producer (warp 0), MMA issuer (1), V producer (2), V
-// repair (3); then NM softmax warpgroups; with quantised pools one more that
-// expands codes.  K and V tiles go through one ring of slots, K of tile t in
-// place 2t, V in place 2t + 1.
+// Warps: warpgroup 0 = producer of K (warp 0), an MMA issuer for each row tile
+// (1, 2), producer of V (3); then NM softmax warpgroups; with quantised pools one
+// more that expands codes.  K and V tiles have a ring of slots each.
 //  - bf16 rows are brought by TMA boxes straight into the 128-byte-swizzled
 //    operand layout, quantised rows by bulk copies into their own rows' place
 //    and expanded there.
 //  - A V tile that reaches the drafts or the sequence's end is repaired before
-//    the MMA sees it: rows that hold no token become zeros, and non-finite
-//    values of drafts are taken out (they would reach, as 0 * NaN, rows that do
+//    the MMA sees it, by its producer or as it is expanded: rows that hold no token
+//    become zeros, and non-finite values of drafts are taken out (they would reach, as 0 * NaN, rows that do
 //    not see the draft) and added back at the end to the rows that see it.
 //
 // Bound by HBM up to about 128 rows (K and V once); beyond that the 128 x 128
 // exponentials of a tile (16 a clock and SM) and the MMAs come near it.
 #include <cuda_bf16.h>
 
+#include <climits>
 #include <cstring>
 #include <type_traits>
 
@@ -72,7 +72,10 @@ struct TtCfg {
   static constexpr int STEPS = NM;               // steps of a tile
   static constexpr int ROW_TILE = 128 * D * 2;   // bytes of 128 bf16 rows: a Q tile, a K or V slot
   // slots that fit beside the queries (227 KB in all); heads of 64 have slots of half the size
-  static constexpr int NS = (D == 128 ? 1 : 2) * (NM == 2 && QUANT ? 4 : 5);
+  // K slots 0 .. NK - 1, then V slots: two rings, so that no barrier of a slot is shared by both producers
+  static constexpr int NK = D == 128 ? 2 : 4;
+  static constexpr int NV = (D == 128 ? 1 : 2) * (NM == 2 && QUANT ? 2 : 3);
+  static constexpr int NS = NK + NV;
   static constexpr int WGS = 1 + NM + (QUANT ? 1 : 0);
   static constexpr int THREADS = 128 * WGS;
   static constexpr int SOFTMAX_T0 = 128;
@@ -92,21 +95,29 @@ struct TtMeta {
   float ks[MAX_PIECES], vs[MAX_PIECES];
 };
 
+// Page-table entries of a stretch of a sequence's pages, in shared memory; the next
+// entries wait in registers, so that running out of the cached ones waits for nothing.
+constexpr int PAGE_RUN = 64;
+struct TtPages {
+  int32_t id[PAGE_RUN];
+  uint8_t fmt[PAGE_RUN];
+};
+
 template <int NS, int NM, bool QUANT>
 struct TtSmem {
   uint64_t slot_full[NS], slot_empty[NS], raw_full[NS];
   // by row tile and, where two steps can be under way, by the step's parity: a wait by
   // parity must begin no earlier than one phase before the one it is for
   uint64_t s_full[2 * NM], p_full[2 * NM], pv_done[2 * NM], q_full[NM], o_free[NM];
-  uint64_t meta_full[META_RING], drain, meet;
+  uint64_t meta_full[META_RING], drain[NM], meet;
   uint32_t tmem_base;
   int flag[NS];
   unsigned long long nonfinite[META_RING];  // of item k & 7: drafts whose V was repaired
-  uint32_t v_valid[META_RING][4];
   int direct[NS];                           // the slot's tile needs no expansion or repair
   TreeScratch scratch;
   TtMeta meta[QUANT ? META_RING : 1];
-  uint32_t valid[META_RING][4];
+  uint32_t valid[META_RING][4], v_valid[META_RING][4];
+  TtPages pages[2];
   // K scale (times softmax scale and log2 e) and V scale of each token
   alignas(16) float ks[QUANT ? META_RING : 1][QUANT ? TT : 4], vs[QUANT ? META_RING : 1][QUANT ? TT : 4];
   // joining of the copies (narrow): 16 columns of O of every row, its maximum and sum
@@ -147,6 +158,16 @@ __device__ __forceinline__ void tt_ld16(uint32_t taddr, float *v) {
       : "memory");
 }
 
+__device__ __forceinline__ void tt_st32(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
 __device__ __forceinline__ void tt_st16(uint32_t taddr, const uint32_t *r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
@@ -287,166 +308,22 @@ __device__ __noinline__ bool tt_next_item(const TreeParams &p, TreeCursor &cur, 
   return tree_next<TT, RB>(p, cur, it);
 }
 
-// place in the ring of slots
-template <int NS>
+// place in a ring of slots, FIRST .. FIRST + N - 1
+template <int FIRST, int N>
 struct Ring {
-  int s = 0;
+  int s = FIRST;
   uint32_t ph = 0;
-  __device__ __forceinline__ void step(int n) {
-    s += n;
-    if (s >= NS) {
-      s -= NS;
+  __device__ __forceinline__ void step() {
+    if (++s == FIRST + N) {
+      s = FIRST;
       ph ^= 1u;
     }
   }
 };
-
-// ---- producers -----------------------------------------------------------------
-
-// One of the tile's pages, as lane `lane` of a producer sees it.
-struct Piece {
-  long long id;
-  int fmt;
-};
-
-__device__ __forceinline__ Piece tt_fetch(const TreeParams &p, const TreeItem &it, int t, int lane) {
-  Piece x{-1, 0};
-  const int j0 = t * TT, rows = min(TT, it.n - j0);
-  const int pg = j0 / p.P + lane;
-  if (t < it.t1 && rows > 0 && static_cast<long long>(pg) * p.P < j0 + rows) {
-    const long long cell = static_cast<long long>(it.b) * p.max_pages + pg;
-    x.id = p.page_table[cell];
-    x.fmt = p.page_fmt ? p.page_fmt[cell] : p.uniform_fmt;
-  }
-  return x;
-}
-
-// K (KV = 0) or V (KV = 1) of every tile, by one warp (one code for both: see the kernel).  Page-table entries are
-// read two tiles ahead and scales one, so that neither is waited for.
-//
-// The description of tile t is kept in place t & 7.  It may be overwritten by
-// tile t + 8 because K's slot of tile t + 8 is free only when the scores of a
-// tile t + 2 or later were issued (a ring has at most 12 slots, 6 tiles), which is after the softmax of
-// tile t handed over its P.
-template <int D, int NM, bool QUANT>
-__device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_out, const int KV) {
-  using Cfg = TtCfg<D, NM, QUANT>;
-  const TreeParams &p = c.p;
-  const int lane = threadIdx.x & 31;
-  Ring<Cfg::NS> r;
-  r.step(KV);
-  uint32_t raw_mask = 0, used = 0;   // slots filled through raw_full; slots filled at all
-  uint32_t phase_of = 0;             // the phase each was filled in
-  uint32_t tile = 0;
-  TreeItem item;
-  while (!*timed_out && tt_next_item<Cfg::RB>(p, cur, item)) {
-    const TreeItem it = item;
-    if (KV == 0 && lane == 0 && it.bad) set_err(p.err, CFR_DEVERR_SEQ_LEN);
-    const int pre = it.n - it.c;
-    Piece now = tt_fetch(p, it, it.t0, lane), next = tt_fetch(p, it, it.t0 + 1, lane);
-    for (int t = it.t0; t < it.t1; ++t, ++tile) {
-      const Piece after = tt_fetch(p, it, t + 2, lane);
-      const int j0 = t * TT, rows = max(0, min(TT, it.n - j0));
-      const int tin0 = j0 % p.P;
-      const int npiece = rows > 0 ? (tin0 + rows + p.P - 1) / p.P : 0;
-      bool ok = false;
-      int fmt = now.fmt;
-      if (lane < npiece) {
-        const bool known = fmt < kFmtCount;
-        const bool pool = known && p.k_pool[known ? fmt : 0];
-        ok = pool && now.id >= 0 && now.id < p.pool_pages[known ? fmt : 0];
-        if (!ok && KV == 0)
-          set_err(p.err, !known ? CFR_DEVERR_PAGE_FMT : !pool ? CFR_DEVERR_POOL : CFR_DEVERR_PAGE_ID);
-      }
-      const bool quant = QUANT && ok && is_quantised(fmt);
-      const bool any_quant = QUANT && __any_sync(0xffffffffu, quant);
-      const bool any4 = QUANT && __any_sync(0xffffffffu, quant && fmt == CFR_FMT_I4);
-      float2 sc = make_float2(1.f, 1.f);
-      if (QUANT && KV == 0 && quant)
-        sc = *reinterpret_cast<const float2 *>(p.scales[fmt] + (now.id * p.Hkv + it.g) * 2);
-      // this lane's page: tile rows [a, z)
-      const int a = lane == 0 ? 0 : min(rows, lane * p.P - tin0);
-      const int z = min(rows, (lane + 1) * p.P - tin0);
-      const int boxes = (z - a + c.box - 1) / c.box;
-      const uint32_t mine = !ok ? 0u : quant ? static_cast<uint32_t>((z - a) * row_bytes(fmt, D))
-                                             : static_cast<uint32_t>(boxes * c.box * D * 2);
-      const uint32_t bytes = __reduce_add_sync(0xffffffffu, mine);
-      // tokens of valid pages: lane w holds those of 32 w on
-      uint32_t valid = 0;
-#pragma unroll 1
-      for (int w = 0; w < 4; ++w) {
-        const int lo = max(a - 32 * w, 0), hi = min(z - 32 * w, 32);
-        const uint32_t any = __reduce_or_sync(0xffffffffu, ok && lo < hi ? (0xFFFFFFFFu >> (32 - (hi - lo))) << lo : 0u);
-        if (lane == w) valid = any;
-      }
-      const bool full = __all_sync(0xffffffffu, lane >= 4 || valid == 0xFFFFFFFFu);
-      const bool direct = !any_quant && (KV == 0 || (full && j0 + TT <= pre));
-      int go = 1;
-      if (lane == 0) go = tt_wait(&c.S.slot_empty[r.s], r.ph ^ 1u, p.err, timed_out) ? 1 : 0;
-      if (!__shfl_sync(0xffffffffu, go, 0)) {
-        *timed_out = true;
-        break;
-      }
-      uint64_t *done = direct ? &c.S.slot_full[r.s] : &c.S.raw_full[r.s];
-      const int mi = tile & (META_RING - 1);
-      if (KV == 0 && QUANT && lane < npiece) {
-        c.S.meta[mi].fmt[lane] = ok ? static_cast<uint8_t>(fmt) : 255;
-        c.S.meta[mi].ks[lane] = sc.x;
-        c.S.meta[mi].vs[lane] = sc.y;
-      }
-      if (lane < 4) (KV == 0 ? c.S.valid : c.S.v_valid)[mi][lane] = valid;
-      if (lane == 0) {
-        if (QUANT && KV == 0) {
-          c.S.meta[mi].tin0 = tin0;
-          c.S.meta[mi].scaled = any_quant ? (any4 ? 3 : 1) : 0;
-        }
-        c.S.direct[r.s] = direct;
-      }
-      __syncwarp();
-      if (lane == 0) {
-        if (KV == 0 && !QUANT) mbar_arrive(&c.S.meta_full[mi]);
-        // a tile that needs nothing is shown to the expanding or repairing warps all the same, in order:
-        // a slot holds K and V in turn, and its barriers have one phase for each
-        if (direct) mbar_arrive(&c.S.raw_full[r.s]);
-        mbar_arrive_expect_tx(done, bytes);
-      }
-      __syncwarp();
-      used |= 1u << r.s;
-      raw_mask = direct ? raw_mask & ~(1u << r.s) : raw_mask | (1u << r.s);
-      phase_of = r.ph ? phase_of | (1u << r.s) : phase_of & ~(1u << r.s);
-      if (ok) {
-        uint8_t *dst = c.slot(r.s) + a * 128;
-        const int in_page = lane == 0 ? tin0 : 0;
-        if (quant) {
-          const int rb = row_bytes(fmt, D);
-          const uint8_t *pool = KV ? p.v_pool[fmt] : p.k_pool[fmt];
-          // (places: see tt_expand)
-          bulk_g2s(D == 128 && fmt == CFR_FMT_I4 ? dst + TT * 128 : dst, pool + ((now.id * p.Hkv + it.g) * p.P + in_page) * rb, mine, done);
-        } else {
-          const int y = static_cast<int>((now.id * p.Hkv + it.g) * p.P + in_page);
-          for (int x = 0; x < boxes; ++x)
-#pragma unroll
-            for (int half = 0; half < D / 64; ++half)
-              tma_load_2d(dst + half * (TT * 128) + x * c.box * 128, KV ? &c.vmap : &c.kmap, half * 64,
-                          y + x * c.box, done);
-        }
-      }
-      now = next;
-      next = after;
-      r.step(2);
-    }
-  }
-  if (*timed_out && lane == 0) {
-    // leave no copy in flight
-    for (int s = 0; s < Cfg::NS; ++s) {
-      bool late = false;
-      if ((used >> s) & 1u)
-        tt_wait((raw_mask >> s) & 1u ? &c.S.raw_full[s] : &c.S.slot_full[s], (phase_of >> s) & 1u, p.err, &late);
-    }
-  }
-}
-
-// ---- repair and expansion -------------------------------------------------------
+template <typename Cfg>
+using KRing = Ring<0, Cfg::NK>;
+template <typename Cfg>
+using VRing = Ring<Cfg::NK, Cfg::NV>;
 
 // Row i of a V tile before the MMA: zeros where it holds no token; non-finite
 // values of a draft taken out and the draft noted.
@@ -469,78 +346,261 @@ __device__ __noinline__ void tt_repair_row(uint8_t *v, int i, bool valid, int dr
   if (bad) atomicOr(noted, 1ull << draft);
 }
 
-// V repair of caches of bf16 pages only, one warp.  It takes part in the release
-// of every slot, so that it is never a phase behind a slot's barrier.
-template <int D, int NM>
-__device__ void tt_repair(TtCtx<D, NM, false> &c, TreeCursor cur, bool *timed_out) {
-  using Cfg = TtCfg<D, NM, false>;
+// ---- producers -----------------------------------------------------------------
+
+// K (KV = 0) or V (KV = 1) of every tile, by one warp each (one code for both, for the
+// instruction cache).  A tile is worked out before its slot is waited for; its copies are
+// issued by one lane in uniform control flow (from the lanes that hold the pages, a
+// copy took about 100 cycles to issue, and 16 of them a tile of 16-token pages bound the kernel).
+//
+// Tiles go from the newest to the oldest: with ALiBi, or any attention that favours the
+// recent, the running maximum is then found at once and O is hardly ever rescaled.
+//
+// The description of the CTA's tile t is kept in place t & 7.  It may be overwritten by
+// tile t + 8 because K's slot of tile t + 8 is free only when the scores of a
+// tile t + 4 or later were issued (there are at most 4 slots of K), which is after the softmax of
+// tile t handed over its P.
+template <int D, int NM, bool QUANT>
+__device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_out, const int KV) {
+  using Cfg = TtCfg<D, NM, QUANT>;
   const TreeParams &p = c.p;
   const int lane = threadIdx.x & 31;
-  Ring<Cfg::NS> r;
+  TtPages &pc = c.S.pages[KV];
+  uint32_t lead;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(lead));
+  const int r_first = KV ? Cfg::NK : 0, r_end = KV ? Cfg::NS : Cfg::NK;
+  int slot_i = r_first;
+  uint32_t slot_ph = 0;
+  uint32_t raw_mask = 0, used = 0;   // slots filled through raw_full; slots filled at all
+  uint32_t phase_of = 0;             // the phase each was filled in
   uint32_t tile = 0, k = 0;
+  const int P = p.P;
+  // (bf16 pages only) a V tile whose copies are under way and that has to be repaired when they
+  // are done: the next tile's copies are issued first
+  int pend_slot = -1, pend_j0 = 0, pend_mi = 0, pend_item = 0;
+  uint32_t raw_ph = 0;   // the phase that each slot's raw_full is in
+  int pre = 0;
+  const auto repair = [&]() {
+    if (QUANT || pend_slot < 0) return;
+    tt_wait(&c.S.raw_full[pend_slot], (raw_ph >> pend_slot) & 1u, p.err, timed_out);
+    if (__any_sync(0xffffffffu, *timed_out)) {
+      *timed_out = true;
+      return;
+    }
+    raw_ph ^= 1u << pend_slot;
+    raw_mask &= ~(1u << pend_slot);
+    used &= ~(1u << pend_slot);
+#pragma unroll 1
+    for (int i = lane; i < TT; i += 32) {
+      const bool valid = (c.S.v_valid[pend_mi][i >> 5] >> (i & 31)) & 1u;
+      if (!valid || pend_j0 + i >= pre)
+        tt_repair_row<D>(c.slot(pend_slot), i, valid, pend_j0 + i - pre, &c.S.nonfinite[pend_item]);
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&c.S.slot_full[pend_slot]);
+    pend_slot = -1;
+  };
   TreeItem item;
   for (; !*timed_out && tt_next_item<Cfg::RB>(p, cur, item); ++k) {
     const TreeItem it = item;
-    const int pre = it.n - it.c;
-    if (lane == 0) c.S.nonfinite[k & (META_RING - 1)] = 0ull;
-    __syncwarp();
-    for (int t2 = 2 * it.t0; t2 < 2 * it.t1; ++t2) {
-      int go = 1;
-      if (lane == 0) go = tt_wait(&c.S.raw_full[r.s], r.ph, p.err, timed_out) ? 1 : 0;
-      if (!__shfl_sync(0xffffffffu, go, 0)) {
+    if (!QUANT && KV == 1 && lane == 0) c.S.nonfinite[k & (META_RING - 1)] = 0ull;
+    if (KV == 0 && lane == 0 && it.bad) set_err(p.err, CFR_DEVERR_SEQ_LEN);
+    pre = it.n - it.c;
+    const long long table = static_cast<long long>(it.b) * p.max_pages;
+    // pages [lo, lo + PAGE_RUN) of the sequence are cached, [nlo, nlo + PAGE_RUN) wait in registers
+    const int pg_first = it.t0 * TT / P;
+    int lo = INT_MAX, nlo = 0;
+    int32_t nid[PAGE_RUN / 32];
+    uint8_t nfmt[PAGE_RUN / 32];
+    const auto fetch = [&](int from) {   // pages from .. from + PAGE_RUN - 1, those of the item
+#pragma unroll
+      for (int i = 0; i < PAGE_RUN / 32; ++i) {
+        const int pg = from + 32 * i + lane;
+        if (pg >= pg_first && static_cast<long long>(pg) * P < it.n) {
+          nid[i] = p.page_table[table + pg];
+          nfmt[i] = p.page_fmt ? p.page_fmt[table + pg] : static_cast<uint8_t>(p.uniform_fmt);
+        }
+      }
+    };
+    for (int t = it.t1 - 1; t >= it.t0; --t, ++tile) {
+      const int j0 = t * TT, rows = max(0, min(TT, it.n - j0));
+      const int pg0 = j0 / P, tin0 = j0 - pg0 * P;
+      const int npiece = rows > 0 ? (tin0 + rows + P - 1) / P : 0;
+      if (npiece > 0 && pg0 < lo) {
+        if (lo == INT_MAX) {
+          nlo = pg0 + npiece - PAGE_RUN;
+          fetch(nlo);
+        }
+        lo = nlo;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < PAGE_RUN / 32; ++i) {
+          pc.id[32 * i + lane] = nid[i];
+          pc.fmt[32 * i + lane] = nfmt[i];
+        }
+        __syncwarp();
+        // the next run ends where this one can first fall short: at the pages of one more tile
+        nlo = lo + MAX_PIECES - PAGE_RUN;
+        fetch(nlo);
+      }
+      bool ok = false;
+      int fmt = 0;
+      long long sub = 0;
+      if (lane < npiece) {
+        fmt = pc.fmt[pg0 + lane - lo];
+        const long long id = pc.id[pg0 + lane - lo];
+        const bool known = fmt < kFmtCount;
+        const bool pool = known && p.k_pool[known ? fmt : 0];
+        ok = pool && id >= 0 && id < p.pool_pages[known ? fmt : 0];
+        if (!ok && KV == 0) set_err(p.err, !known ? CFR_DEVERR_PAGE_FMT : !pool ? CFR_DEVERR_POOL : CFR_DEVERR_PAGE_ID);
+        sub = id * p.Hkv + it.g;
+      }
+      const bool quant = QUANT && ok && is_quantised(fmt);
+      const bool any_quant = QUANT && __any_sync(0xffffffffu, quant);
+      const bool any4 = QUANT && __any_sync(0xffffffffu, quant && fmt == CFR_FMT_I4);
+      float2 sc = make_float2(1.f, 1.f);
+      if (QUANT && quant && KV == 0) sc = *reinterpret_cast<const float2 *>(p.scales[fmt] + sub * 2);
+      // this lane's page: tile rows [a, z)
+      const int a = lane == 0 ? 0 : min(rows, lane * P - tin0);
+      const int z = min(rows, (lane + 1) * P - tin0);
+      const int boxes = (z - a + c.box - 1) / c.box;
+      const uint32_t mine = !ok ? 0u : quant ? static_cast<uint32_t>((z - a) * row_bytes(fmt, D))
+                                             : static_cast<uint32_t>(boxes * c.box * D * 2);
+      const uint32_t bytes = __reduce_add_sync(0xffffffffu, mine);
+      const uint32_t okb = __ballot_sync(0xffffffffu, ok);
+      // tokens of valid pages: lane w holds those of 32 w on
+      uint32_t valid = 0xFFFFFFFFu;
+      const bool full = rows == TT && okb == (0xFFFFFFFFu >> (32 - npiece));
+      if (!full) {
+#pragma unroll 1
+        for (int w = 0; w < 4; ++w) {
+          const int x = max(a - 32 * w, 0), y = min(z - 32 * w, 32);
+          const uint32_t any = __reduce_or_sync(0xffffffffu, ok && x < y ? (0xFFFFFFFFu >> (32 - (y - x))) << x : 0u);
+          if (lane == w) valid = any;
+        }
+      }
+      const int mi = tile & (META_RING - 1);
+      const bool direct = !any_quant && (KV == 0 || (full && j0 + TT <= pre));
+      tt_wait(&c.S.slot_empty[slot_i], slot_ph ^ 1u, p.err, timed_out);
+      if (__any_sync(0xffffffffu, *timed_out)) {
         *timed_out = true;
         break;
       }
-      (void)mbar_try_wait(&c.S.raw_full[r.s], r.ph);
-      const bool is_v = t2 & 1;
-      if (is_v && !c.S.direct[r.s]) {
-        const int j0 = (t2 >> 1) * TT;
-        for (int i = lane; i < TT; i += 32) {
-          const bool valid = (c.S.v_valid[tile & (META_RING - 1)][i >> 5] >> (i & 31)) & 1u;
-          if (!valid || j0 + i >= pre)
-            tt_repair_row<D>(c.slot(r.s), i, valid, j0 + i - pre, &c.S.nonfinite[k & (META_RING - 1)]);
+      uint64_t *done = direct ? &c.S.slot_full[slot_i] : &c.S.raw_full[slot_i];
+      if (KV == 0) {
+        if (QUANT && lane < npiece) {
+          c.S.meta[mi].fmt[lane] = ok ? static_cast<uint8_t>(fmt) : 255;
+          c.S.meta[mi].ks[lane] = sc.x;
+          c.S.meta[mi].vs[lane] = sc.y;
         }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c.S.slot_full[r.s]);
+        if (QUANT && lane == 0) {
+          c.S.meta[mi].tin0 = tin0;
+          c.S.meta[mi].scaled = any_quant ? (any4 ? 3 : 1) : 0;
+        }
+      }
+      if (lane < 4) (KV == 0 ? c.S.valid : c.S.v_valid)[mi][lane] = valid;
+      if (lane == 0) c.S.direct[slot_i] = direct;
+      __syncwarp();
+      if (lane == 0) {
+        if (KV == 0 && !QUANT) mbar_arrive(&c.S.meta_full[mi]);
+        // a tile that needs nothing is shown to the expanding warps all the same, in order
+        if (QUANT && direct) mbar_arrive(&c.S.raw_full[slot_i]);
+        mbar_arrive_expect_tx(done, bytes);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&c.S.slot_empty[r.s]);
-      if (is_v) ++tile;
-      r.step(1);
+      used |= 1u << slot_i;
+      raw_mask = direct ? raw_mask & ~(1u << slot_i) : raw_mask | (1u << slot_i);
+      const bool ph_of = QUANT || direct ? slot_ph : (raw_ph >> slot_i) & 1u;
+      phase_of = ph_of ? phase_of | (1u << slot_i) : phase_of & ~(1u << slot_i);
+      const CUtensorMap *map = KV ? &c.vmap : &c.kmap;
+      uint8_t *const slot = c.slot(slot_i);
+#pragma unroll 1
+      for (int f = 0; f < npiece; ++f) {
+        if (!((okb >> f) & 1u)) continue;
+        const long long sub_f = __shfl_sync(0xffffffffu, sub, f);
+        const int a_f = f == 0 ? 0 : f * P - tin0, in_page = f == 0 ? tin0 : 0;
+        uint8_t *dst = slot + a_f * 128;
+        if (QUANT && any_quant) {
+          const int fmt_f = __shfl_sync(0xffffffffu, fmt, f);
+          const uint32_t mine_f = __shfl_sync(0xffffffffu, mine, f);
+          if (is_quantised(fmt_f)) {
+            const uint8_t *pool = KV ? p.v_pool[fmt_f] : p.k_pool[fmt_f];
+            // (places: see tt_expand)
+            if (lead)
+              bulk_g2s(D == 128 && fmt_f == CFR_FMT_I4 ? dst + TT * 128 : dst,
+                       pool + (sub_f * P + in_page) * row_bytes(fmt_f, D), mine_f, done);
+            continue;
+          }
+        }
+        int y = static_cast<int>(sub_f * P + in_page);
+        const int z_f = min(rows, (f + 1) * P - tin0);
+#pragma unroll 1
+        for (int x = a_f; x < z_f; x += c.box, y += c.box, dst += c.box * 128)
+          if (lead)
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half) tma_load_2d(dst + half * (TT * 128), map, half * 64, y, done);
+      }
+      repair();
+      if (*timed_out) break;
+      if (!QUANT && !direct) {
+        pend_slot = slot_i;
+        pend_j0 = j0;
+        pend_mi = mi;
+        pend_item = k & (META_RING - 1);
+      }
+      if (++slot_i == r_end) {
+        slot_i = r_first;
+        slot_ph ^= 1u;
+      }
+    }
+    if (!*timed_out) repair();   // (the drafts are this item's)
+  }
+  if (*timed_out && lane == 0) {
+    // leave no copy in flight
+    for (int s = 0; s < Cfg::NS; ++s) {
+      bool late = false;
+      if ((used >> s) & 1u)
+        tt_wait((raw_mask >> s) & 1u ? &c.S.raw_full[s] : &c.S.slot_full[s], (phase_of >> s) & 1u, p.err, &late);
     }
   }
 }
 
+// ---- expansion -------------------------------------------------------------------
+
 // Expansion (and V repair) of caches with quantised pages: thread i owns row i.
-// It takes part in the release of every slot, as the repair warp above does.
+// It takes part in the release of every slot, so that it is never a phase behind a
+// slot's barrier.
 template <int D, int NM>
 __device__ void tt_expand(TtCtx<D, NM, true> &c, TreeCursor cur, bool *timed_out) {
   using Cfg = TtCfg<D, NM, true>;
   const TreeParams &p = c.p;
   const int i = threadIdx.x - Cfg::LOADER_T0;
-  Ring<Cfg::NS> r;
+  KRing<Cfg> kr;
+  VRing<Cfg> vr;
   uint32_t tile = 0, k = 0;
   TreeItem item;
   for (; tt_next_item<Cfg::RB>(p, cur, item); ++k) {
     const TreeItem it = item;
     const int pre = it.n - it.c;
     if (i == 0) c.S.nonfinite[k & (META_RING - 1)] = 0ull;
-    for (int t = it.t0; t < it.t1; ++t, ++tile) {
+    for (int t = it.t1 - 1; t >= it.t0; --t, ++tile) {
       const int mi = tile & (META_RING - 1);
       const TtMeta &m = c.S.meta[mi];
       int fmt = 255, a = 0;
       bool valid = false;
       for (int kv = 0; kv < 2; ++kv) {
+        const int slot = kv ? vr.s : kr.s;
+        const uint32_t ph = kv ? vr.ph : kr.ph;
         // one thread waits, the barrier hands on its outcome
-        if (i == 0) c.S.flag[r.s] = tt_wait(&c.S.raw_full[r.s], r.ph, p.err, timed_out) ? 1 : 0;
+        if (i == 0) c.S.flag[slot] = tt_wait(&c.S.raw_full[slot], ph, p.err, timed_out) ? 1 : 0;
         named_sync(1, 128);
-        if (!c.S.flag[r.s]) {
+        if (!c.S.flag[slot]) {
           *timed_out = true;
           return;
         }
-        (void)mbar_try_wait(&c.S.raw_full[r.s], r.ph);
-        const bool direct = c.S.direct[r.s];
+        (void)mbar_try_wait(&c.S.raw_full[slot], ph);
+        const bool direct = c.S.direct[slot];
         const bool any4 = m.scaled & 2;   // 4-bit rows among the tile's
         if (kv == 0) {
           valid = (c.S.valid[mi][i >> 5] >> (i & 31)) & 1u;
@@ -551,30 +611,30 @@ __device__ void tt_expand(TtCtx<D, NM, true> &c, TreeCursor cur, bool *timed_out
           c.S.vs[mi][i] = valid ? m.vs[pc] : 0.f;
         }
         if (!direct) {
-          uint8_t *op = c.slot(r.s);
+          uint8_t *op = c.slot(slot);
           const bool eight = fmt == CFR_FMT_I8 || fmt == CFR_FMT_FP8, four = fmt == CFR_FMT_I4;
           const int draft = t * TT + i - pre;
           const bool look = kv == 1 && fmt == CFR_FMT_FP8 && draft >= 0;   // E4M3 has NaN
           // 64 values at a time (a row of one half of the slot), so that the code stays small;
           // rows are read in an order that spreads a warp's lanes over the banks
           const auto put8 = [&](const uint4 (&raw)[4], int hh) {
-#pragma unroll
+#pragma unroll 1
             for (int x = 0; x < 4; ++x) {
               const int ci = (x + i) & 3;   // codes 16 ci .. of the 64
+              const uint4 w = x == 0 ? raw[0] : x == 1 ? raw[1] : x == 2 ? raw[2] : raw[3];
               uint32_t o[8];
-              expand16<8>(fmt, raw[x], o);
-              const uint4 u = make_uint4(o[0], o[1], o[2], o[3]), v = make_uint4(o[4], o[5], o[6], o[7]);
+              expand16<8>(fmt, w, o);
               uint8_t *hb = op + hh * (TT * 128);
-              *reinterpret_cast<uint4 *>(hb + sw128(i, 2 * ci)) = u;
-              *reinterpret_cast<uint4 *>(hb + sw128(i, 2 * ci + 1)) = v;
+              *reinterpret_cast<uint4 *>(hb + sw128(i, 2 * ci)) = make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4 *>(hb + sw128(i, 2 * ci + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
             }
           };
           const auto put4 = [&](const uint4 (&raw)[2], int hh) {
-#pragma unroll
+#pragma unroll 1
             for (int x = 0; x < 2; ++x) {
               const int ci = (x + (i >> 1)) & 1;   // codes 32 ci .. of the 64
               uint32_t o[16];
-              expand16<16>(fmt, raw[x], o);
+              expand16<16>(fmt, x == 0 ? raw[0] : raw[1], o);
               uint8_t *hb = op + hh * (TT * 128);
 #pragma unroll
               for (int y = 0; y < 4; ++y)
@@ -626,11 +686,14 @@ __device__ void tt_expand(TtCtx<D, NM, true> &c, TreeCursor cur, bool *timed_out
         }
         named_sync(1, 128);
         if (i == 0) {
-          if (!direct) mbar_arrive(&c.S.slot_full[r.s]);
+          if (!direct) mbar_arrive(&c.S.slot_full[slot]);
           if (kv == 0) mbar_arrive(&c.S.meta_full[mi]);
-          mbar_arrive(&c.S.slot_empty[r.s]);
+          mbar_arrive(&c.S.slot_empty[slot]);
         }
-        r.step(1);
+        if (kv)
+          vr.step();
+        else
+          kr.step();
       }
     }
   }
@@ -638,47 +701,47 @@ __device__ void tt_expand(TtCtx<D, NM, true> &c, TreeCursor cur, bool *timed_out
 
 // ---- MMA issue ------------------------------------------------------------------
 
-// The whole warp walks the steps and one lane issues: with control flow and
-// operands the same in every lane, descriptors stay in uniform registers (from a
-// lone lane each MMA took 80 to 100 cycles to issue, for 32 to 64 of tensor time).
+// The MMAs of row tile m, by one warp (two row tiles: two warps, so that neither
+// waits for the other's softmax).  The whole warp walks the steps and one lane
+// issues: with control flow and operands the same in every lane, descriptors
+// stay in uniform registers (from a lone lane each MMA took 80 to 100 cycles to
+// issue, for 32 to 64 of tensor time).
 template <int D, int NM, bool QUANT>
-__device__ void tt_issue(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_out) {
+__device__ void tt_issue(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_out, int m_) {
   using Cfg = TtCfg<D, NM, QUANT>;
   const TreeParams &p = c.p;
   const auto same = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+  const int m = NM == 1 ? 0 : same(m_);
   const uint32_t tmem = same(c.S.tmem_base);
-  const uint32_t qa = same(smem_u32(c.q)), sa = same(smem_u32(c.slots));
+  const uint32_t qa = same(smem_u32(c.q)) + m * Cfg::ROW_TILE, sa = same(smem_u32(c.slots));
   uint32_t lead;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(lead));
   constexpr uint32_t qk_desc = tc_idesc(1, 0, 0, Cfg::STEP), pv_desc = tc_idesc(1, 0, 1, D);
   constexpr int STEP_BYTES = Cfg::STEP * 128;     // of a step's rows in each 64-column half of a slot
-  Ring<Cfg::NS> kr, vr;
-  vr.step(1);
-  uint32_t cnt[2] = {0, 0}, items[2] = {0, 0};    // steps and items of each row tile so far
+  KRing<Cfg> kr;
+  VRing<Cfg> vr;
+  uint32_t cnt = 0, items = 0;                    // steps and items of the row tile so far
   const auto wait = [&](uint64_t *bar, uint32_t par) {
     tt_wait(bar, par, p.err, timed_out);
     return __all_sync(0xffffffffu, !*timed_out) != 0;
   };
-  const auto scores = [&](int m, uint32_t n, int h) {   // S of row tile m's n-th step, from the K slot
-    const uint32_t d = tmem + Cfg::s_col(m, n & 1);
-    const uint64_t a = tc_sdesc(qa + m * Cfg::ROW_TILE, 16, 1024, 2);
-    const uint64_t b = tc_sdesc(sa + kr.s * Cfg::ROW_TILE + h * STEP_BYTES, 16, 1024, 2);
-    if (lead) {
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint64_t off = ((k >> 2) * (TT * 128) + (k & 3) * 32) >> 4;
-        tc_mma(d, a + off, b + off, qk_desc, k > 0 ? 1u : 0u);
-      }
-      tc_commit(&c.S.s_full[2 * m + (n & 1)]);
-    }
-  };
   bool go = true;
   TreeItem item;
   while (go && tt_next_item<Cfg::RB>(p, cur, item)) {
-    const TreeItem it = item;
-    const int ms = NM == 2 && same(it.rows) > 128 ? 2 : 1;
-    const int steps = same((it.t1 - it.t0) * Cfg::STEPS);
-    for (int m = 0; m < ms && go; ++m) go = wait(&c.S.q_full[m], items[m] & 1u);
+    const int steps = same((item.t1 - item.t0) * Cfg::STEPS);
+    if (NM == 2 && same(item.rows) <= 128 * m) {
+      // no rows here: the slots go by
+      for (int s = 0; s < steps / Cfg::STEPS && go; ++s) {
+        go = wait(&c.S.slot_full[kr.s], kr.ph);
+        if (go && lead) mbar_arrive(&c.S.slot_empty[kr.s]);
+        if (go) go = wait(&c.S.slot_full[vr.s], vr.ph);
+        if (go && lead) mbar_arrive(&c.S.slot_empty[vr.s]);
+        kr.step();
+        vr.step();
+      }
+      continue;
+    }
+    go = wait(&c.S.q_full[m], items & 1u);
     if (!go) break;
     // step -1 only issues the scores of step 0
     for (int s = -1; s < steps; ++s) {
@@ -687,44 +750,46 @@ __device__ void tt_issue(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_out
         if (h == 0) go = wait(&c.S.slot_full[kr.s], kr.ph);
         if (!go) break;
         tc_fence_after();
-        for (int m = 0; m < ms; ++m) scores(m, cnt[m] + (s < 0 ? 0 : 1), h);
-        if (h == Cfg::STEPS - 1) {
-          if (lead) tc_commit(&c.S.slot_empty[kr.s]);
-          kr.step(2);
-        }
-      }
-      if (s < 0) continue;
-      const int h = s % Cfg::STEPS;
-      if (h == 0) go = wait(&c.S.slot_full[vr.s], vr.ph);
-      if (!go) break;
-      for (int m = 0; m < ms; ++m) {
-        const int b = cnt[m] & 1;
-        if (s == 0) go = wait(&c.S.o_free[m], (items[m] & 1u) ^ 1u);
-        if (go) go = wait(&c.S.p_full[2 * m + b], (cnt[m] >> 1) & 1u);
-        if (!go) break;
-        tc_fence_after();
-        const uint32_t d = tmem + Cfg::O_COL + m * 128, a = tmem + Cfg::p_col(m, b);
-        const uint64_t v = tc_sdesc(sa + vr.s * Cfg::ROW_TILE + h * STEP_BYTES, TT * 128, 1024, 2);
+        const uint32_t n = cnt + (s < 0 ? 0 : 1);
+        const uint32_t d = tmem + Cfg::s_col(m, n & 1);
+        const uint64_t a = tc_sdesc(qa, 16, 1024, 2);
+        const uint64_t b = tc_sdesc(sa + kr.s * Cfg::ROW_TILE + h * STEP_BYTES, 16, 1024, 2);
         if (lead) {
 #pragma unroll
-          for (int k = 0; k < Cfg::STEP / 16; ++k)
-            tt_mma_ts(d, a + k * 8, v + static_cast<uint64_t>(k * 2048 >> 4), pv_desc, s > 0 || k > 0 ? 1u : 0u);
-          tc_commit(&c.S.pv_done[2 * m + b]);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t off = ((k >> 2) * (TT * 128) + (k & 3) * 32) >> 4;
+            tc_mma(d, a + off, b + off, qk_desc, k > 0 ? 1u : 0u);
+          }
+          tc_commit(&c.S.s_full[2 * m + (n & 1)]);
+          if (h == Cfg::STEPS - 1) tc_commit(&c.S.slot_empty[kr.s]);
         }
-        ++cnt[m];
+        if (h == Cfg::STEPS - 1) kr.step();
       }
+      if (s < 0) continue;
+      const int h = s % Cfg::STEPS, b = cnt & 1;
+      if (h == 0) go = wait(&c.S.slot_full[vr.s], vr.ph);
+      if (go && s == 0) go = wait(&c.S.o_free[m], (items & 1u) ^ 1u);
+      if (go) go = wait(&c.S.p_full[2 * m + b], (cnt >> 1) & 1u);
       if (!go) break;
-      if (h == Cfg::STEPS - 1) {
-        if (lead) tc_commit(&c.S.slot_empty[vr.s]);
-        vr.step(2);
+      tc_fence_after();
+      const uint32_t d = tmem + Cfg::O_COL + m * 128, a = tmem + Cfg::p_col(m, b);
+      const uint64_t v = tc_sdesc(sa + vr.s * Cfg::ROW_TILE + h * STEP_BYTES, TT * 128, 1024, 2);
+      if (lead) {
+#pragma unroll
+        for (int k = 0; k < Cfg::STEP / 16; ++k)
+          tt_mma_ts(d, a + k * 8, v + static_cast<uint64_t>(k * 2048 >> 4), pv_desc, s > 0 || k > 0 ? 1u : 0u);
+        tc_commit(&c.S.pv_done[2 * m + b]);
+        if (h == Cfg::STEPS - 1) tc_commit(&c.S.slot_empty[vr.s]);
       }
+      ++cnt;
+      if (h == Cfg::STEPS - 1) vr.step();
     }
-    for (int m = 0; m < ms; ++m) ++items[m];
+    ++items;
   }
   // nothing of the tensor cores may be in flight when TMEM is freed
-  if (lead) tc_commit(&c.S.drain);
+  if (lead) tc_commit(&c.S.drain[m]);
   bool late = false;
-  tt_wait(&c.S.drain, 0, p.err, &late);
+  tt_wait(&c.S.drain[m], 0, p.err, &late);
 }
 
 // ---- softmax ---------------------------------------------------------------------
@@ -860,6 +925,9 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_o
   const uint32_t lanes = c.S.tmem_base + (static_cast<uint32_t>(r & 96) << 16);   // this warp's TMEM lanes
   const uint32_t o_at = lanes + Cfg::O_COL + m * 128;
   const float scale = p.sigma * kLog2e;
+  // scores that a thread holds at once: a step's 64 where the code for them fits the instruction cache beside
+  // the other roles (in registers throughout: 1M tokens 764 us against 865), 32 with the expansion of codes
+  constexpr int CH = QUANT ? 32 : 64;
   uint32_t cnt = 0, tile = 0, k = 0;   // steps of this row tile, tiles and items of the CTA
   uint32_t met = 0;                    // meetings of the warpgroup's threads so far
   int zeroed = 0;                      // (narrow) the width for which P's other columns are zeros
@@ -995,7 +1063,7 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_o
       }
       const uint32_t s_at = lanes + Cfg::s_col(m, b) + first;
       const int in_tile = h * Cfg::STEP + first;                // the copy's first token in the tile
-      const int off = pre - ((it.t0 + s / Cfg::STEPS) * TT + in_tile);  // its tokens before the drafts
+      const int off = pre - ((it.t1 - 1 - s / Cfg::STEPS) * TT + in_tile);  // its tokens before the drafts
       unsigned long long seen = c.S.valid[mi][in_tile >> 5];
       if (wide) seen |= static_cast<unsigned long long>(c.S.valid[mi][(in_tile >> 5) + 1]) << 32;
       const bool masked = off < row.width || seen != (wide ? ~0ull : 0xFFFFFFFFull);
@@ -1014,55 +1082,69 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_o
         tt_masked<GENERAL>(p, s_at, row.width, seen, scaled ? ks : nullptr, scale, row.slope, row.pos, pre, off, it.c, it.b);
         sc = 1.f;
       }
-      float x[64];
-      tt_ld32(s_at, x);
-      if (wide) tt_ld32(s_at + 32, x + 32);
-      tc_wait_ld();
-      if (QUANT && scaled && !one_page && !masked) {
+      // CH tokens at a time, the last first; the second pass then begins with the
+      // ones that are in registers
+      const bool finish_here = !masked && ((QUANT && scaled && !one_page) || (GENERAL && (p.cap > 0.f || p.slopes)));
+      const float sc_in = sc;
+      if (finish_here) sc = 1.f;
+      const bool half = CH == 64 && row.width == 32;   // (the rest of x is not used then)
+      float x[CH], top = -INFINITY;
+#pragma unroll 1
+      for (int ch = half ? 0 : row.width - CH; ch >= 0; ch -= CH) {
+        tt_ld32(s_at + ch, x);
+        if (CH == 64 && !half) tt_ld32(s_at + ch + 32, x + CH - 32);
+        tc_wait_ld();
+        if ((QUANT || GENERAL) && finish_here) {
+          float mul = sc_in;   // what is still to be multiplied
+          if (QUANT && scaled && !one_page) {
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          if (i == 32 && !wide) break;
-          const float4 k4 = *reinterpret_cast<const float4 *>(ks + i);
-          const float2 y = mul2(make_float2(x[i], x[i + 1]), make_float2(k4.x, k4.y));
-          const float2 z = mul2(make_float2(x[i + 2], x[i + 3]), make_float2(k4.z, k4.w));
-          x[i] = y.x;
-          x[i + 1] = y.y;
-          x[i + 2] = z.x;
-          x[i + 3] = z.y;
+            for (int i = 0; i < CH; i += 4) {
+              if (i == 32 && half) break;
+              const float4 k4 = *reinterpret_cast<const float4 *>(ks + ch + i);
+              const float2 y = mul2(make_float2(x[i], x[i + 1]), make_float2(k4.x, k4.y));
+              const float2 z = mul2(make_float2(x[i + 2], x[i + 3]), make_float2(k4.z, k4.w));
+              x[i] = y.x;
+              x[i + 1] = y.y;
+              x[i + 2] = z.x;
+              x[i + 3] = z.y;
+            }
+            mul = 1.f;
+          }
+          if (GENERAL && p.cap > 0.f) {
+            const float c2 = p.cap * kLog2e;
+            const float2 k1 = make_float2(mul * 2.f / p.cap, mul * 2.f / p.cap);
+#pragma unroll
+            for (int i = 0; i < CH; i += 2) {
+              if (i == 32 && half) break;
+              const float2 y = mul2(make_float2(x[i], x[i + 1]), k1);
+              const float2 z = add2(make_float2(exp2_approx(y.x), exp2_approx(y.y)), make_float2(1.f, 1.f));
+              const float2 w = fma2(make_float2(rcp_approx(z.x), rcp_approx(z.y)), make_float2(-2.f * c2, -2.f * c2), make_float2(c2, c2));
+              x[i] = w.x;
+              x[i + 1] = w.y;
+            }
+            mul = 1.f;
+          }
+          if (GENERAL && p.slopes) {
+            const float base = row.slope * static_cast<float>(pre - off + ch - row.pos);
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+              if (i == 32 && half) break;
+              x[i] = fmaf(x[i], mul, fmaf(row.slope, static_cast<float>(i), base));
+            }
+          }
+          if (CH == 32 && ch > 0) tt_st32(s_at + ch, reinterpret_cast<const uint32_t *>(x));
         }
-        sc = 1.f;
-      }
-      if (GENERAL && p.cap > 0.f && !masked) {
-        const float c2 = p.cap * kLog2e;
-        const float2 k1 = make_float2(sc * 2.f / p.cap, sc * 2.f / p.cap);
+        float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-          if (i == 32 && !wide) break;
-          const float2 y = mul2(make_float2(x[i], x[i + 1]), k1);
-          const float2 z = add2(make_float2(exp2_approx(y.x), exp2_approx(y.y)), make_float2(1.f, 1.f));
-          const float2 w = fma2(make_float2(rcp_approx(z.x), rcp_approx(z.y)), make_float2(-2.f * c2, -2.f * c2), make_float2(c2, c2));
-          x[i] = w.x;
-          x[i + 1] = w.y;
+        for (int i = 4; i < CH; i += 4) {
+          if (i == 32 && half) break;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], x[i + y]);
         }
-        sc = 1.f;
+        top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
       }
-      if (GENERAL && p.slopes && !masked) {
-        const float base = row.slope * static_cast<float>(pre - off - row.pos);
-#pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          if (i == 32 && !wide) break;
-          x[i] = fmaf(x[i], sc, fmaf(row.slope, static_cast<float>(i), base));
-        }
-        sc = 1.f;
-      }
-      float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-      for (int i = 4; i < 64; i += 4) {
-        if (i == 32 && !wide) break;
-#pragma unroll
-        for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], x[i + y]);
-      }
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+      if (CH == 32 && (QUANT || GENERAL) && finish_here) tt_wait_st();
+      top *= sc;
       if (s == 0) {
         ref = top;
       } else if (__any_sync(0xffffffffu, top > ref + RESCALE_STEP)) {
@@ -1094,20 +1176,26 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_o
       float2 sum[2] = {};
       const uint32_t p_at = lanes + Cfg::p_col(m, b) + first / 2;
       const auto exps = [&](auto by_token) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (half == 1 && !wide) break;
-          uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const int j = half * 32 + i;
-            const float2 y = fma2(make_float2(x[j], x[j + 1]), sc2, less2);
-            float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-            sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], e);
-            if (decltype(by_token)::value) e = mul2(e, *reinterpret_cast<const float2 *>(vs + j));
-            w[i >> 1] = pack_bf16(e.x, e.y);
+#pragma unroll 1
+        for (int ch = 0; ch < row.width; ch += CH) {
+          if (ch > 0) {
+            tt_ld32(s_at + ch, x);
+            tc_wait_ld();
           }
-          tt_st16(p_at + 16 * half, w);
+#pragma unroll
+          for (int i0 = 0; i0 < CH; i0 += 32) {
+            if (i0 == 32 && half) break;
+            uint32_t w[16];
+#pragma unroll
+            for (int i = i0; i < i0 + 32; i += 2) {
+              const float2 y = fma2(make_float2(x[i], x[i + 1]), sc2, less2);
+              float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+              sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], e);
+              if (decltype(by_token)::value) e = mul2(e, *reinterpret_cast<const float2 *>(vs + ch + i));
+              w[(i - i0) >> 1] = pack_bf16(e.x, e.y);
+            }
+            tt_st16(p_at + (ch + i0) / 2, w);   // (over columns of S that were read before)
+          }
         }
       };
       if (QUANT && scaled && !one_page)
@@ -1152,7 +1240,7 @@ __global__ void __launch_bounds__((TtCfg<D, NM, QUANT>::THREADS), 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < Cfg::NS; ++i) {
       mbar_init(&S.slot_full[i], 1);
-      mbar_init(&S.slot_empty[i], 2);   // the MMAs' reads, and the repairing or expanding warps
+      mbar_init(&S.slot_empty[i], NM + (QUANT ? 1 : 0));   // the MMAs' reads, and the expanding warps
       mbar_init(&S.raw_full[i], 1);
     }
     for (int i = 0; i < 2 * NM; ++i) {
@@ -1163,9 +1251,9 @@ __global__ void __launch_bounds__((TtCfg<D, NM, QUANT>::THREADS), 1)
     for (int i = 0; i < NM; ++i) {
       mbar_init(&S.q_full[i], 128);
       mbar_init(&S.o_free[i], 128);
+      mbar_init(&S.drain[i], 1);
     }
     for (int i = 0; i < META_RING; ++i) mbar_init(&S.meta_full[i], 1);
-    mbar_init(&S.drain, 1);
     mbar_init(&S.meet, 128);
     fence_mbar_init();
   }
@@ -1185,12 +1273,10 @@ __global__ void __launch_bounds__((TtCfg<D, NM, QUANT>::THREADS), 1)
   bool timed_out = false;
   const int wg = warp >> 2;
   if (wg == 0) {
-    if (warp == 0 || warp == 2) {
-      tt_producer<D, NM, QUANT>(c, cur, &timed_out, warp >> 1);
-    } else if (warp == 1) {
-      tt_issue<D, NM, QUANT>(c, cur, &timed_out);
-    } else if constexpr (!QUANT) {
-      tt_repair<D, NM>(c, cur, &timed_out);
+    if (warp == 0 || warp == 3) {
+      tt_producer<D, NM, QUANT>(c, cur, &timed_out, warp & 1);
+    } else if (warp <= NM) {
+      tt_issue<D, NM, QUANT>(c, cur, &timed_out, warp - 1);
     }
   } else if (wg <= NM) {
     tt_softmax<D, NM, QUANT, GENERAL>(c, cur, &timed_out);
