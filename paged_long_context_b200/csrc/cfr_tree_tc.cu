@@ -62,6 +62,7 @@ namespace {
 
 constexpr int TT = 128;        // tokens of a tile
 constexpr int META_RING = 8;   // tiles whose description is kept (see tt_producer)
+constexpr int ITEM_RING = 8;   // items published
 constexpr int MAX_PIECES = 17; // pages (of 8 tokens or more) that a tile can touch
 constexpr float RESCALE_STEP = 8.f;
 
@@ -103,21 +104,28 @@ struct TtPages {
   uint8_t fmt[PAGE_RUN];
 };
 
+struct TtNoMeta {
+  int tin0, scaled;
+};
+
 template <int NS, int NM, bool QUANT>
 struct TtSmem {
   uint64_t slot_full[NS], slot_empty[NS], raw_full[NS];
   // by row tile and, where two steps can be under way, by the step's parity: a wait by
   // parity must begin no earlier than one phase before the one it is for
   uint64_t s_full[2 * NM], p_full[2 * NM], pv_done[2 * NM], q_full[NM], o_free[NM];
-  uint64_t meta_full[META_RING], drain[NM], meet;
+  uint64_t meta_full[META_RING], drain[NM], meet, item_full[ITEM_RING];
   uint32_t tmem_base;
-  int flag[NS];
+  int flag[NS], item_go[2];
   unsigned long long nonfinite[META_RING];  // of item k & 7: drafts whose V was repaired
   int direct[NS];                           // the slot's tile needs no expansion or repair
-  TreeScratch scratch;
-  TtMeta meta[QUANT ? META_RING : 1];
+  TreeItem item[ITEM_RING];
+  typename std::conditional<QUANT, TtMeta, TtNoMeta>::type meta[QUANT ? META_RING : 1];
   uint32_t valid[META_RING][4], v_valid[META_RING][4];
-  TtPages pages[2];
+  union {
+    TtPages pages[2];
+    TreeScratch scratch;   // (before the roles begin)
+  };
   // K scale (times softmax scale and log2 e) and V scale of each token
   alignas(16) float ks[QUANT ? META_RING : 1][QUANT ? TT : 4], vs[QUANT ? META_RING : 1][QUANT ? TT : 4];
   // joining of the copies (narrow): 16 columns of O of every row, its maximum and sum
@@ -302,10 +310,16 @@ __device__ __forceinline__ bool tt_wait(uint64_t *bar, uint32_t parity, uint32_t
   return false;
 }
 
-// tree_next out of line, once for all roles
-template <int RB>
-__device__ __noinline__ bool tt_next_item(const TreeParams &p, TreeCursor &cur, TreeItem &it) {
-  return tree_next<TT, RB>(p, cur, it);
+// Item k of the CTA, published in place k & 7 by the producer of K one item ahead (walking the cut takes
+// a few microseconds, which every role would spend between items); false past the last.  A place is
+// used again 8 items later, when its readers are through: the producer is ahead of the others by its
+// slots and two steps, fewer than 8 tiles, and an item has at least one.
+template <typename Smem>
+__device__ __forceinline__ bool tt_item(const TreeParams &p, Smem &S, uint32_t k, TreeItem &it, bool *timed_out) {
+  const int i = k & (ITEM_RING - 1);
+  if (!tt_wait(&S.item_full[i], (k / ITEM_RING) & 1u, p.err, timed_out)) return false;
+  it = S.item[i];
+  return it.rows > 0;
 }
 
 // place in a ring of slots, FIRST .. FIRST + N - 1
@@ -361,7 +375,7 @@ __device__ __noinline__ void tt_repair_row(uint8_t *v, int i, bool valid, int dr
 // tile t + 4 or later were issued (there are at most 4 slots of K), which is after the softmax of
 // tile t handed over its P.
 template <int D, int NM, bool QUANT>
-__device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_out, const int KV) {
+__device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor &cur, bool *timed_out, const int KV) {
   using Cfg = TtCfg<D, NM, QUANT>;
   const TreeParams &p = c.p;
   const int lane = threadIdx.x & 31;
@@ -401,8 +415,22 @@ __device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_
     if (lane == 0) mbar_arrive(&c.S.slot_full[pend_slot]);
     pend_slot = -1;
   };
-  TreeItem item;
-  for (; !*timed_out && tt_next_item<Cfg::RB>(p, cur, item); ++k) {
+  // (the producer of K) the CTA's next item to the other roles
+  uint32_t published = 0;
+  const auto publish = [&]() {
+    if (lane == 0) {
+      TreeItem x;
+      if (!tree_next<TT, Cfg::RB>(p, cur, x)) x.rows = 0;
+      c.S.item[published & (ITEM_RING - 1)] = x;
+      mbar_arrive(&c.S.item_full[published & (ITEM_RING - 1)]);
+    }
+    ++published;
+  };
+  for (;; ++k) {
+    while (KV == 0 && published < k + 2) publish();
+    TreeItem item;
+    const bool some = tt_item(p, c.S, k, item, timed_out);
+    if (!__all_sync(0xffffffffu, some)) break;
     const TreeItem it = item;
     if (!QUANT && KV == 1 && lane == 0) c.S.nonfinite[k & (META_RING - 1)] = 0ull;
     if (KV == 0 && lane == 0 && it.bad) set_err(p.err, CFR_DEVERR_SEQ_LEN);
@@ -489,7 +517,7 @@ __device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_
       }
       uint64_t *done = direct ? &c.S.slot_full[slot_i] : &c.S.raw_full[slot_i];
       if (KV == 0) {
-        if (QUANT && lane < npiece) {
+        if constexpr (QUANT) if (lane < npiece) {
           c.S.meta[mi].fmt[lane] = ok ? static_cast<uint8_t>(fmt) : 255;
           c.S.meta[mi].ks[lane] = sc.x;
           c.S.meta[mi].vs[lane] = sc.y;
@@ -555,6 +583,7 @@ __device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_
       }
     }
     if (!*timed_out) repair();   // (the drafts are this item's)
+    if (*timed_out) break;
   }
   if (*timed_out && lane == 0) {
     // leave no copy in flight
@@ -572,16 +601,20 @@ __device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_
 // It takes part in the release of every slot, so that it is never a phase behind a
 // slot's barrier.
 template <int D, int NM>
-__device__ void tt_expand(TtCtx<D, NM, true> &c, TreeCursor cur, bool *timed_out) {
+__device__ void tt_expand(TtCtx<D, NM, true> &c, bool *timed_out) {
   using Cfg = TtCfg<D, NM, true>;
   const TreeParams &p = c.p;
   const int i = threadIdx.x - Cfg::LOADER_T0;
   KRing<Cfg> kr;
   VRing<Cfg> vr;
   uint32_t tile = 0, k = 0;
-  TreeItem item;
-  for (; tt_next_item<Cfg::RB>(p, cur, item); ++k) {
-    const TreeItem it = item;
+  for (;; ++k) {
+    // one thread waits, the barrier hands on its outcome
+    if (i == 0) c.S.item_go[k & 1] = tt_wait(&c.S.item_full[k & (ITEM_RING - 1)], (k / ITEM_RING) & 1u, p.err, timed_out) ? 1 : 0;
+    named_sync(1, 128);
+    if (!c.S.item_go[k & 1]) *timed_out = true;
+    TreeItem it;
+    if (!tt_item(p, c.S, k, it, timed_out)) return;
     const int pre = it.n - it.c;
     if (i == 0) c.S.nonfinite[k & (META_RING - 1)] = 0ull;
     for (int t = it.t1 - 1; t >= it.t0; --t, ++tile) {
@@ -707,7 +740,7 @@ __device__ void tt_expand(TtCtx<D, NM, true> &c, TreeCursor cur, bool *timed_out
 // stay in uniform registers (from a lone lane each MMA took 80 to 100 cycles to
 // issue, for 32 to 64 of tensor time).
 template <int D, int NM, bool QUANT>
-__device__ void tt_issue(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_out, int m_) {
+__device__ void tt_issue(TtCtx<D, NM, QUANT> &c, bool *timed_out, int m_) {
   using Cfg = TtCfg<D, NM, QUANT>;
   const TreeParams &p = c.p;
   const auto same = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
@@ -726,8 +759,10 @@ __device__ void tt_issue(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_out
     return __all_sync(0xffffffffu, !*timed_out) != 0;
   };
   bool go = true;
-  TreeItem item;
-  while (go && tt_next_item<Cfg::RB>(p, cur, item)) {
+  for (uint32_t k = 0; go; ++k) {
+    TreeItem item;
+    const bool some = tt_item(p, c.S, k, item, timed_out);
+    if (!__all_sync(0xffffffffu, some)) break;
     const int steps = same((item.t1 - item.t0) * Cfg::STEPS);
     if (NM == 2 && same(item.rows) <= 128 * m) {
       // no rows here: the slots go by
@@ -803,11 +838,9 @@ struct TtRow {
   bool real;
 };
 
-// This thread's row of the item, and its query as the A operand (rows past the item's
-// are zeros).
-template <int D, int NM, bool QUANT, bool GENERAL>
-__device__ __forceinline__ void tt_row(TtCtx<D, NM, QUANT> &c, const TreeItem &it, int m, int r, TtRow &w) {
-  const TreeParams &p = c.p;
+// This thread's row of the item.
+template <int D, int NM, bool GENERAL>
+__device__ __forceinline__ void tt_row(const TreeParams &p, const TreeItem &it, int m, int r, TtRow &w) {
   if (NM == 1) {
     const int lg = it.rows <= 32 ? 5 : 6;   // four copies of 32 rows, or two of 64
     w.row = r & ((1 << lg) - 1);
@@ -816,15 +849,13 @@ __device__ __forceinline__ void tt_row(TtCtx<D, NM, QUANT> &c, const TreeItem &i
   } else {
     w.row = m * 128 + r;
     w.copy = 0;
-    w.width = TtCfg<D, NM, QUANT>::STEP;
+    w.width = 128 / NM;
   }
   w.real = w.row < it.rows;
   w.bits = 0;
   w.out_row = 0;
   w.slope = 0.f;
   w.pos = 0;
-  uint8_t *q = c.q + m * TtCfg<D, NM, QUANT>::ROW_TILE;
-  const uint4 *src = nullptr;
   if (w.real) {
     int i, h;
     tree_row(p, it, it.row0 + w.row, i, h);
@@ -834,12 +865,25 @@ __device__ __forceinline__ void tt_row(TtCtx<D, NM, QUANT> &c, const TreeItem &i
       w.slope = p.slopes[h] * kLog2e;
       w.pos = it.n - it.c + (p.depths ? p.depths[static_cast<long long>(it.b) * p.nq + i] : i);
     }
-    src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.q) + w.out_row * (D * 2));
   }
+}
+
+// The row's query into the A operand (rows past the item's are zeros), asynchronously;
+// tt_show_q makes it the tensor cores' and says so.
+template <int D, int NM, bool QUANT>
+__device__ __forceinline__ void tt_load_q(TtCtx<D, NM, QUANT> &c, int m, int r, const TtRow &w) {
+  const uint32_t q = smem_u32(c.q + m * TtCfg<D, NM, QUANT>::ROW_TILE);
+  const uint8_t *src = static_cast<const uint8_t *>(c.p.q) + w.out_row * (D * 2);
+  const uint32_t bytes = w.real ? 16u : 0u;   // of 16: the rest is zeros
 #pragma unroll
   for (int ch = 0; ch < D / 8; ++ch)
-    *reinterpret_cast<uint4 *>(q + (ch >> 3) * (TT * 128) + sw128(r, ch & 7)) =
-        w.real ? src[ch] : make_uint4(0u, 0u, 0u, 0u);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(q + (ch >> 3) * (TT * 128) + sw128(r, ch & 7)),
+                 "l"(src + 16 * ch), "r"(bytes)
+                 : "memory");
+}
+template <int D, int NM, bool QUANT>
+__device__ __forceinline__ void tt_show_q(TtCtx<D, NM, QUANT> &c, int m) {
+  asm volatile("cp.async.wait_all;" ::: "memory");
   fence_async_smem();
   mbar_arrive(&c.S.q_full[m]);
 }
@@ -917,7 +961,7 @@ __device__ __noinline__ void tt_masked(const TreeParams &p, uint32_t s_at, int w
 }
 
 template <int D, int NM, bool QUANT, bool GENERAL>
-__device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_out) {
+__device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
   using Cfg = TtCfg<D, NM, QUANT>;
   const TreeParams &p = c.p;
   const int m = NM == 2 ? (threadIdx.x - Cfg::SOFTMAX_T0) >> 7 : 0;
@@ -928,7 +972,7 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_o
   // scores that a thread holds at once: a step's 64 where the code for them fits the instruction cache beside
   // the other roles (in registers throughout: 1M tokens 764 us against 865), 32 with the expansion of codes
   constexpr int CH = QUANT ? 32 : 64;
-  uint32_t cnt = 0, tile = 0, k = 0;   // steps of this row tile, tiles and items of the CTA
+  uint32_t cnt = 0, tile = 0, next_k = 0;   // steps of this row tile, tiles of the CTA, items read
   uint32_t met = 0;                    // meetings of the warpgroup's threads so far
   int zeroed = 0;                      // (narrow) the width for which P's other columns are zeros
   // every wait's outcome is the warp's: TMEM instructions are for whole warps
@@ -942,21 +986,16 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_o
     mbar_arrive(&c.S.meet);
     return wait(&c.S.meet, met++ & 1u);
   };
-  // the next item that has rows for this row tile
-  const auto advance = [&](TreeItem &it) {
-    TreeItem item;
-    while (tt_next_item<Cfg::RB>(p, cur, item)) {
-      it = item;
-      if (m * 128 < it.rows) return true;
-      tile += it.t1 - it.t0;
-      ++k;
-    }
-    return false;
+  // reads the next item: 0 if there is none, 1 if it has rows for this row tile, 2 if not
+  const auto peek = [&](TreeItem &x) {
+    const bool some = tt_item(p, c.S, next_k, x, timed_out);
+    if (!__all_sync(0xffffffffu, some)) return 0;
+    ++next_k;
+    return m * 128 < x.rows ? 1 : 2;
   };
   TreeItem it, next;
   TtRow row{}, next_row{};
   float ref = -INFINITY, l = 0.f;
-  bool open = false;                   // an item whose rows are not written out yet
   uint32_t item_of = 0;                // its number
   // joins the copies and writes an item's rows, or its partials
   const auto finish = [&]() {
@@ -1022,16 +1061,30 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_o
     }
     return true;
   };
+  next.t0 = next.t1 = 0;
+  int look = 2;
   for (;;) {
-    // the next item's queries go in before the last one's rows are written out
-    const bool more = advance(next);
-    if (more) tt_row<D, NM, QUANT, GENERAL>(c, next, m, r, next_row);
-    if (open && !finish()) return;
-    if (!more) return;
+    if (look == 2) {
+      do {
+        tile += next.t1 - next.t0;
+        look = peek(next);
+      } while (look == 2);
+      if (look == 1) {
+        tt_row<D, NM, GENERAL>(p, next, m, r, next_row);
+        tt_load_q<D, NM, QUANT>(c, m, r, next_row);
+        tt_show_q<D, NM, QUANT>(c, m);
+      }
+    }
+    if (look == 0 || *timed_out) return;
     it = next;
     row = next_row;
-    item_of = k++;
-    open = true;
+    item_of = next_k - 1;
+    // the item after this one, which is published by now (one further on is not before this one is under way):
+    // its rows are known well before its queries go in, which is when the last scores of this
+    // one are done, under their softmax
+    look = peek(next);
+    if (*timed_out) return;
+    if (look == 1) tt_row<D, NM, GENERAL>(p, next, m, r, next_row);
     const int pre = it.n - it.c;
     const int first = row.copy * row.width;   // the copy's first token of a step
     const bool wide = NM == 2 || row.width == 64;
@@ -1053,6 +1106,7 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_o
       // (scores first: they say that the tile 8 before this one was described, whatever tiles this
       // warpgroup passed over)
       if (!wait(&c.S.s_full[2 * m + b], (cnt >> 1) & 1u)) return;
+      if (look == 1 && s + 1 == steps) tt_load_q<D, NM, QUANT>(c, m, r, next_row);
       if (h == 0 && !wait(&c.S.meta_full[mi], (tile / META_RING) & 1u)) return;
       tc_fence_after();
       if (idle) {   // a warp without rows: what it leaves in P reaches no other row
@@ -1209,6 +1263,8 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, TreeCursor cur, bool *timed_o
       mbar_arrive(&c.S.p_full[2 * m + b]);
       if (h == Cfg::STEPS - 1) ++tile;
     }
+    if (look == 1) tt_show_q<D, NM, QUANT>(c, m);
+    if (!finish()) return;
   }
 }
 
@@ -1254,6 +1310,7 @@ __global__ void __launch_bounds__((TtCfg<D, NM, QUANT>::THREADS), 1)
       mbar_init(&S.drain[i], 1);
     }
     for (int i = 0; i < META_RING; ++i) mbar_init(&S.meta_full[i], 1);
+    for (int i = 0; i < ITEM_RING; ++i) mbar_init(&S.item_full[i], 1);
     mbar_init(&S.meet, 128);
     fence_mbar_init();
   }
@@ -1276,12 +1333,12 @@ __global__ void __launch_bounds__((TtCfg<D, NM, QUANT>::THREADS), 1)
     if (warp == 0 || warp == 3) {
       tt_producer<D, NM, QUANT>(c, cur, &timed_out, warp & 1);
     } else if (warp <= NM) {
-      tt_issue<D, NM, QUANT>(c, cur, &timed_out, warp - 1);
+      tt_issue<D, NM, QUANT>(c, &timed_out, warp - 1);
     }
   } else if (wg <= NM) {
-    tt_softmax<D, NM, QUANT, GENERAL>(c, cur, &timed_out);
+    tt_softmax<D, NM, QUANT, GENERAL>(c, &timed_out);
   } else if constexpr (QUANT) {
-    tt_expand<D, NM>(c, cur, &timed_out);
+    tt_expand<D, NM>(c, &timed_out);
   }
   __syncwarp();
   tc_fence_before();
