@@ -265,23 +265,30 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
   const int cut = blockIdx.x + 1;
   const long long W = tree_find<TT, RB>(
       p, scratch, tid, 256, [&](long long w) { return tree_start(w, cut, p.grid); }, cur);
-  if (cur.u >= W || W == 0) return;
-  cur.end = cur.u + 1;
-  const long long u = cur.u;
+  if (cur.u >= W) return;
+  // the item that the cut falls into, and its first unit
   TreeItem it;
-  if (!tree_next<TT, RB>(p, cur, it)) return;
-  if (it.t0 == 0) return;                                             // the cut falls between items
-  const long long first = u - it.t0, last = first + it.tiles;         // the item's units
-  if (tree_start(W, cut - 1, p.grid) > first) return;                 // an earlier cut is inside it too
-  if (tree_start(W, cut - 1, p.grid) == u) return;                    // (an empty stretch before this cut)
+  long long first;
+  {
+    const TreeSeq s = tree_seq<TT, RB>(p, cur.b);
+    const int each = s.tiles + TREE_ITEM_COST;
+    first = cur.base + (cur.u - cur.base) / each * each;
+    TreeCursor all{first, first + each, cur.base, cur.b};
+    if (!tree_next<TT, RB>(p, all, it)) return;
+  }
+  const long long last = first + it.tiles + TREE_ITEM_COST;
+  if (tree_tile(cur.u - first) == 0) return;                              // no tiles before the cut
+  const long long before = tree_start(W, cut - 1, p.grid);
+  if (before >= first && tree_tile(before - first) > 0) return;           // an earlier cut parts the item too
   const int row = blockIdx.y * 8 + warp;
   if (row >= it.rows) return;
   float M = -INFINITY, L = 0.f, acc[DV] = {};
   for (int i = cut - 1; i < p.grid; ++i) {
-    const long long lo = tree_start(W, i, p.grid);
+    const long long lo = tree_start(W, i, p.grid), hi = tree_start(W, i + 1, p.grid);
     if (lo >= last) break;
-    if (tree_start(W, i + 1, p.grid) == lo) continue;
-    const long long s = (2LL * i + (lo > first ? 0 : 1)) * RB + row;
+    const int t0 = lo <= first ? 0 : tree_tile(lo - first), t1 = tree_tile(min(hi, last) - first);
+    if (t0 >= t1) continue;
+    const long long s = (2LL * i + (t0 > 0 ? 0 : 1)) * RB + row;
     const float m = p.part_m[s], l = p.part_l[s];
     if (l == 0.f) continue;
     const float mn = fmaxf(M, m);

@@ -5,7 +5,8 @@
 // rows); it spans the ceil(n_b / TT) token tiles of the sequence.  The tiles of
 // all items, in that order, are one line of W units, and CTA i of G takes the
 // units [W i / G, W (i + 1) / G): every CTA gets the same number of tiles
-// whatever the lengths.  A CTA's stretch covers at most one item's end, whole
+// whatever the lengths (an item counts as TREE_ITEM_COST tiles more than it has, for what beginning and
+// ending one takes; those units come before its first tile).  A CTA's stretch covers at most one item's end, whole
 // items, and one item's beginning, so it leaves at most two partials: slot 2 i
 // for an item that began in an earlier CTA, 2 i + 1 for one that goes on in a
 // later one.  Whole items are written out at once.  Every kernel computes the
@@ -15,6 +16,8 @@
 #include "cfr_common.cuh"
 
 namespace cfr {
+
+constexpr int TREE_ITEM_COST = 2;
 
 struct TreeParams {
   const void *q;
@@ -55,6 +58,14 @@ template <int TT, int RB>
 __device__ __forceinline__ int tree_blocks(const TreeParams &p, int c, int g) {
   const int cnt = p.heads_each ? p.heads_each : p.head_off[g + 1] - p.head_off[g];
   return (c * cnt + RB - 1) / RB;
+}
+
+// Units of a sequence's items, and the tile at unit `off` of an item.
+__device__ __forceinline__ long long tree_units(const TreeSeq &s) {
+  return static_cast<long long>(s.blocks) * (s.tiles + TREE_ITEM_COST);
+}
+__device__ __forceinline__ int tree_tile(long long off) {
+  return off > TREE_ITEM_COST ? static_cast<int>(off - TREE_ITEM_COST) : 0;
 }
 
 template <int TT, int RB>
@@ -116,7 +127,7 @@ __device__ __forceinline__ long long tree_find(const TreeParams &p, TreeScratch 
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
     const TreeSeq q = tree_seq<TT, RB>(p, b);
-    mine += static_cast<long long>(q.blocks) * q.tiles;
+    mine += tree_units(q);
   }
   long long incl = mine;
   const int lane = tid & 31;
@@ -139,7 +150,7 @@ __device__ __forceinline__ long long tree_find(const TreeParams &p, TreeScratch 
     int b = b0;
     for (;; ++b) {
       const TreeSeq q = tree_seq<TT, RB>(p, b);
-      const long long units = static_cast<long long>(q.blocks) * q.tiles;
+      const long long units = tree_units(q);
       if (u < at + units) break;
       at += units;
     }
@@ -153,19 +164,27 @@ __device__ __forceinline__ long long tree_find(const TreeParams &p, TreeScratch 
   return W;
 }
 
-// The next piece of the stretch; false at its end.
+// The next piece of the stretch that has tiles; false at its end.
 template <int TT, int RB>
 __device__ __forceinline__ bool tree_next(const TreeParams &p, TreeCursor &cur, TreeItem &it) {
-  if (cur.u >= cur.end) return false;
-  TreeSeq s = tree_seq<TT, RB>(p, cur.b);
-  while (cur.u >= cur.base + static_cast<long long>(s.blocks) * s.tiles) {
-    cur.base += static_cast<long long>(s.blocks) * s.tiles;
-    s = tree_seq<TT, RB>(p, ++cur.b);
-  }
-  const long long off = cur.u - cur.base;
-  int item = static_cast<int>(off / s.tiles);
-  it.t0 = static_cast<int>(off - static_cast<long long>(item) * s.tiles);
-  it.t1 = static_cast<int>(min(static_cast<long long>(s.tiles), it.t0 + (cur.end - cur.u)));
+  TreeSeq s;
+  int item;
+  do {
+    if (cur.u >= cur.end) return false;
+    s = tree_seq<TT, RB>(p, cur.b);
+    while (cur.u >= cur.base + tree_units(s)) {
+      cur.base += tree_units(s);
+      s = tree_seq<TT, RB>(p, ++cur.b);
+    }
+    const int each = s.tiles + TREE_ITEM_COST;
+    const long long off = cur.u - cur.base;
+    item = static_cast<int>(off / each);
+    const long long in = off - static_cast<long long>(item) * each;   // units of the item before u
+    const long long to = min(static_cast<long long>(each), in + (cur.end - cur.u));
+    it.t0 = tree_tile(in);
+    it.t1 = tree_tile(to);
+    cur.u += to - in;
+  } while (it.t0 == it.t1);
   it.tiles = s.tiles;
   it.b = cur.b;
   it.c = s.c;
@@ -182,7 +201,6 @@ __device__ __forceinline__ bool tree_next(const TreeParams &p, TreeCursor &cur, 
   it.cnt = p.head_off[it.g + 1] - p.head_off[it.g];
   it.row0 = item * RB;
   it.rows = min(RB, s.c * it.cnt - it.row0);
-  cur.u += it.t1 - it.t0;
   return true;
 }
 

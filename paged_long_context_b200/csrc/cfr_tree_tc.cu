@@ -267,22 +267,12 @@ __device__ __forceinline__ void expand16(int fmt, uint4 v, uint32_t (&o)[N]) {
   }
 }
 
-// clears the non-finite bf16 values of a word; true when there was one
-__device__ __forceinline__ bool repair_word(uint32_t &w) {
-  bool bad = false;
-  if ((w & 0x7F80u) == 0x7F80u) {
-    w &= 0xFFFF0000u;
-    bad = true;
-  }
-  if ((w & 0x7F800000u) == 0x7F800000u) {
-    w &= 0x0000FFFFu;
-    bad = true;
-  }
-  return bad;
-}
-__device__ __forceinline__ bool repair16(uint4 &v) {
-  const bool a = repair_word(v.x), b = repair_word(v.y), c = repair_word(v.z), d = repair_word(v.w);
-  return a || b || c || d;
+// true when a bf16 pair holds a non-finite value: its exponent of ones carries into the sign's place
+__device__ __forceinline__ uint32_t nonfinite_pair(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+// clears the non-finite values of a pair
+__device__ __forceinline__ uint32_t repair_pair(uint32_t w) {
+  const uint32_t bad = nonfinite_pair(w) >> 15;   // bit 0 and bit 16
+  return w & ~(bad * 0xFFFFu);
 }
 
 template <int D, int NM, bool QUANT>
@@ -350,9 +340,9 @@ __device__ __noinline__ void tt_repair_row(uint8_t *v, int i, bool valid, int dr
     if (!valid) {
       *at = make_uint4(0u, 0u, 0u, 0u);
     } else {
-      uint4 w = *at;
-      if (repair16(w)) {
-        *at = w;
+      const uint4 w = *at;
+      if (nonfinite_pair(w.x) | nonfinite_pair(w.y) | nonfinite_pair(w.z) | nonfinite_pair(w.w)) {
+        *at = make_uint4(repair_pair(w.x), repair_pair(w.y), repair_pair(w.z), repair_pair(w.w));
         bad = true;
       }
     }
@@ -910,6 +900,29 @@ __device__ __forceinline__ void tt_add_back(const TreeParams &p, const TreeItem 
   }
 }
 
+// The 16 values of each of four neighbouring lanes' rows, exchanged so that lane j holds values 4 j .. 4 j + 3
+// of all four rows (o[4 k ..]: row k).  Four lanes then write 64 bytes of a row; a lane writing
+// its own row touches a line for itself, and the lines of an item took longer than its tiles' exponentials.
+__device__ __forceinline__ void tt_turn4(float (&o)[16], int lane) {
+#pragma unroll
+  for (int step = 2; step >= 1; step >>= 1) {
+    const bool up = lane & step;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      if (b & step) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float &lo = o[4 * b + i], &hi = o[4 * (b + step) + i];
+        const float got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, step);
+        if (up)
+          lo = got;
+        else
+          hi = got;
+      }
+    }
+  }
+}
+
 // N finished output values of a row (or, where `part`, of its partial) from column col on
 template <int N>
 __device__ __forceinline__ void tt_put(const TreeParams &p, bool part, long long row, int col, const float *o) {
@@ -1021,6 +1034,9 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
     }
     if (whole) f = l_all == 0.f ? 0.f : f / l_all;
     const int share = 16 / copies;   // columns of 16 that a copy's thread puts together
+    long long to4[4];   // (wide) the four lanes' rows, -1: none
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to4[i] = __shfl_sync(0xffffffffu, row.real ? to_row : -1ll, (r & 28) + i);
 #pragma unroll 1
     for (int ch = 0; ch < D / 16; ++ch) {
       float o[16];
@@ -1030,7 +1046,13 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[i] = l_all == 0.f ? 0.f : o[i] * f;
       if (NM == 2) {
-        if (row.real) tt_put<16>(p, !whole, to_row, 16 * ch, o);
+        tt_turn4(o, r & 31);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (to4[i] >= 0) {
+            const float v[4] = {o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]};
+            tt_put<4>(p, !whole, to4[i], 16 * ch + 4 * (r & 3), v);
+          }
       } else {
         float4 *at = reinterpret_cast<float4 *>(c.S.join[r]);
 #pragma unroll
