@@ -77,10 +77,11 @@ struct TtCfg {
   static constexpr int NK = D == 128 ? 2 : 4;
   static constexpr int NV = (D == 128 ? 1 : 2) * (NM == 2 && QUANT ? 2 : 3);
   static constexpr int NS = NK + NV;
-  static constexpr int WGS = 1 + NM + (QUANT ? 1 : 0);
+  // expanding warpgroups: K and V in turn by one where registers allow no more, else one for each
+  static constexpr int LOADERS = QUANT ? (NM == 1 ? 2 : 1) : 0;
+  static constexpr int WGS = 1 + NM + LOADERS;
   static constexpr int THREADS = 128 * WGS;
   static constexpr int SOFTMAX_T0 = 128;
-  static constexpr int LOADER_T0 = 128 * (1 + NM);
   // TMEM columns: S, two buffers of STEP for each row tile; O, 128 for each; narrow: P, two
   // buffers of its own, so that the zeros of other copies' tokens stay (wide: P over its S)
   static constexpr int TMEM_COLS = 512;
@@ -116,7 +117,7 @@ struct TtSmem {
   uint64_t s_full[2 * NM], p_full[2 * NM], pv_done[2 * NM], q_full[NM], o_free[NM];
   uint64_t meta_full[META_RING], drain[NM], meet, item_full[ITEM_RING];
   uint32_t tmem_base;
-  int flag[NS], item_go[2];
+  int flag[NS], expand_go[2][2];
   unsigned long long nonfinite[META_RING];  // of item k & 7: drafts whose V was repaired
   int direct[NS];                           // the slot's tile needs no expansion or repair
   TreeItem item[ITEM_RING];
@@ -236,35 +237,6 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf2(uint32_t w, int i) {
   const uint32_t h = e4m3x2_to_h2(w, i);
   const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
   return pack_bf16(f.x, f.y);
-}
-
-// 16 bytes of codes as bf16 words: 8 words (int8, E4M3) or 16 (int4)
-template <int N>
-__device__ __forceinline__ void expand16(int fmt, uint4 v, uint32_t (&o)[N]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  if constexpr (N == 16) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t x = w[q] ^ 0x88888888u;
-      const uint32_t lo = x & 0x0F0F0F0Fu, hi = (x >> 4) & 0x0F0F0F0Fu;
-      o[4 * q + 0] = i4x2_to_bf2(lo, hi, 0x4400u);
-      o[4 * q + 1] = i4x2_to_bf2(lo, hi, 0x5511u);
-      o[4 * q + 2] = i4x2_to_bf2(lo, hi, 0x6622u);
-      o[4 * q + 3] = i4x2_to_bf2(lo, hi, 0x7733u);
-    }
-  } else if (fmt == CFR_FMT_I8) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      o[2 * q] = i8x2_to_bf2(w[q], 0x4140u);
-      o[2 * q + 1] = i8x2_to_bf2(w[q], 0x4342u);
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      o[2 * q] = e4m3x2_to_bf2(w[q], 0);
-      o[2 * q + 1] = e4m3x2_to_bf2(w[q], 1);
-    }
-  }
 }
 
 // true when a bf16 pair holds a non-finite value: its exponent of ones carries into the sign's place
@@ -587,107 +559,133 @@ __device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor &cur, bool *timed
 
 // ---- expansion -------------------------------------------------------------------
 
+// Eight bytes of codes a 32-bit word at a time: int8 and E4M3 codes give two bf16 words
+// a word, int4 codes four.
+template <int FMT>
+__device__ __forceinline__ void expand_word(uint32_t w, uint32_t *o) {
+  if constexpr (FMT == CFR_FMT_I8) {
+    o[0] = i8x2_to_bf2(w, 0x4140u);
+    o[1] = i8x2_to_bf2(w, 0x4342u);
+  } else if constexpr (FMT == CFR_FMT_FP8) {
+    o[0] = e4m3x2_to_bf2(w, 0);
+    o[1] = e4m3x2_to_bf2(w, 1);
+  } else {
+    const uint32_t x = w ^ 0x88888888u;
+    const uint32_t lo = x & 0x0F0F0F0Fu, hi = (x >> 4) & 0x0F0F0F0Fu;
+    o[0] = i4x2_to_bf2(lo, hi, 0x4400u);
+    o[1] = i4x2_to_bf2(lo, hi, 0x5511u);
+    o[2] = i4x2_to_bf2(lo, hi, 0x6622u);
+    o[3] = i4x2_to_bf2(lo, hi, 0x7733u);
+  }
+}
+
+// 64 values of row i, N 16-byte pieces of codes in the order (x + turn) mod N, into one half of a slot
+template <int FMT, int N>
+__device__ __forceinline__ void expand_half(uint8_t *half, int i, int turn, const uint4 (&raw)[N]) {
+#pragma unroll
+  for (int x = 0; x < N; ++x) {
+    const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+    const int ci = (x + turn) & (N - 1);
+#pragma unroll
+    for (int y = 0; y < 8 / N; ++y) {   // 16 bytes of bf16
+      uint32_t o[4];
+      if constexpr (N == 4) {
+        expand_word<FMT>(w[2 * y], o);
+        expand_word<FMT>(w[2 * y + 1], o + 2);
+      } else {
+        expand_word<FMT>(w[y], o);
+      }
+      *reinterpret_cast<uint4 *>(half + sw128(i, ci * (8 / N) + y)) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+}
+
 // Expansion (and V repair) of caches with quantised pages: thread i owns row i.
-// It takes part in the release of every slot, so that it is never a phase behind a
-// slot's barrier.
+// `which`: K slots (0), V slots (1) or both in turn (2).  It takes part in the release
+// of every slot, so that it is never a phase behind a slot's barrier.  What bounds it is
+// the latency of one warp's chain on each scheduler, hence a warpgroup each for K and V.
 template <int D, int NM>
-__device__ void tt_expand(TtCtx<D, NM, true> &c, bool *timed_out) {
+__device__ void tt_expand(TtCtx<D, NM, true> &c, bool *timed_out, const int which) {
   using Cfg = TtCfg<D, NM, true>;
   const TreeParams &p = c.p;
-  const int i = threadIdx.x - Cfg::LOADER_T0;
+  const int i = threadIdx.x & 127;
+  const int bar = 1 + (which & 1);
   KRing<Cfg> kr;
   VRing<Cfg> vr;
-  uint32_t tile = 0, k = 0;
-  for (;; ++k) {
+  uint32_t tile = 0;
+  for (uint32_t k = 0;; ++k) {
     // one thread waits, the barrier hands on its outcome
-    if (i == 0) c.S.item_go[k & 1] = tt_wait(&c.S.item_full[k & (ITEM_RING - 1)], (k / ITEM_RING) & 1u, p.err, timed_out) ? 1 : 0;
-    named_sync(1, 128);
-    if (!c.S.item_go[k & 1]) *timed_out = true;
+    int *go = &c.S.expand_go[which & 1][k & 1];
+    if (i == 0) *go = tt_wait(&c.S.item_full[k & (ITEM_RING - 1)], (k / ITEM_RING) & 1u, p.err, timed_out) ? 1 : 0;
+    named_sync(bar, 128);
+    if (!*go) *timed_out = true;
     TreeItem it;
     if (!tt_item(p, c.S, k, it, timed_out)) return;
     const int pre = it.n - it.c;
-    if (i == 0) c.S.nonfinite[k & (META_RING - 1)] = 0ull;
+    if (i == 0 && which) c.S.nonfinite[k & (META_RING - 1)] = 0ull;
     for (int t = it.t1 - 1; t >= it.t0; --t, ++tile) {
       const int mi = tile & (META_RING - 1);
       const TtMeta &m = c.S.meta[mi];
-      int fmt = 255, a = 0;
-      bool valid = false;
-      for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll 1
+      for (int kv = which == 1 ? 1 : 0; kv < (which == 0 ? 1 : 2); ++kv) {
         const int slot = kv ? vr.s : kr.s;
         const uint32_t ph = kv ? vr.ph : kr.ph;
-        // one thread waits, the barrier hands on its outcome
-        if (i == 0) c.S.flag[slot] = tt_wait(&c.S.raw_full[slot], ph, p.err, timed_out) ? 1 : 0;
-        named_sync(1, 128);
+        if (i == 0) {
+          // (the description of the tile is K's; the warpgroup of V has it by meta_full)
+          bool got = which != 1 || tt_wait(&c.S.meta_full[mi], (tile / META_RING) & 1u, p.err, timed_out);
+          got = got && tt_wait(&c.S.raw_full[slot], ph, p.err, timed_out);
+          c.S.flag[slot] = got ? 1 : 0;
+        }
+        named_sync(bar, 128);
         if (!c.S.flag[slot]) {
           *timed_out = true;
           return;
         }
         (void)mbar_try_wait(&c.S.raw_full[slot], ph);
+        if (which == 1) (void)mbar_try_wait(&c.S.meta_full[mi], (tile / META_RING) & 1u);
         const bool direct = c.S.direct[slot];
         const bool any4 = m.scaled & 2;   // 4-bit rows among the tile's
+        const bool valid = (c.S.valid[mi][i >> 5] >> (i & 31)) & 1u;
+        const int pc = (m.tin0 + i) / p.P;
+        const int fmt = valid ? m.fmt[pc] : 255;
         if (kv == 0) {
-          valid = (c.S.valid[mi][i >> 5] >> (i & 31)) & 1u;
-          const int pc = (m.tin0 + i) / p.P;
-          fmt = valid ? m.fmt[pc] : 255;
-          a = pc == 0 ? 0 : pc * p.P - m.tin0;
           c.S.ks[mi][i] = valid ? m.ks[pc] * (p.sigma * kLog2e) : 0.f;
           c.S.vs[mi][i] = valid ? m.vs[pc] : 0.f;
         }
         if (!direct) {
           uint8_t *op = c.slot(slot);
+          const int a = pc == 0 ? 0 : pc * p.P - m.tin0;   // first row of the row's page
           const bool eight = fmt == CFR_FMT_I8 || fmt == CFR_FMT_FP8, four = fmt == CFR_FMT_I4;
           const int draft = t * TT + i - pre;
-          const bool look = kv == 1 && fmt == CFR_FMT_FP8 && draft >= 0;   // E4M3 has NaN
-          // 64 values at a time (a row of one half of the slot), so that the code stays small;
-          // rows are read in an order that spreads a warp's lanes over the banks
-          const auto put8 = [&](const uint4 (&raw)[4], int hh) {
-#pragma unroll 1
-            for (int x = 0; x < 4; ++x) {
-              const int ci = (x + i) & 3;   // codes 16 ci .. of the 64
-              const uint4 w = x == 0 ? raw[0] : x == 1 ? raw[1] : x == 2 ? raw[2] : raw[3];
-              uint32_t o[8];
-              expand16<8>(fmt, w, o);
-              uint8_t *hb = op + hh * (TT * 128);
-              *reinterpret_cast<uint4 *>(hb + sw128(i, 2 * ci)) = make_uint4(o[0], o[1], o[2], o[3]);
-              *reinterpret_cast<uint4 *>(hb + sw128(i, 2 * ci + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
-            }
-          };
-          const auto put4 = [&](const uint4 (&raw)[2], int hh) {
-#pragma unroll 1
-            for (int x = 0; x < 2; ++x) {
-              const int ci = (x + (i >> 1)) & 1;   // codes 32 ci .. of the 64
-              uint32_t o[16];
-              expand16<16>(fmt, x == 0 ? raw[0] : raw[1], o);
-              uint8_t *hb = op + hh * (TT * 128);
-#pragma unroll
-              for (int y = 0; y < 4; ++y)
-                *reinterpret_cast<uint4 *>(hb + sw128(i, 4 * ci + y)) =
-                    make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
-            }
-          };
+          // 64 values at a time (a row of one half of the slot); codes are read in an order that
+          // spreads a warp's lanes over the banks
           if (D == 128) {
             // 8-bit rows lie where the row's first half goes, so each thread overwrites its own; 4-bit rows
             // lie in the second half's place of their page's rows, which is written once all were read
-            uint4 raw4[2];
-            if (eight) {
+            const uint8_t *src = op + TT * 128 + a * 128 + (i - a) * 64;
 #pragma unroll 1
-              for (int hh = 1; hh >= 0; --hh) {
+            for (int hh = 1; hh >= 0; --hh) {
+              if (eight) {
                 uint4 raw[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
                   raw[x] = *reinterpret_cast<const uint4 *>(op + i * 128 + hh * 64 + 16 * ((x + i) & 3));
-                put8(raw, hh);
+                if (fmt == CFR_FMT_I8)
+                  expand_half<CFR_FMT_I8, 4>(op + hh * (TT * 128), i, i, raw);
+                else
+                  expand_half<CFR_FMT_FP8, 4>(op + hh * (TT * 128), i, i, raw);
               }
-            }
-            const uint8_t *src = op + TT * 128 + a * 128 + (i - a) * 64;
-#pragma unroll 1
-            for (int hh = 0; hh < 2; ++hh) {
-              if (four)
+              if (any4) {
+                const int h4 = hh ^ 1;   // first half first
+                uint4 raw[2];
+                if (four) {
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
-                  raw4[x] = *reinterpret_cast<const uint4 *>(src + hh * 32 + 16 * ((x + (i >> 1)) & 1));
-              if (hh == 1 && any4) named_sync(1, 128);
-              if (four) put4(raw4, hh);
+                  for (int x = 0; x < 2; ++x)
+                    raw[x] = *reinterpret_cast<const uint4 *>(src + h4 * 32 + 16 * ((x + (i >> 1)) & 1));
+                }
+                if (h4 == 1) named_sync(bar, 128);
+                if (four) expand_half<CFR_FMT_I4, 2>(op + h4 * (TT * 128), i, i >> 1, raw);
+              }
             }
           } else {
             uint4 raw[4], raw4[2];
@@ -699,15 +697,17 @@ __device__ void tt_expand(TtCtx<D, NM, true> &c, bool *timed_out) {
 #pragma unroll
               for (int x = 0; x < 2; ++x) raw4[x] = *reinterpret_cast<const uint4 *>(src + 16 * ((x + (i >> 1)) & 1));
             }
-            named_sync(1, 128);  // every row is in registers before any is written
-            if (eight) put8(raw, 0);
-            if (four) put4(raw4, 0);
+            named_sync(bar, 128);  // every row is in registers before any is written
+            if (fmt == CFR_FMT_I8) expand_half<CFR_FMT_I8, 4>(op, i, i, raw);
+            if (fmt == CFR_FMT_FP8) expand_half<CFR_FMT_FP8, 4>(op, i, i, raw);
+            if (four) expand_half<CFR_FMT_I4, 2>(op, i, i >> 1, raw4);
           }
-          if (kv == 1 && (eight || four ? look : !valid || draft >= 0))
+          // a V row without a token, or of a draft (int8 and int4 codes are finite)
+          if (kv == 1 && (eight || four ? fmt == CFR_FMT_FP8 && draft >= 0 : !valid || draft >= 0))
             tt_repair_row<D>(op, i, valid, draft, &c.S.nonfinite[k & (META_RING - 1)]);
           fence_async_smem();
         }
-        named_sync(1, 128);
+        named_sync(bar, 128);
         if (i == 0) {
           if (!direct) mbar_arrive(&c.S.slot_full[slot]);
           if (kv == 0) mbar_arrive(&c.S.meta_full[mi]);
@@ -1360,7 +1360,7 @@ __global__ void __launch_bounds__((TtCfg<D, NM, QUANT>::THREADS), 1)
   } else if (wg <= NM) {
     tt_softmax<D, NM, QUANT, GENERAL>(c, &timed_out);
   } else if constexpr (QUANT) {
-    tt_expand<D, NM>(c, &timed_out);
+    tt_expand<D, NM>(c, &timed_out, Cfg::LOADERS == 1 ? 2 : wg - NM - 1);
   }
   __syncwarp();
   tc_fence_before();
