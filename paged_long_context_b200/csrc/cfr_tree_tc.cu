@@ -579,13 +579,14 @@ __device__ __forceinline__ void expand_word(uint32_t w, uint32_t *o) {
   }
 }
 
-// 64 values of row i, N 16-byte pieces of codes in the order (x + turn) mod N, into one half of a slot
+// 64 values of a row, N 16-byte pieces of codes in the order (x + turn) mod N, into one half
+// of a slot; `row` is the row's place there and `swz` its swizzle, (row mod 8) * 16.
 template <int FMT, int N>
-__device__ __forceinline__ void expand_half(uint8_t *half, int i, int turn, const uint4 (&raw)[N]) {
+__device__ __forceinline__ void expand_half(uint32_t row, uint32_t swz, int turn, const uint4 (&raw)[N]) {
 #pragma unroll
   for (int x = 0; x < N; ++x) {
     const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
-    const int ci = (x + turn) & (N - 1);
+    const uint32_t at = static_cast<uint32_t>((x + turn) & (N - 1)) * (128 / N);   // its first byte in the row
 #pragma unroll
     for (int y = 0; y < 8 / N; ++y) {   // 16 bytes of bf16
       uint32_t o[4];
@@ -595,9 +596,16 @@ __device__ __forceinline__ void expand_half(uint8_t *half, int i, int turn, cons
       } else {
         expand_word<FMT>(w[y], o);
       }
-      *reinterpret_cast<uint4 *>(half + sw128(i, ci * (8 / N) + y)) = make_uint4(o[0], o[1], o[2], o[3]);
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((at + 16 * y) ^ swz)), "r"(o[0]), "r"(o[1]),
+                   "r"(o[2]), "r"(o[3])
+                   : "memory");
     }
   }
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
 }
 
 // Expansion (and V repair) of caches with quantised pages: thread i owns row i.
@@ -646,7 +654,7 @@ __device__ void tt_expand(TtCtx<D, NM, true> &c, bool *timed_out, const int whic
         const bool direct = c.S.direct[slot];
         const bool any4 = m.scaled & 2;   // 4-bit rows among the tile's
         const bool valid = (c.S.valid[mi][i >> 5] >> (i & 31)) & 1u;
-        const int pc = (m.tin0 + i) / p.P;
+        const int pc = p.P >= TT ? (m.tin0 + i >= p.P ? 1 : 0) : (m.tin0 + i) / p.P;
         const int fmt = valid ? m.fmt[pc] : 255;
         if (kv == 0) {
           c.S.ks[mi][i] = valid ? m.ks[pc] * (p.sigma * kLog2e) : 0.f;
@@ -659,48 +667,47 @@ __device__ void tt_expand(TtCtx<D, NM, true> &c, bool *timed_out, const int whic
           const int draft = t * TT + i - pre;
           // 64 values at a time (a row of one half of the slot); codes are read in an order that
           // spreads a warp's lanes over the banks
+          const uint32_t base = smem_u32(op), row = base + i * 128, swz = (i & 7) * 16;
           if (D == 128) {
             // 8-bit rows lie where the row's first half goes, so each thread overwrites its own; 4-bit rows
             // lie in the second half's place of their page's rows, which is written once all were read
-            const uint8_t *src = op + TT * 128 + a * 128 + (i - a) * 64;
+            const uint32_t src = base + TT * 128 + a * 128 + (i - a) * 64;
 #pragma unroll 1
             for (int hh = 1; hh >= 0; --hh) {
               if (eight) {
                 uint4 raw[4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                  raw[x] = *reinterpret_cast<const uint4 *>(op + i * 128 + hh * 64 + 16 * ((x + i) & 3));
+                for (int x = 0; x < 4; ++x) raw[x] = ld_shared16(row + hh * 64 + 16 * ((x + i) & 3));
                 if (fmt == CFR_FMT_I8)
-                  expand_half<CFR_FMT_I8, 4>(op + hh * (TT * 128), i, i, raw);
+                  expand_half<CFR_FMT_I8, 4>(row + hh * (TT * 128), swz, i, raw);
                 else
-                  expand_half<CFR_FMT_FP8, 4>(op + hh * (TT * 128), i, i, raw);
+                  expand_half<CFR_FMT_FP8, 4>(row + hh * (TT * 128), swz, i, raw);
               }
               if (any4) {
                 const int h4 = hh ^ 1;   // first half first
                 uint4 raw[2];
                 if (four) {
 #pragma unroll
-                  for (int x = 0; x < 2; ++x)
-                    raw[x] = *reinterpret_cast<const uint4 *>(src + h4 * 32 + 16 * ((x + (i >> 1)) & 1));
+                  for (int x = 0; x < 2; ++x) raw[x] = ld_shared16(src + h4 * 32 + 16 * ((x + (i >> 1)) & 1));
                 }
                 if (h4 == 1) named_sync(bar, 128);
-                if (four) expand_half<CFR_FMT_I4, 2>(op + h4 * (TT * 128), i, i >> 1, raw);
+                if (four) expand_half<CFR_FMT_I4, 2>(row + h4 * (TT * 128), swz, i >> 1, raw);
               }
             }
           } else {
             uint4 raw[4], raw4[2];
-            const uint8_t *src = op + a * 128 + (i - a) * row_bytes(eight ? CFR_FMT_I8 : CFR_FMT_I4, D);
+            const uint32_t src = base + a * 128 + (i - a) * (eight ? D : D / 2);
             if (eight) {
 #pragma unroll
-              for (int x = 0; x < 4; ++x) raw[x] = *reinterpret_cast<const uint4 *>(src + 16 * ((x + i) & 3));
+              for (int x = 0; x < 4; ++x) raw[x] = ld_shared16(src + 16 * ((x + i) & 3));
             } else if (four) {
 #pragma unroll
-              for (int x = 0; x < 2; ++x) raw4[x] = *reinterpret_cast<const uint4 *>(src + 16 * ((x + (i >> 1)) & 1));
+              for (int x = 0; x < 2; ++x) raw4[x] = ld_shared16(src + 16 * ((x + (i >> 1)) & 1));
             }
             named_sync(bar, 128);  // every row is in registers before any is written
-            if (fmt == CFR_FMT_I8) expand_half<CFR_FMT_I8, 4>(op, i, i, raw);
-            if (fmt == CFR_FMT_FP8) expand_half<CFR_FMT_FP8, 4>(op, i, i, raw);
-            if (four) expand_half<CFR_FMT_I4, 2>(op, i, i >> 1, raw4);
+            if (fmt == CFR_FMT_I8) expand_half<CFR_FMT_I8, 4>(row, swz, i, raw);
+            if (fmt == CFR_FMT_FP8) expand_half<CFR_FMT_FP8, 4>(row, swz, i, raw);
+            if (four) expand_half<CFR_FMT_I4, 2>(row, swz, i >> 1, raw4);
           }
           // a V row without a token, or of a draft (int8 and int4 codes are finite)
           if (kv == 1 && (eight || four ? fmt == CFR_FMT_FP8 && draft >= 0 : !valid || draft >= 0))
