@@ -318,44 +318,66 @@ def append_kv(pool: KvPool, page_table, page_fmt, uniform_fmt: int, positions, k
                                    _stream(stream)))
 
 
-def _want(name: str, t, dtypes, shape=None, strided_tokens=False, none_ok=False):
-    """Checks what the C ABI cannot see of a tensor argument: its type, shape, layout and
-    device.  strided_tokens: rows may be any distance apart, each row is contiguous."""
-    if t is None:
-        if none_ok:
-            return
-        raise ValueError(f"{name}: a tensor is required")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: {t.dtype} where {' or '.join(map(str, dtypes))} is wanted")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)} where {tuple(shape)} is wanted")
-    if strided_tokens:
-        if t.dim() != 3 or (t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]))):
-            raise ValueError(f"{name}: each token's [heads][head_dim] values must be contiguous")
-    elif not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {t.device}, while device {torch.cuda.current_device()} is current")
 
-
-_INT32 = (torch.int32,)
+_I32S, _I64S, _U8S, _F32S, _F64S = (torch.int32,), (torch.int64, torch.uint64), (torch.uint8,), \
+    (torch.float32,), (torch.float64,)
 _HOT = (torch.float32, torch.bfloat16)
 
 
-def _fmt_of(t) -> int:
-    return synth.F32 if t.dtype == torch.float32 else synth.BF16
+def _device() -> int:
+    """The current CUDA device, -1 before CUDA is initialised (the device of host tensors)."""
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
 
 
-def _token_stride(t) -> int:
-    """Values from one token's row to the next (a single row's stride is free: its own size)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+def _raw_stream(stream, dev: int) -> int:
+    """A cudaStream_t as a number; the current stream of the device when none is given."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else 0
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _want_table(page_table, page_fmt):
-    _want("page_table", page_table, _INT32)
-    if page_table.dim() != 2:
-        raise ValueError("page_table: [batch][max_pages] is wanted")
-    _want("page_fmt", page_fmt, (torch.uint8,), page_table.shape, none_ok=True)
+def _refuse(name, t, dtypes, shape, dev, layout):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: a tensor is required")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: {t.dtype} where {' or '.join(map(str, dtypes))} is wanted")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} where {tuple(shape)} is wanted")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, where {'the host' if dev < 0 else f'cuda:{dev}, the current device,'} is wanted")
+    raise ValueError(f"{name}: {layout}")
+
+
+def _want(name, t, dtypes, shape, dev):
+    """Address of a contiguous tensor argument, after the checks that the C ABI cannot make: its
+    type, shape, layout and device (shape None: any)."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and (shape is None or t.shape == shape) \
+            and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    _refuse(name, t, dtypes, shape, dev, "must be contiguous")
+
+
+def _may(name, t, dtypes, shape, dev):
+    return None if t is None else _want(name, t, dtypes, shape, dev)
+
+
+def _want_rows(name, t, dtypes, shape, dev):
+    """Address and token stride (in values) of a [tokens][heads][head_dim] argument whose tokens may
+    be any distance apart; each token's values are contiguous."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == dev:
+        n, heads, d = shape
+        st = t.stride()
+        if n * heads == 0 or (st[2] == 1 and (heads == 1 or st[1] == d)):
+            # (a single row's stride is free: its own size)
+            return t.data_ptr(), st[0] if n > 1 else heads * d
+    _refuse(name, t, dtypes, shape, dev, "each token's [heads][head_dim] values must be contiguous")
+
+
+def _want_table(page_table, page_fmt, dev):
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table: an int32 tensor [batch][max_pages] is wanted")
+    return (_want("page_table", page_table, _I32S, page_table.shape, dev),
+            _may("page_fmt", page_fmt, _U8S, page_table.shape, dev))
 
 
 def qk_norm_rope_append(pool: KvPool, q, k, v, rope_positions, inv_freq, q_out, page_table, page_fmt,
@@ -364,56 +386,60 @@ def qk_norm_rope_append(pool: KvPool, q, k, v, rope_positions, inv_freq, q_out, 
     """cfr_qk_norm_rope_append: norm and rotate a step's queries and keys, and write its K and V
     into F32 / BF16 pages; q, k, v are [tokens][heads][head_dim] (views of a packed projection are
     fine); returns the status."""
-    n, d = q.shape[0], pool.head_dim
-    _want_table(page_table, page_fmt)
-    _want("q", q, _HOT, (n, q.shape[1], d), strided_tokens=True)
-    for name, t in (("k", k), ("v", v)):
-        _want(name, t, (q.dtype,), (n, pool.num_kv_heads, d), strided_tokens=True)
-    _want("q_out", q_out, (q.dtype,), q.shape)
-    for name, t in (("seq_ids", seq_ids), ("token_ids", token_ids)):
-        _want(name, t, _INT32, (n,))
-    _want("rope_positions", rope_positions, _INT32, (n,), none_ok=inv_freq is None)
-    _want("inv_freq", inv_freq, (torch.float64,), none_ok=True)
-    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
-        _want(name, t, (torch.float32,), (d,), none_ok=True)
-    _want("err", err, _INT32, none_ok=True)
-    rot = 0 if inv_freq is None else 2 * int(inv_freq.numel())
-    return int(lib().cfr_qk_norm_rope_append(
-        ctypes.byref(pool), _p(page_table), int(page_table.shape[1]), _p(page_fmt), uniform_fmt,
-        int(page_table.shape[0]), _p(q), _token_stride(q), _p(k), _token_stride(k), _p(v),
-        _token_stride(v), _fmt_of(q), n, int(q.shape[1]), _p(q_weight), _p(k_weight), float(eps),
-        _p(rope_positions), _p(inv_freq), rot, 1 if interleaved else 0, _p(q_out), _p(seq_ids),
-        _p(token_ids), _p(err), _stream(stream)))
+    dev = _device()
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q: a tensor [tokens][heads][head_dim] is wanted")
+    n, hq, d = q.shape[0], q.shape[1], pool.head_dim
+    like, kv_shape = (q.dtype,), (n, pool.num_kv_heads, d)
+    table, fmts = _want_table(page_table, page_fmt, dev)
+    qp, qs = _want_rows("q", q, _HOT, (n, hq, d), dev)
+    kp, ks = _want_rows("k", k, like, kv_shape, dev)
+    vp, vs = _want_rows("v", v, like, kv_shape, dev)
+    rot = 0
+    inv = pos = None
+    if inv_freq is not None:
+        inv = _want("inv_freq", inv_freq, _F64S, None, dev)
+        pos = _want("rope_positions", rope_positions, _I32S, (n,), dev)
+        rot = 2 * inv_freq.numel()
+    st = lib().cfr_qk_norm_rope_append(
+        ctypes.byref(pool), table, page_table.shape[1], fmts, uniform_fmt, page_table.shape[0], qp, qs,
+        kp, ks, vp, vs, synth.F32 if q.dtype == torch.float32 else synth.BF16, n, hq,
+        _may("q_weight", q_weight, _F32S, (d,), dev), _may("k_weight", k_weight, _F32S, (d,), dev), eps,
+        pos, inv, rot, 1 if interleaved else 0, _want("q_out", q_out, like, (n, hq, d), dev),
+        _want("seq_ids", seq_ids, _I32S, (n,), dev), _want("token_ids", token_ids, _I32S, (n,), dev),
+        _may("err", err, _I32S, None, dev), _raw_stream(stream, dev))
+    return int(st)
 
 
-def _chunk_args(pool, page_table, page_fmt, uniform_fmt, row_offsets, starts, a, b, names, err):
-    batch = int(page_table.shape[0])
-    _want_table(page_table, page_fmt)
-    _want("row_offsets", row_offsets, _INT32, (batch + 1,))
-    _want("starts", starts, _INT32, (batch,))
-    _want(names[0], a, _HOT, (a.shape[0], pool.num_kv_heads, pool.head_dim), strided_tokens=True)
-    _want(names[1], b, (a.dtype,), a.shape, strided_tokens=True)
-    _want("err", err, _INT32, none_ok=True)
-    return (ctypes.byref(pool), _p(page_table), int(page_table.shape[1]), _p(page_fmt), uniform_fmt,
-            batch, _p(row_offsets), _p(starts), _p(a), _token_stride(a), _p(b), _token_stride(b),
-            _fmt_of(a), int(a.shape[0]), _p(err))
+def _chunk(fn, pool, page_table, page_fmt, uniform_fmt, row_offsets, starts, a, b, names, err, stream):
+    dev = _device()
+    if not isinstance(a, torch.Tensor) or a.dim() != 3:
+        raise ValueError(f"{names[0]}: a tensor [rows][kv heads][head_dim] is wanted")
+    shape = (a.shape[0], pool.num_kv_heads, pool.head_dim)
+    table, fmts = _want_table(page_table, page_fmt, dev)
+    batch, max_pages = page_table.shape
+    ap, sa = _want_rows(names[0], a, _HOT, shape, dev)
+    bp, sb = _want_rows(names[1], b, (a.dtype,), shape, dev)
+    return int(fn(ctypes.byref(pool), table, max_pages, fmts, uniform_fmt, batch,
+                  _want("row_offsets", row_offsets, _I32S, (batch + 1,), dev),
+                  _want("starts", starts, _I32S, (batch,), dev), ap, sa, bp, sb,
+                  synth.F32 if a.dtype == torch.float32 else synth.BF16, shape[0],
+                  _may("err", err, _I32S, None, dev), _raw_stream(stream, dev)))
 
 
 def write_kv(pool: KvPool, page_table, page_fmt, uniform_fmt: int, row_offsets, starts, k_new, v_new,
              err=None, stream=None) -> int:
     """cfr_write_kv: store a ragged chunk of new tokens into pages of any format, quantising as it
     writes; k_new, v_new are [rows][kv heads][head_dim]; returns the status."""
-    args = _chunk_args(pool, page_table, page_fmt, uniform_fmt, row_offsets, starts, k_new, v_new,
-                       ("k_new", "v_new"), err)
-    return int(lib().cfr_write_kv(*args, _stream(stream)))
+    return _chunk(lib().cfr_write_kv, pool, page_table, page_fmt, uniform_fmt, row_offsets, starts,
+                  k_new, v_new, ("k_new", "v_new"), err, stream)
 
 
 def read_kv(pool: KvPool, page_table, page_fmt, uniform_fmt: int, row_offsets, starts, k_out, v_out,
             err=None, stream=None) -> int:
     """cfr_read_kv: cached tokens back as dense fp32 or bf16 rows; returns the status."""
-    args = _chunk_args(pool, page_table, page_fmt, uniform_fmt, row_offsets, starts, k_out, v_out,
-                       ("k_out", "v_out"), err)
-    return int(lib().cfr_read_kv(*args, _stream(stream)))
+    return _chunk(lib().cfr_read_kv, pool, page_table, page_fmt, uniform_fmt, row_offsets, starts,
+                  k_out, v_out, ("k_out", "v_out"), err, stream)
 
 
 def tree_workspace_size(batch, num_queries, num_q_heads, num_kv_heads, head_dim) -> int:
@@ -428,26 +454,22 @@ def paged_decode_tree(pool: KvPool, q, page_table, seq_lens, out, lse, workspace
     """cfr_paged_decode_tree: attention of drafted tokens (q is [batch][queries][heads][head_dim])
     over the cache, under a tree mask of int64 bit rows [batch][queries]; returns the status.
     head_map is a host int32 tensor."""
-    _want("q", q, _HOT)
-    if q.dim() != 4 or q.shape[3] != pool.head_dim:
-        raise ValueError("q: [batch][queries][heads][head_dim] is wanted")
-    batch, nq, hq, d = q.shape
-    _want_table(page_table, page_fmt)
-    _want("page_table", page_table, _INT32, (batch, page_table.shape[1]))
-    _want("seq_lens", seq_lens, _INT32, (batch,))
-    _want("out", out, _HOT, q.shape)
-    _want("lse", lse, (torch.float32,), (batch, nq, hq), none_ok=True)
-    _want("workspace", workspace, (torch.uint8,))
-    _want("q_lens", q_lens, _INT32, (batch,), none_ok=True)
-    _want("tree_mask", tree_mask, (torch.int64, torch.uint64), (batch, nq), none_ok=True)
-    _want("depths", depths, _INT32, (batch, nq), none_ok=True)
-    _want("alibi_slopes", alibi_slopes, (torch.float32,), (hq,), none_ok=True)
-    _want("err", err, _INT32, none_ok=True)
-    _want("head_map", head_map, _INT32, (hq,), none_ok=True)
-    if head_map is not None and head_map.is_cuda:
-        raise ValueError("head_map: a host tensor is wanted")
-    return int(lib().cfr_paged_decode_tree(
-        _p(q), _fmt_of(q), ctypes.byref(pool), _p(page_table), int(page_table.shape[1]), _p(seq_lens),
-        batch, _p(page_fmt), uniform_fmt, hq, nq, _p(q_lens), _p(tree_mask), _p(depths), _p(head_map),
-        _p(alibi_slopes), float(softmax_scale), float(logit_cap), _p(out), _fmt_of(out), _p(lse),
-        _p(workspace), int(workspace.numel()), _p(err), _stream(stream)))
+    dev = _device()
+    if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.shape[3] != pool.head_dim:
+        raise ValueError("q: a tensor [batch][queries][heads][head_dim] is wanted")
+    shape = q.shape
+    batch, nq, hq, _ = shape
+    table, fmts = _want_table(page_table, page_fmt, dev)
+    if page_table.shape[0] != batch:
+        raise ValueError(f"page_table: {page_table.shape[0]} rows for {batch} sequences")
+    st = lib().cfr_paged_decode_tree(
+        _want("q", q, _HOT, None, dev), synth.F32 if q.dtype == torch.float32 else synth.BF16,
+        ctypes.byref(pool), table, page_table.shape[1], _want("seq_lens", seq_lens, _I32S, (batch,), dev),
+        batch, fmts, uniform_fmt, hq, nq, _may("q_lens", q_lens, _I32S, (batch,), dev),
+        _may("tree_mask", tree_mask, _I64S, (batch, nq), dev),
+        _may("depths", depths, _I32S, (batch, nq), dev), _may("head_map", head_map, _I32S, (hq,), -1),
+        _may("alibi_slopes", alibi_slopes, _F32S, (hq,), dev), softmax_scale, logit_cap,
+        _want("out", out, _HOT, shape, dev), synth.F32 if out.dtype == torch.float32 else synth.BF16,
+        _may("lse", lse, _F32S, (batch, nq, hq), dev), _want("workspace", workspace, _U8S, None, dev),
+        workspace.numel(), _may("err", err, _I32S, None, dev), _raw_stream(stream, dev))
+    return int(st)
