@@ -53,129 +53,251 @@ __device__ __forceinline__ Chunk chunk_of(const ChunkParams &p, int b) {
 
 // ---- write -------------------------------------------------------------------
 
-constexpr int kWriteResident = 8;  // vectors a thread holds between the passes
+// vectors a thread holds between the passes: 512 threads hold a page of 256 tokens x 128 bf16 values, with
+// two blocks on an SM, so that one's loads run under the other's encoding
+template <int IN>
+constexpr int kWriteResident = IN == CFR_FMT_F32 ? 4 : 8;
+
+// Stores vectors v0, v0 + T, ... (in `buf`) of a page's new rows as codes; vectors near a
+// tie are marked and encoded again with the division behind the loop.
+template <int IN, int DST, int R>
+__device__ __forceinline__ void store_coded(uint8_t *dst, const RawVec<IN> (&buf)[R], int v0, int T, int nvec, float scale,
+                                            bool fast, float r_lo, float r_hi) {
+  uint32_t redo = 0u;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int v = v0 + i * T;
+    if (v >= nvec) continue;
+    float x[kVec];
+    decode_raw<IN>(buf[i], 1.f, x);
+    uint32_t tb[kVec];
+    if (!fast || codes8_fast<DST>(x, r_lo, r_hi, tb))
+      redo |= 1u << i;
+    else
+      store_codes8<DST>(dst, v, tb);
+  }
+  if (!redo) return;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (!((redo >> i) & 1u)) continue;
+    float x[kVec];
+    decode_raw<IN>(buf[i], 1.f, x);
+    uint32_t tb[kVec];
+    codes8_exact<DST>(x, scale, tb);
+    store_codes8<DST>(dst, v0 + i * T, tb);
+  }
+}
 
 template <int IN>
-__global__ void __launch_bounds__(512) write_kernel(const __grid_constant__ ChunkParams p) {
-  __shared__ int sb;
+__global__ void __launch_bounds__(512, IN == CFR_FMT_F32 ? 1 : 2) write_kernel(const __grid_constant__ ChunkParams p) {
+  constexpr int R = kWriteResident<IN>;
+  __shared__ int found[4];   // sequence, its first row, rows, first token
   __shared__ float red[16];
   const int tid = threadIdx.x, T = blockDim.x;
   const int heads2 = 2 * p.c.Hkv;
   const int which = blockIdx.x % heads2;
   const int seg = blockIdx.x / heads2;
   const int g = which >> 1, kv = which & 1;
-  if (tid == 0) sb = -1;
+  const int P = p.c.P, D = p.c.D;
+  if (tid == 0) found[2] = 0;
   __syncthreads();
   for (int i = tid; i < p.c.batch; i += T) {
-    const int lo = p.row_off[i] / p.c.P + 2 * i;
-    if (lo <= seg && (i + 1 == p.c.batch || p.row_off[i + 1] / p.c.P + 2 * (i + 1) > seg)) sb = i;
-    if (blockIdx.x == 0) chunk_of(p, i);  // reports offsets that no CTA below would look at
+    const int r0 = p.row_off[i], r1 = p.row_off[i + 1], start = p.starts[i];
+    const int lo = r0 / P + 2 * i;
+    if (lo <= seg && (i + 1 == p.c.batch || r1 / P + 2 * (i + 1) > seg)) {
+      const Chunk k = chunk_of(p, i);
+      found[0] = i;
+      found[1] = r0;
+      found[2] = k.n;
+      found[3] = start;
+    } else if (blockIdx.x == 0) {
+      chunk_of(p, i);   // reports offsets that no other block would look at
+    }
   }
   __syncthreads();
-  const int b = sb;
-  if (b < 0) return;
-  const Chunk k = chunk_of(p, b);
-  if (k.n == 0) return;
-  const int P = p.c.P, D = p.c.D;
-  const long long lp = k.start / P + (seg - (k.r0 / P + 2 * b));  // the CTA's logical page
-  const long long t0 = max(static_cast<long long>(k.start), lp * P);
-  const long long t1 = min(static_cast<long long>(k.start) + k.n, (lp + 1) * P);
+  const int b = found[0], r0 = found[1], n = found[2], start = found[3];
+  if (n == 0) return;
+  const long long lp = start / P + (seg - (r0 / P + 2 * b));  // the block's logical page
+  const long long t0 = max(static_cast<long long>(start), lp * P);
+  const long long t1 = min(static_cast<long long>(start) + n, (lp + 1) * P);
   if (t0 >= t1) return;
   int fmt;
   long long slot;
   if (!resolve_page(p.c, b, static_cast<int>(lp), kAllFormats, fmt, slot)) return;
   const int tin = static_cast<int>(t0 - lp * P);  // first new row of the page
-  const int vpr = D / kVec;                       // vectors of a row
-  const int nvec = static_cast<int>(t1 - t0) * vpr;
-  const long long stride = kv ? p.v_stride : p.k_stride;
+  const int vshift = D == 128 ? 4 : 3, vpr = 1 << vshift;   // vectors of a row
+  const int nvec = static_cast<int>(t1 - t0) << vshift;
   constexpr int EB = IN == CFR_FMT_F32 ? 4 : 2;
-  const uint8_t *src = static_cast<const uint8_t *>(kv ? p.v_in : p.k_in) +
-                       ((k.r0 + (t0 - k.start)) * stride + static_cast<long long>(g) * D) * EB;
+  const long long stride = (kv ? p.v_stride : p.k_stride) * EB;
+  const uint8_t *src = static_cast<const uint8_t *>(kv ? p.v_in : p.k_in) + (r0 + (t0 - start)) * stride +
+                       static_cast<long long>(g) * D * EB;
   uint8_t *page = (kv ? p.c.v_pool[fmt] : p.c.k_pool[fmt]) + row_at(p.c, fmt, slot, g, 0);
-  const auto load = [&](int v) {
-    const int row = v / vpr;
-    return load_raw<IN>(src + row * stride * EB, v - row * vpr);
+  uint8_t *rows = page + static_cast<long long>(tin) * row_bytes(fmt, D);
+  RawVec<IN> buf[R];
+  const auto load = [&](int v0) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int v = v0 + i * T;
+      if (v < nvec) buf[i] = load_raw<IN>(src + (v >> vshift) * stride, v & (vpr - 1));
+    }
   };
-  float scale = 1.f;
-  RawVec<IN> buf[kWriteResident];
-  const bool resident = nvec <= kWriteResident * T;
-  if (is_quantised(fmt)) {
-    float amax = 0.f;
-    for (int v0 = 0; v0 < nvec; v0 += kWriteResident * T) {
+  if (!is_quantised(fmt)) {
+#pragma unroll 1
+  for (int v0 = tid; v0 < nvec; v0 += R * T) {
+      load(v0);
 #pragma unroll
-      for (int i = 0; i < kWriteResident; ++i)
-        if (v0 + i * T + tid < nvec) buf[i] = load(v0 + i * T + tid);
-#pragma unroll
-      for (int i = 0; i < kWriteResident; ++i) {
-        if (v0 + i * T + tid < nvec) {
-          float x[kVec];
-          decode_raw<IN>(buf[i], 1.f, x);
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) amax = fmaxf(amax, fabsf(x[e]));
-        }
-      }
-    }
-    float *stored = p.c.scales[fmt] + (slot * p.c.Hkv + g) * 2 + kv;
-    const float old = *stored;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if ((tid & 31) == 0) red[tid >> 5] = amax;
-    __syncthreads();  // every thread has read the old scale by here
-    amax = red[0];
-    for (int w = 1; w < T / 32; ++w) amax = fmaxf(amax, red[w]);
-    scale = __fdiv_rn(amax, qmax_of(fmt));
-    if (tin > 0) {
-      scale = fmaxf(scale, old);
-      if (scale != old) {  // the kept rows, each vector by one thread
-        for (int v = tid; v < tin * vpr; v += T) {
-          float x[kVec];
-          if (fmt == CFR_FMT_I8)
-            decode_raw<CFR_FMT_I8>(load_raw<CFR_FMT_I8>(page, v), old, x);
-          else if (fmt == CFR_FMT_I4)
-            decode_raw<CFR_FMT_I4>(load_raw<CFR_FMT_I4>(page, v), old, x);
-          else
-            decode_raw<CFR_FMT_FP8>(load_raw<CFR_FMT_FP8>(page, v), old, x);
-          store8(fmt, page, static_cast<long long>(v) * kVec, scale, x);
-        }
-      }
-    }
-    if (tid == 0) *stored = scale;
-  }
-  const long long base = static_cast<long long>(tin) * D;
-  for (int v0 = 0; v0 < nvec; v0 += kWriteResident * T) {
-    if (!resident || !is_quantised(fmt)) {
-#pragma unroll
-      for (int i = 0; i < kWriteResident; ++i)
-        if (v0 + i * T + tid < nvec) buf[i] = load(v0 + i * T + tid);
-    }
-#pragma unroll
-    for (int i = 0; i < kWriteResident; ++i) {
-      const int v = v0 + i * T + tid;
-      if (v < nvec) {
+      for (int i = 0; i < R; ++i) {
+        const int v = v0 + i * T;
+        if (v >= nvec) continue;
         float x[kVec];
         decode_raw<IN>(buf[i], 1.f, x);
-        store8(fmt, page, base + static_cast<long long>(v) * kVec, scale, x);
+        store8(fmt, rows, static_cast<long long>(v) * kVec, 1.f, x);
       }
     }
+    return;
+  }
+  // pass 1: max|x| of the new rows
+  float *stored = p.c.scales[fmt] + (slot * p.c.Hkv + g) * 2 + kv;
+  const float old = *stored;
+  float amax = 0.f;
+#pragma unroll 1
+  for (int v0 = tid; v0 < nvec; v0 += R * T) {
+    load(v0);
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (v0 + i * T >= nvec) continue;
+      if constexpr (IN == CFR_FMT_BF16) {
+        m = absmax_acc(absmax_acc(absmax_acc(absmax_acc(m, buf[i].a.x), buf[i].a.y), buf[i].a.z), buf[i].a.w);
+      } else {
+        float x[kVec];
+        decode_raw<IN>(buf[i], 1.f, x);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) amax = fmaxf(amax, fabsf(x[e]));
+      }
+    }
+    if (IN == CFR_FMT_BF16) amax = fmaxf(amax, absmax_value(m));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if ((tid & 31) == 0) red[tid >> 5] = amax;
+  __syncthreads();  // every thread has read the old scale by here
+  amax = red[0];
+  for (int w = 1; w < T / 32; ++w) amax = fmaxf(amax, red[w]);
+  float scale = __fdiv_rn(amax, qmax_of(fmt));
+  if (tin > 0) {
+    scale = fmaxf(scale, old);
+    if (scale != old) {  // the kept rows, each vector by one thread
+      for (int v = tid; v < tin << vshift; v += T) {
+        float x[kVec];
+        if (fmt == CFR_FMT_I8)
+          decode_raw<CFR_FMT_I8>(load_raw<CFR_FMT_I8>(page, v), old, x);
+        else if (fmt == CFR_FMT_I4)
+          decode_raw<CFR_FMT_I4>(load_raw<CFR_FMT_I4>(page, v), old, x);
+        else
+          decode_raw<CFR_FMT_FP8>(load_raw<CFR_FMT_FP8>(page, v), old, x);
+        store8(fmt, page, static_cast<long long>(v) * kVec, scale, x);
+      }
+    }
+  }
+  if (tid == 0) *stored = scale;
+  // pass 2: codes, from the registers where the rows fit them
+  const bool fast = scale >= 1.17549435e-38f && scale <= 3.40282347e+38f;  // normal and finite
+  const float r = __frcp_rn(scale), r_lo = __fmul_rn(r, 1.f - 0x1p-20f), r_hi = __fmul_rn(r, 1.f + 0x1p-20f);
+  const bool resident = nvec <= R * T;
+#pragma unroll 1
+  for (int v0 = tid; v0 < nvec; v0 += R * T) {
+    if (!resident) load(v0);
+    if (fmt == CFR_FMT_I8)
+      store_coded<IN, CFR_FMT_I8, R>(rows, buf, v0, T, nvec, scale, fast, r_lo, r_hi);
+    else if (fmt == CFR_FMT_I4)
+      store_coded<IN, CFR_FMT_I4, R>(rows, buf, v0, T, nvec, scale, fast, r_lo, r_hi);
+    else
+      store_coded<IN, CFR_FMT_FP8, R>(rows, buf, v0, T, nvec, scale, fast, r_lo, r_hi);
   }
 }
 
 // ---- read --------------------------------------------------------------------
 
-constexpr int kReadThreads = 256, kReadRows = 8;
+constexpr int kReadThreads = 256;
 
+// One row (of K or V), nvec vectors over its heads, by one warp, U vectors a lane at a time:
+// a lane keeps its place in a head and steps over 32 / (vectors of a head) heads.
+template <int SRC, int OUT>
+__device__ __forceinline__ void read_row(const uint8_t *src, long long head_bytes, const float *scales, uint8_t *dst, int nvec,
+                                         int vshift, int lane) {
+  constexpr int U = SRC == CFR_FMT_F32 ? 2 : 4;
+  const int hstep = 32 >> vshift;
+  const long long step = hstep * head_bytes;
+  const RawVec<SRC> *at = reinterpret_cast<const RawVec<SRC> *>(src + (lane >> vshift) * head_bytes) + (lane & ((1 << vshift) - 1));
+  if (is_quantised(SRC)) scales += 2 * (lane >> vshift);
+#pragma unroll 1
+  for (int v0 = lane; v0 < nvec; v0 += 32 * U) {
+    RawVec<SRC> raw[U];
+    float scale[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (v0 + 32 * u < nvec) {
+        raw[u] = *at;
+        scale[u] = is_quantised(SRC) ? *scales : 1.f;
+      }
+      at = reinterpret_cast<const RawVec<SRC> *>(reinterpret_cast<const uint8_t *>(at) + step);
+      if (is_quantised(SRC)) scales += 2 * hstep;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int v = v0 + 32 * u;
+      if (v >= nvec) continue;
+      if constexpr (SRC == OUT) {
+        reinterpret_cast<RawVec<SRC> *>(dst)[v] = raw[u];
+      } else {
+        float x[kVec];
+        decode_raw<SRC>(raw[u], scale[u], x);
+        store8(OUT, dst, static_cast<long long>(v) * kVec, 1.f, x);
+      }
+    }
+  }
+}
+
+// places of a block's rows
+struct ReadRows {
+  int fmt[32], tin[32];
+  long long slot[32];
+  uint32_t present;   // formats among them
+};
+
+// the block's rows of one format, a warp taking a row of K or of V at a time
+template <int SRC, int OUT>
+__device__ __forceinline__ void read_rows(const ChunkParams &p, const ReadRows &s, int per, int row0) {
+  if (!((s.present >> SRC) & 1u)) return;
+  constexpr int EB = OUT == CFR_FMT_F32 ? 4 : 2;
+  const int lane = threadIdx.x & 31;
+  const int vshift = p.c.D == 128 ? 4 : 3, nvec = p.c.Hkv << vshift;
+  const long long head_bytes = static_cast<long long>(p.c.P) * row_bytes(SRC, p.c.D);
+#pragma unroll 1
+  for (int i = threadIdx.x >> 5; i < 2 * per; i += kReadThreads / 32) {
+    const int r = i >> 1, kv = i & 1;
+    if (s.fmt[r] != SRC) continue;
+    const uint8_t *src = (kv ? p.c.v_pool[SRC] : p.c.k_pool[SRC]) + row_at(p.c, SRC, s.slot[r], 0, s.tin[r]);
+    const float *scales = is_quantised(SRC) ? p.c.scales[SRC] + s.slot[r] * p.c.Hkv * 2 + kv : nullptr;
+    uint8_t *dst = static_cast<uint8_t *>(kv ? p.v_out : p.k_out) +
+                   static_cast<long long>(row0 + r) * (kv ? p.v_stride : p.k_stride) * EB;
+    read_row<SRC, OUT>(src, head_bytes, scales, dst, nvec, vshift, lane);
+  }
+}
+
+// `per`: rows of a block, at most 32
 template <int OUT>
-__global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ChunkParams p) {
-  __shared__ int sfmt[kReadRows], stin[kReadRows];
-  __shared__ long long sslot[kReadRows];
+__global__ void __launch_bounds__(kReadThreads, 6) read_kernel(const __grid_constant__ ChunkParams p, int per) {
+  __shared__ ReadRows s;
   const int tid = threadIdx.x;
-  const int row0 = blockIdx.x * kReadRows;
-  if (tid < kReadRows) {
+  const int row0 = blockIdx.x * per;
+  if (tid < 32) {
     const int row = row0 + tid;
     int fmt = -1;
     long long slot = 0;
     int tin = 0;
-    if (row < p.num_rows) {
+    if (tid < per && row < p.num_rows) {
       // the last sequence whose rows begin at or before this one
       int lo = 0, hi = p.c.batch;
       while (hi - lo > 1) {
@@ -192,37 +314,21 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
         tin = j % p.c.P;
       }
     }
-    sfmt[tid] = fmt;
-    stin[tid] = tin;
-    sslot[tid] = slot;
+    s.fmt[tid] = fmt;
+    s.tin[tid] = tin;
+    s.slot[tid] = slot;
+    const uint32_t present = __reduce_or_sync(0xffffffffu, fmt >= 0 ? 1u << fmt : 0u);
+    if (tid == 0) s.present = present;
   }
   if (blockIdx.x == 0)
     for (int i = tid; i < p.c.batch; i += kReadThreads) chunk_of(p, i);
   __syncthreads();
-  const int D = p.c.D, vpr = D / kVec;
-  const int per = p.c.Hkv * vpr;  // vectors of a row of K or V
-  constexpr int EB = OUT == CFR_FMT_F32 ? 4 : 2;
-  for (int i = tid; i < 2 * kReadRows * per; i += kReadThreads) {
-    const int kv = i >= kReadRows * per;
-    const int e = kv ? i - kReadRows * per : i;
-    const int r = e / per, in_row = e - r * per;
-    const int fmt = sfmt[r];
-    if (fmt < 0) continue;
-    const int g = in_row / vpr, c8 = in_row - g * vpr;
-    const uint8_t *src = (kv ? p.c.v_pool[fmt] : p.c.k_pool[fmt]) + row_at(p.c, fmt, sslot[r], g, stin[r]);
-    const float scale = is_quantised(fmt) ? p.c.scales[fmt][(sslot[r] * p.c.Hkv + g) * 2 + kv] : 1.f;
-    float x[kVec];
-    switch (fmt) {
-      case CFR_FMT_F32: decode_raw<CFR_FMT_F32>(load_raw<CFR_FMT_F32>(src, c8), 1.f, x); break;
-      case CFR_FMT_BF16: decode_raw<CFR_FMT_BF16>(load_raw<CFR_FMT_BF16>(src, c8), 1.f, x); break;
-      case CFR_FMT_I8: decode_raw<CFR_FMT_I8>(load_raw<CFR_FMT_I8>(src, c8), scale, x); break;
-      case CFR_FMT_I4: decode_raw<CFR_FMT_I4>(load_raw<CFR_FMT_I4>(src, c8), scale, x); break;
-      default: decode_raw<CFR_FMT_FP8>(load_raw<CFR_FMT_FP8>(src, c8), scale, x); break;
-    }
-    uint8_t *dst = static_cast<uint8_t *>(kv ? p.v_out : p.k_out) +
-                   (static_cast<long long>(row0 + r) * (kv ? p.v_stride : p.k_stride) + static_cast<long long>(g) * D) * EB;
-    store8(OUT, dst, c8 * kVec, 1.f, x);
-  }
+  // format by format: one loop that chose at every row kept the registers of all of them
+  read_rows<CFR_FMT_BF16, OUT>(p, s, per, row0);
+  read_rows<CFR_FMT_I8, OUT>(p, s, per, row0);
+  read_rows<CFR_FMT_I4, OUT>(p, s, per, row0);
+  read_rows<CFR_FMT_FP8, OUT>(p, s, per, row0);
+  read_rows<CFR_FMT_F32, OUT>(p, s, per, row0);
 }
 
 // host checks shared by both directions
@@ -295,12 +401,16 @@ cfr_status cfr_read_kv(const cfr_kv_pool *kv, const int32_t *page_table, int32_t
   if (num_rows == 0) return CFR_OK;
   p.k_out = k_out;
   p.v_out = v_out;
-  const unsigned blocks = static_cast<unsigned>((static_cast<long long>(num_rows) + kReadRows - 1) / kReadRows);
+  // rows of a block: 32 where that leaves a block for every SM several times over, fewer for
+  // short chunks (a few hundred rows have to reach all SMs)
+  int per = 32;
+  while (per > 4 && num_rows < per * 600) per >>= 1;
+  const unsigned blocks = static_cast<unsigned>((static_cast<long long>(num_rows) + per - 1) / per);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (out_fmt == CFR_FMT_F32)
-    read_kernel<CFR_FMT_F32><<<blocks, kReadThreads, 0, s>>>(p);
+    read_kernel<CFR_FMT_F32><<<blocks, kReadThreads, 0, s>>>(p, per);
   else
-    read_kernel<CFR_FMT_BF16><<<blocks, kReadThreads, 0, s>>>(p);
+    read_kernel<CFR_FMT_BF16><<<blocks, kReadThreads, 0, s>>>(p, per);
   return cudaGetLastError() == cudaSuccess ? CFR_OK : CFR_ERR_CUDA;
 }
 

@@ -63,14 +63,25 @@ __device__ __forceinline__ void decode_raw(const RawVec<SRC> &r, float scale, fl
       x[2 * k + 1] = bf16_hi(a[k]);
     }
   } else if constexpr (SRC == CFR_FMT_I8) {
+    // (integer conversions run at an eighth of the rate of these: 2^23 + code + 128, exact, less 2^23 + 128)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = __fmul_rn(i8_at(k < 4 ? r.w.x : r.w.y, k & 3), scale);
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t u = (k < 4 ? r.w.x : r.w.y) ^ 0x80808080u;
+      x[k] = __fmul_rn(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540u | (k & 3))) - 8388736.f, scale);
+    }
   } else if constexpr (SRC == CFR_FMT_FP8) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = __fmul_rn(e4m3_at(k < 4 ? r.w.x : r.w.y, k & 3), scale);
-  } else {  // CFR_FMT_I4
+    for (int k = 0; k < 8; k += 2) {
+      const uint32_t h = e4m3x2_to_h2(k < 4 ? r.w.x : r.w.y, (k & 3) >> 1);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+      x[k] = __fmul_rn(f.x, scale);
+      x[k + 1] = __fmul_rn(f.y, scale);
+    }
+  } else {  // CFR_FMT_I4: 2^23 + code + 8 less 2^23 + 8
+    const uint32_t u = r.w ^ 0x88888888u, lo = u & 0x0F0F0F0Fu, hi = (u >> 4) & 0x0F0F0F0Fu;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = __fmul_rn(i4_at(r.w, k), scale);
+    for (int k = 0; k < 8; ++k)
+      x[k] = __fmul_rn(__uint_as_float(__byte_perm(k & 1 ? hi : lo, 0x4B000000u, 0x7540u | (k >> 1))) - 8388616.f, scale);
   }
 }
 
@@ -138,6 +149,106 @@ __device__ __forceinline__ void store_zero8(int fmt, uint8_t *blk, long long e) 
 
 __device__ __forceinline__ float qmax_of(int fmt) {
   return fmt == CFR_FMT_I8 ? 127.f : fmt == CFR_FMT_I4 ? 7.f : 448.f;
+}
+
+// ---------------------------------------------------------------------------
+// Codes without a division per element.
+//
+// The codes are the ones defined above, code = rint(fl(x / scale)) (or the
+// E4M3 code of fl(x / scale)), reached without a division per element.  Let q = x / scale (exact) and f = fl(q).
+// With a normal, finite scale and r = fl(1 / scale) (one correctly rounded
+// reciprocal per block), take r- = fl(r * (1 - 2^-20)) and r+ = fl(r * (1 + 2^-20)).
+// Each of r, r-, r+ and f carries a relative rounding error of at most 2^-24,
+// so x*r- and x*r+ (exact products) lie on either side of f:
+//   |x*r-| <= |q| (1 - 2^-20 + 2^-23) < |f|,   |x*r+| >= |q| (1 + 2^-20 - 2^-23) > |f|
+// (for tiny |q| all three round to 0).  One fused multiply-add of each into
+// the magic constant 1.5 * 2^23, whose unit in the last place is 1, rounds
+// the exact product to the nearest integer (ties to even) and leaves it in
+// the low bits of the sum.  Rounding to nearest is monotone, so when both
+// sums agree they equal rint(f): that is the code, and |code| <= Q (the clamp
+// cannot bind: |x| <= max|x| and scale >= max|x| / Q to within 2^-24).  When
+// they differ (a half-integer within about |q| * 2^-20 of the product, and
+// every NaN), the eight elements of the vector are encoded again with the
+// IEEE division.  On bf16 blocks of N(0,1) values that is about one element in
+// 600: a value that is a simple fraction of max|x| (max|x| / 2, say) puts
+// x / scale within an ulp of a half-integer.  E4M3 destinations
+// round the two products to fp32 and then to E4M3, both monotone, so equal
+// codes of the two are the code of f.  A block whose maximum is infinite or
+// whose scale is zero or subnormal (where the bounds above fail) is encoded
+// with the division throughout.
+// ---------------------------------------------------------------------------
+
+constexpr float kRintMagic = 12582912.0f;         // 1.5 * 2^23
+constexpr uint32_t kRintMagicBits = 0x4B400000u;  // its bit pattern
+
+// Running max|x| of bf16 pairs: per half, max(|m|, |w|) (its sign bit left
+// arbitrary).  The bf16 max returns the other operand when one is NaN, as
+// fmaxf does.
+__device__ __forceinline__ uint32_t absmax_acc(uint32_t m, uint32_t w) {
+  uint32_t d;
+  asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(m), "r"(w));
+  return d;
+}
+
+__device__ __forceinline__ float absmax_value(uint32_t m) {
+  return fmaxf(bf16_lo(m & 0x7FFF7FFFu), bf16_hi(m & 0x7FFF7FFFu));
+}
+
+// stores eight codes (the low byte, or for int4 the low nibble, of each tb)
+// as vector v of the block
+template <int DST>
+__device__ __forceinline__ void store_codes8(uint8_t *dst, int v, const uint32_t (&tb)[kVec]) {
+  if constexpr (DST == CFR_FMT_I4) {  // element 2i in the low nibble of byte i
+    uint32_t n[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) n[k] = (tb[2 * k] & 0x0Fu) | (tb[2 * k + 1] << 4);
+    reinterpret_cast<uint32_t *>(dst)[v] =
+        __byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410);
+  } else {  // int8 and E4M3: one byte each
+    const uint32_t lo = __byte_perm(__byte_perm(tb[0], tb[1], 0x0040), __byte_perm(tb[2], tb[3], 0x0040), 0x5410);
+    const uint32_t hi = __byte_perm(__byte_perm(tb[4], tb[5], 0x0040), __byte_perm(tb[6], tb[7], 0x0040), 0x5410);
+    reinterpret_cast<uint2 *>(dst)[v] = make_uint2(lo, hi);
+  }
+}
+
+// The eight codes of one vector of decoded values x, from the two bracketing
+// products x * r_lo and x * r_hi; true when they disagree somewhere (or a
+// value is NaN), and the vector must be encoded again with the division.
+//  - int8 / int4: each as 0x4B400000 + code (the rounded sum with 1.5 * 2^23);
+//  - E4M3: the code of each rounded product (rounding to fp32 and then to E4M3
+//    are both monotone, so equal codes of the two products are the code of
+//    fl(x / scale), which lies between them).
+template <int DST>
+__device__ __forceinline__ bool codes8_fast(const float (&x)[kVec], float r_lo, float r_hi,
+                                            uint32_t (&tb)[kVec]) {
+  bool near = false;
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) {
+    if constexpr (DST == CFR_FMT_FP8) {
+      const uint32_t lo = __nv_cvt_float_to_fp8(__fmul_rn(x[k], r_lo), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float_to_fp8(__fmul_rn(x[k], r_hi), __NV_SATFINITE, __NV_E4M3);
+      near |= (lo != hi) || (x[k] != x[k]);
+      tb[k] = lo;
+    } else {
+      const float lo = __fmaf_rn(x[k], r_lo, kRintMagic);
+      const float hi = __fmaf_rn(x[k], r_hi, kRintMagic);
+      near |= lo != hi;
+      tb[k] = __float_as_uint(lo);
+    }
+  }
+  return near;
+}
+
+// the same codes with the IEEE division
+template <int DST>
+__device__ __forceinline__ void codes8_exact(const float (&x)[kVec], float scale, uint32_t (&tb)[kVec]) {
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) {
+    if constexpr (DST == CFR_FMT_FP8)
+      tb[k] = fp8_code(x[k], scale);
+    else
+      tb[k] = kRintMagicBits + static_cast<uint32_t>(int_code(x[k], scale, DST == CFR_FMT_I8 ? 127 : 7));
+  }
 }
 
 }  // namespace cfr

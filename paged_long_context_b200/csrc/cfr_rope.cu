@@ -9,11 +9,11 @@
 // fp32, rounded once where the row is stored.
 //
 // One CTA per token: its cosines and sines are computed once, by its first
-// rotary_dim / 2 threads, and serve all of its query and key rows.  A row of
-// head_dim values is head_dim / 8 lanes of eight values, 16 bytes of bf16 each;
-// the row's sum of squares and, for pairs half a rotation apart, the partner
-// values travel by shuffles, so nothing but the sines goes through shared
-// memory.  Bound by HBM: every value is read once and written once.
+// rotary_dim / 2 threads, and serve all of its query and key rows, whose values
+// are on their way meanwhile.  A row is head_dim / 8 lanes of eight values: where
+// pairs lie half a rotation apart, four values of each half, so that a rotation
+// needs no other lane; the row's sum of squares is the only thing that travels
+// by shuffles.  Bound by HBM: every value is read once and written once.
 #include "cfr_cells.cuh"
 
 namespace cfr {
@@ -30,24 +30,82 @@ struct RopeParams {
   const int32_t *rope_pos, *seq_ids, *token_ids;
   const double *inv_freq;
   float eps;
-  int num_q_heads, rot, interleaved;
+  int num_q_heads, rot;
 };
 
-template <int IN, int D>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+// four consecutive stored values
+template <int FMT>
+struct Quad {
+  uint2 w;
+};
+template <>
+struct Quad<CFR_FMT_F32> {
+  uint4 w;
+};
+__device__ __forceinline__ void unpack4(const Quad<CFR_FMT_F32> &q, float *x) {
+  x[0] = __uint_as_float(q.w.x);
+  x[1] = __uint_as_float(q.w.y);
+  x[2] = __uint_as_float(q.w.z);
+  x[3] = __uint_as_float(q.w.w);
+}
+__device__ __forceinline__ void unpack4(const Quad<CFR_FMT_BF16> &q, float *x) {
+  x[0] = bf16_lo(q.w.x);
+  x[1] = bf16_hi(q.w.x);
+  x[2] = bf16_lo(q.w.y);
+  x[3] = bf16_hi(q.w.y);
+}
+__device__ __forceinline__ uint32_t pair_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ void put4(int fmt, uint8_t *row, int e, const float *x) {
+  if (fmt == CFR_FMT_F32)
+    *reinterpret_cast<float4 *>(row + 4 * e) = make_float4(x[0], x[1], x[2], x[3]);
+  else
+    *reinterpret_cast<uint2 *>(row + 2 * e) = make_uint2(pair_bf16(x[0], x[1]), pair_bf16(x[2], x[3]));
+}
+
+template <int IN, int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRopeThreads, IN == CFR_FMT_F32 ? 3 : 4) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int LPR = D / kVec;               // lanes of one row
   constexpr int RPI = kRopeThreads / LPR;     // rows of one step
-  __shared__ float2 cs[D / 2];
-  __shared__ long long place[3];              // format (-1: not written), slot, row
+  constexpr int AHEAD = 3;                    // steps whose rows are loaded at once
+  constexpr int EB = IN == CFR_FMT_F32 ? 4 : 2;
+  __shared__ __align__(16) float cosines[D / 2], sines[D / 2];
+  __shared__ long long place[2];              // format (-1: not written); row of the first head in its pool
   const long long t = blockIdx.x;
   const int tid = threadIdx.x;
+  const int hq = p.num_q_heads, hkv = p.c.Hkv, rows = hq + 2 * hkv;
+  const int c8 = tid % LPR, r_mine = tid / LPR;
+  // this lane's values: e0 .. e0 + 3 and e1 .. e1 + 3, the halves of four pairs where they lie
+  // half a rotation apart and the lane is one that turns
+  const bool turned = c8 * kVec < p.rot;
+  const bool halves = turned && !INTERLEAVED;
+  const int e0 = halves ? 4 * c8 : kVec * c8, gap = halves ? p.rot / 2 : 4;   // e1 = e0 + gap
+  // rows of q, k, v in a line, row r at its base + r * D values
+  const uint8_t *const from_q = static_cast<const uint8_t *>(p.q) + (t * p.q_stride + e0) * EB;
+  const uint8_t *const from_k = static_cast<const uint8_t *>(p.k) + (t * p.k_stride + e0 - hq * D) * EB;
+  const uint8_t *const from_v = static_cast<const uint8_t *>(p.v) + (t * p.v_stride + e0 - (hq + hkv) * D) * EB;
+  Quad<IN> lo[AHEAD], hi[AHEAD];
+  const auto load = [&](int r0) {
+#pragma unroll
+    for (int s = 0; s < AHEAD; ++s) {
+      const int r = r0 + s * RPI + r_mine;
+      if (r >= rows) continue;
+      const uint8_t *at = (r < hq ? from_q : r < hq + hkv ? from_k : from_v) + r * (D * EB);
+      lo[s] = *reinterpret_cast<const Quad<IN> *>(at);
+      hi[s] = *reinterpret_cast<const Quad<IN> *>(at + gap * EB);
+    }
+  };
+  load(0);
   if (tid < p.rot / 2) {
     constexpr double kInvTurn = 0.15915494309189533577;  // 1 / (2 pi)
     const double turns = static_cast<double>(p.rope_pos[t]) * p.inv_freq[tid] * kInvTurn;
     const float r = static_cast<float>(turns - rint(turns));
     float s, c;
     sincospif(2.f * r, &s, &c);
-    cs[tid] = make_float2(c, s);
+    cosines[tid] = c;
+    sines[tid] = s;
   }
   if (tid == kRopeThreads - 1) {
     const int b = p.seq_ids[t], j = p.token_ids[t];
@@ -60,79 +118,84 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         fmt = -1;
     }
     place[0] = fmt;
-    place[1] = slot;
-    place[2] = j >= 0 ? j % p.c.P : 0;
+    place[1] = slot * hkv * p.c.P + (j >= 0 ? j % p.c.P : 0);
   }
   __syncthreads();
   const int fmt = static_cast<int>(place[0]);
-  const int rows = p.num_q_heads + 2 * p.c.Hkv;
-  const int c8 = tid % LPR;                    // this lane's chunk of a row
-  const int hl = p.rot / 16;                   // lanes of half a rotation
-  const bool turned = c8 * kVec < p.rot;
-  for (int r0 = 0; r0 < rows; r0 += RPI) {     // every lane of a warp takes every step
-    const int r = r0 + tid / LPR;
-    const bool is_q = r < p.num_q_heads, is_v = r >= p.num_q_heads + p.c.Hkv;
-    const int head = is_q ? r : is_v ? r - p.num_q_heads - p.c.Hkv : r - p.num_q_heads;
-    float x[kVec] = {};
-    if (r < rows) {
-      const void *src = is_q ? p.q : is_v ? p.v : p.k;
-      const long long e = t * (is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride) +
-                          static_cast<long long>(head) * D;
-      decode_raw<IN>(load_raw<IN>(static_cast<const uint8_t *>(src) + e * (IN == CFR_FMT_F32 ? 4 : 2), c8), 1.f, x);
-    }
-    float sum = 0.f;
+  float cs[4], sn[4];
+  if (turned) {
+    // pairs 4 c8 .. 4 c8 + 3, either way
+    const float4 c4 = reinterpret_cast<const float4 *>(cosines)[c8], s4 = reinterpret_cast<const float4 *>(sines)[c8];
+    cs[0] = c4.x, cs[1] = c4.y, cs[2] = c4.z, cs[3] = c4.w;
+    sn[0] = s4.x, sn[1] = s4.y, sn[2] = s4.z, sn[3] = s4.w;
+  }
+  // where rows go, the same way: head h of K or V is P rows behind head h - 1 in its page
+  const int eb_page = fmt == CFR_FMT_F32 ? 4 : 2;
+  const long long head_bytes = static_cast<long long>(p.c.P) * D * eb_page;
+  uint8_t *const to_q = static_cast<uint8_t *>(p.q_out) + (t * hq * D + e0) * EB;
+  uint8_t *to_k = nullptr, *to_v = nullptr;
+  if (fmt >= 0) {
+    const long long first = (place[1] * D + e0) * eb_page;
+    to_k = p.c.k_pool[fmt] + first - hq * head_bytes;
+    to_v = p.c.v_pool[fmt] + first - (hq + hkv) * head_bytes;
+  }
+#pragma unroll 1
+  for (int r0 = 0; r0 < rows; r0 += AHEAD * RPI) {     // every lane of a warp takes every step
+    if (r0 > 0) load(r0);
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) sum = fmaf(x[i], x[i], sum);
+    for (int s = 0; s < AHEAD; ++s) {
+      if (r0 + s * RPI >= rows) break;
+      const int r = r0 + s * RPI + r_mine;
+      const bool is_q = r < hq, is_v = r >= hq + hkv;
+      float x[kVec] = {};
+      if (r < rows) {
+        unpack4(lo[s], x);
+        unpack4(hi[s], x + 4);
+      }
+      if (p.q_weight || p.k_weight) {
+        float sum = 0.f;
 #pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float *w = is_v ? nullptr : is_q ? p.q_weight : p.k_weight;
-    if (w) {
-      const float rs = rsqrtf(sum * (1.f / D) + p.eps);
-      const float4 w0 = reinterpret_cast<const float4 *>(w)[2 * c8], w1 = reinterpret_cast<const float4 *>(w)[2 * c8 + 1];
-      const float wv[kVec] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        for (int i = 0; i < kVec; ++i) sum = fmaf(x[i], x[i], sum);
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) x[i] = x[i] * rs * wv[i];
-    }
-    if (p.interleaved) {
+        for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float *w = is_v ? nullptr : is_q ? p.q_weight : p.k_weight;
+        if (w) {
+          const float rs = rsqrtf(sum * (1.f / D) + p.eps);
+          const float4 w0 = *reinterpret_cast<const float4 *>(w + e0), w1 = *reinterpret_cast<const float4 *>(w + e0 + gap);
+          const float wv[kVec] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) x[i] = x[i] * rs * wv[i];
+        }
+      }
       if (turned && !is_v) {
 #pragma unroll
-        for (int i = 0; i < kVec; i += 2) {
-          const float2 t2 = cs[c8 * (kVec / 2) + i / 2];
-          const float a = x[i], b = x[i + 1];
-          x[i] = a * t2.x - b * t2.y;
-          x[i + 1] = b * t2.x + a * t2.y;
+        for (int i = 0; i < 4; ++i) {
+          float &a = INTERLEAVED ? x[2 * i] : x[i], &b = INTERLEAVED ? x[2 * i + 1] : x[i + 4];
+          const float y = a * cs[i] - b * sn[i];
+          b = b * cs[i] + a * sn[i];
+          a = y;
         }
       }
-    } else if (p.rot > 0) {
-      const bool upper = c8 >= hl;
-      const int other = (tid & 31) - c8 + (turned ? (upper ? c8 - hl : c8 + hl) : c8);
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        const float y = __shfl_sync(0xffffffffu, x[i], other);
-        if (turned && !is_v) {
-          const float2 t2 = cs[(upper ? c8 - hl : c8) * kVec + i];
-          x[i] = upper ? fmaf(x[i], t2.x, y * t2.y) : fmaf(x[i], t2.x, -y * t2.y);
-        }
-      }
-    }
-    if (r < rows) {
+      if (r >= rows) continue;
       if (is_q) {
-        const long long e = (t * p.num_q_heads + r) * D;
-        store8(IN, static_cast<uint8_t *>(p.q_out) + e * (IN == CFR_FMT_F32 ? 4 : 2), c8 * kVec, 1.f, x);
+        uint8_t *at = to_q + r * (D * EB);
+        put4(IN, at, 0, x);
+        put4(IN, at, gap, x + 4);
       } else if (fmt >= 0) {
-        uint8_t *pool = is_v ? p.c.v_pool[fmt] : p.c.k_pool[fmt];
-        store8(fmt, pool + row_at(p.c, fmt, place[1], head, static_cast<int>(place[2])), c8 * kVec, 1.f, x);
+        uint8_t *at = (is_v ? to_v : to_k) + r * head_bytes;
+        put4(fmt, at, 0, x);
+        put4(fmt, at, gap, x + 4);
       }
     }
   }
 }
 
-template <int IN>
+template <int IN, bool INTERLEAVED>
 void launch_rope(const RopeParams &p, int tokens, cudaStream_t s) {
   if (p.c.D == 128)
-    rope_kernel<IN, 128><<<tokens, kRopeThreads, 0, s>>>(p);
+    rope_kernel<IN, 128, INTERLEAVED><<<tokens, kRopeThreads, 0, s>>>(p);
   else
-    rope_kernel<IN, 64><<<tokens, kRopeThreads, 0, s>>>(p);
+    rope_kernel<IN, 64, INTERLEAVED><<<tokens, kRopeThreads, 0, s>>>(p);
 }
 
 }  // namespace
@@ -187,12 +250,11 @@ cfr_status cfr_qk_norm_rope_append(const cfr_kv_pool *kv, const int32_t *page_ta
   p.eps = eps;
   p.num_q_heads = num_q_heads;
   p.rot = rotary_dim;
-  p.interleaved = interleaved != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (in_fmt == CFR_FMT_F32)
-    launch_rope<CFR_FMT_F32>(p, num_tokens, s);
+    interleaved ? launch_rope<CFR_FMT_F32, true>(p, num_tokens, s) : launch_rope<CFR_FMT_F32, false>(p, num_tokens, s);
   else
-    launch_rope<CFR_FMT_BF16>(p, num_tokens, s);
+    interleaved ? launch_rope<CFR_FMT_BF16, true>(p, num_tokens, s) : launch_rope<CFR_FMT_BF16, false>(p, num_tokens, s);
   return cudaGetLastError() == cudaSuccess ? CFR_OK : CFR_ERR_CUDA;
 }
 
