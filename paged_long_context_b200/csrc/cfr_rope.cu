@@ -8,9 +8,9 @@
 // ulp of 0.06 rad); its sine and cosine, the norm's sum and the products are
 // fp32, rounded once where the row is stored.
 //
-// One CTA per token: its cosines and sines are computed once, by its first
-// rotary_dim / 2 threads, and serve all of its query and key rows, whose values
-// are on their way meanwhile.  A row is head_dim / 8 lanes of eight values: where
+// A CTA takes one token of a short step, four of a long one (kRopeTokens): their
+// cosines and sines are computed once, a thread each, behind one barrier, and serve
+// all query and key rows, the first token's values being on their way meanwhile.  A row is head_dim / 8 lanes of eight values: where
 // pairs lie half a rotation apart, four values of each half, so that a rotation
 // needs no other lane; the row's sum of squares is the only thing that travels
 // by shuffles.  Bound by HBM: every value is read once and written once.
@@ -20,6 +20,7 @@ namespace cfr {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeTokens = 4;   // most tokens of a CTA
 
 struct RopeParams {
   CacheView c;
@@ -30,7 +31,7 @@ struct RopeParams {
   const int32_t *rope_pos, *seq_ids, *token_ids;
   const double *inv_freq;
   float eps;
-  int num_q_heads, rot;
+  int num_q_heads, rot, num_tokens, per;   // per: tokens of a CTA
 };
 
 // four consecutive stored values
@@ -71,9 +72,10 @@ __global__ void __launch_bounds__(kRopeThreads, IN == CFR_FMT_F32 ? 3 : 4) rope_
   constexpr int RPI = kRopeThreads / LPR;     // rows of one step
   constexpr int AHEAD = 3;                    // steps whose rows are loaded at once
   constexpr int EB = IN == CFR_FMT_F32 ? 4 : 2;
-  __shared__ __align__(16) float cosines[D / 2], sines[D / 2];
-  __shared__ long long place[2];              // format (-1: not written); row of the first head in its pool
-  const long long t = blockIdx.x;
+  __shared__ __align__(16) float cosines[kRopeTokens][D / 2], sines[kRopeTokens][D / 2];
+  __shared__ long long place[kRopeTokens][2];  // format (-1: not written); row of the first head in its pool
+  const long long first_t = static_cast<long long>(blockIdx.x) * p.per;
+  const int tokens = static_cast<int>(min(static_cast<long long>(p.per), p.num_tokens - first_t));
   const int tid = threadIdx.x;
   const int hq = p.num_q_heads, hkv = p.c.Hkv, rows = hq + 2 * hkv;
   const int c8 = tid % LPR, r_mine = tid / LPR;
@@ -83,9 +85,9 @@ __global__ void __launch_bounds__(kRopeThreads, IN == CFR_FMT_F32 ? 3 : 4) rope_
   const bool halves = turned && !INTERLEAVED;
   const int e0 = halves ? 4 * c8 : kVec * c8, gap = halves ? p.rot / 2 : 4;   // e1 = e0 + gap
   // rows of q, k, v in a line, row r at its base + r * D values
-  const uint8_t *const from_q = static_cast<const uint8_t *>(p.q) + (t * p.q_stride + e0) * EB;
-  const uint8_t *const from_k = static_cast<const uint8_t *>(p.k) + (t * p.k_stride + e0 - hq * D) * EB;
-  const uint8_t *const from_v = static_cast<const uint8_t *>(p.v) + (t * p.v_stride + e0 - (hq + hkv) * D) * EB;
+  const uint8_t *from_q = static_cast<const uint8_t *>(p.q) + (first_t * p.q_stride + e0) * EB;
+  const uint8_t *from_k = static_cast<const uint8_t *>(p.k) + (first_t * p.k_stride + e0 - hq * D) * EB;
+  const uint8_t *from_v = static_cast<const uint8_t *>(p.v) + (first_t * p.v_stride + e0 - (hq + hkv) * D) * EB;
   Quad<IN> lo[AHEAD], hi[AHEAD];
   const auto load = [&](int r0) {
 #pragma unroll
@@ -98,17 +100,20 @@ __global__ void __launch_bounds__(kRopeThreads, IN == CFR_FMT_F32 ? 3 : 4) rope_
     }
   };
   load(0);
-  if (tid < p.rot / 2) {
+  const int pairs = p.rot / 2;
+  for (int i = tid; i < tokens * pairs; i += kRopeThreads) {
+    const int k = i / pairs, f = i - k * pairs;
     constexpr double kInvTurn = 0.15915494309189533577;  // 1 / (2 pi)
-    const double turns = static_cast<double>(p.rope_pos[t]) * p.inv_freq[tid] * kInvTurn;
+    const double turns = static_cast<double>(p.rope_pos[first_t + k]) * p.inv_freq[f] * kInvTurn;
     const float r = static_cast<float>(turns - rint(turns));
     float s, c;
     sincospif(2.f * r, &s, &c);
-    cosines[tid] = c;
-    sines[tid] = s;
+    cosines[k][f] = c;
+    sines[k][f] = s;
   }
-  if (tid == kRopeThreads - 1) {
-    const int b = p.seq_ids[t], j = p.token_ids[t];
+  if (tid >= kRopeThreads - tokens) {   // (the last threads have no sine of one token to compute)
+    const int k = kRopeThreads - 1 - tid;
+    const int b = p.seq_ids[first_t + k], j = p.token_ids[first_t + k];
     int fmt = -1;
     long long slot = 0;
     if (b >= 0 && j >= 0) {
@@ -117,81 +122,91 @@ __global__ void __launch_bounds__(kRopeThreads, IN == CFR_FMT_F32 ? 3 : 4) rope_
       else if (!resolve_page(p.c, b, j / p.c.P, kHotFormats, fmt, slot))
         fmt = -1;
     }
-    place[0] = fmt;
-    place[1] = slot * hkv * p.c.P + (j >= 0 ? j % p.c.P : 0);
+    place[k][0] = fmt;
+    place[k][1] = slot * hkv * p.c.P + (j >= 0 ? j % p.c.P : 0);
   }
   __syncthreads();
-  const int fmt = static_cast<int>(place[0]);
-  float cs[4], sn[4];
-  if (turned) {
-    // pairs 4 c8 .. 4 c8 + 3, either way
-    const float4 c4 = reinterpret_cast<const float4 *>(cosines)[c8], s4 = reinterpret_cast<const float4 *>(sines)[c8];
-    cs[0] = c4.x, cs[1] = c4.y, cs[2] = c4.z, cs[3] = c4.w;
-    sn[0] = s4.x, sn[1] = s4.y, sn[2] = s4.z, sn[3] = s4.w;
-  }
-  // where rows go, the same way: head h of K or V is P rows behind head h - 1 in its page
-  const int eb_page = fmt == CFR_FMT_F32 ? 4 : 2;
-  const long long head_bytes = static_cast<long long>(p.c.P) * D * eb_page;
-  uint8_t *const to_q = static_cast<uint8_t *>(p.q_out) + (t * hq * D + e0) * EB;
-  uint8_t *to_k = nullptr, *to_v = nullptr;
-  if (fmt >= 0) {
-    const long long first = (place[1] * D + e0) * eb_page;
-    to_k = p.c.k_pool[fmt] + first - hq * head_bytes;
-    to_v = p.c.v_pool[fmt] + first - (hq + hkv) * head_bytes;
-  }
 #pragma unroll 1
-  for (int r0 = 0; r0 < rows; r0 += AHEAD * RPI) {     // every lane of a warp takes every step
-    if (r0 > 0) load(r0);
+  for (int k = 0; k < tokens; ++k) {
+    if (k > 0) {
+      from_q += p.q_stride * EB;
+      from_k += p.k_stride * EB;
+      from_v += p.v_stride * EB;
+      load(0);
+    }
+    const int fmt = static_cast<int>(place[k][0]);
+    float cs[4], sn[4];
+    if (turned) {
+      // pairs 4 c8 .. 4 c8 + 3, either way
+      const float4 c4 = reinterpret_cast<const float4 *>(cosines[k])[c8], s4 = reinterpret_cast<const float4 *>(sines[k])[c8];
+      cs[0] = c4.x, cs[1] = c4.y, cs[2] = c4.z, cs[3] = c4.w;
+      sn[0] = s4.x, sn[1] = s4.y, sn[2] = s4.z, sn[3] = s4.w;
+    }
+    // where rows go, the same way: head h of K or V is P rows behind head h - 1 in its page
+    const int eb_page = fmt == CFR_FMT_F32 ? 4 : 2;
+    const long long head_bytes = static_cast<long long>(p.c.P) * D * eb_page;
+    uint8_t *const to_q = static_cast<uint8_t *>(p.q_out) + ((first_t + k) * hq * D + e0) * EB;
+    uint8_t *to_k = nullptr, *to_v = nullptr;
+    if (fmt >= 0) {
+      const long long first = (place[k][1] * D + e0) * eb_page;
+      to_k = p.c.k_pool[fmt] + first - hq * head_bytes;
+      to_v = p.c.v_pool[fmt] + first - (hq + hkv) * head_bytes;
+    }
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += AHEAD * RPI) {     // every lane of a warp takes every step
+      if (r0 > 0) load(r0);
 #pragma unroll
-    for (int s = 0; s < AHEAD; ++s) {
-      if (r0 + s * RPI >= rows) break;
-      const int r = r0 + s * RPI + r_mine;
-      const bool is_q = r < hq, is_v = r >= hq + hkv;
-      float x[kVec] = {};
-      if (r < rows) {
-        unpack4(lo[s], x);
-        unpack4(hi[s], x + 4);
-      }
-      if (p.q_weight || p.k_weight) {
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) sum = fmaf(x[i], x[i], sum);
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float *w = is_v ? nullptr : is_q ? p.q_weight : p.k_weight;
-        if (w) {
-          const float rs = rsqrtf(sum * (1.f / D) + p.eps);
-          const float4 w0 = *reinterpret_cast<const float4 *>(w + e0), w1 = *reinterpret_cast<const float4 *>(w + e0 + gap);
-          const float wv[kVec] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) x[i] = x[i] * rs * wv[i];
+      for (int s = 0; s < AHEAD; ++s) {
+        if (r0 + s * RPI >= rows) break;
+        const int r = r0 + s * RPI + r_mine;
+        const bool is_q = r < hq, is_v = r >= hq + hkv;
+        float x[kVec] = {};
+        if (r < rows) {
+          unpack4(lo[s], x);
+          unpack4(hi[s], x + 4);
         }
-      }
-      if (turned && !is_v) {
+        if (p.q_weight || p.k_weight) {
+          float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float &a = INTERLEAVED ? x[2 * i] : x[i], &b = INTERLEAVED ? x[2 * i + 1] : x[i + 4];
-          const float y = a * cs[i] - b * sn[i];
-          b = b * cs[i] + a * sn[i];
-          a = y;
+          for (int i = 0; i < kVec; ++i) sum = fmaf(x[i], x[i], sum);
+#pragma unroll
+          for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          const float *w = is_v ? nullptr : is_q ? p.q_weight : p.k_weight;
+          if (w) {
+            const float rs = rsqrtf(sum * (1.f / D) + p.eps);
+            const float4 w0 = *reinterpret_cast<const float4 *>(w + e0), w1 = *reinterpret_cast<const float4 *>(w + e0 + gap);
+            const float wv[kVec] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) x[i] = x[i] * rs * wv[i];
+          }
         }
-      }
-      if (r >= rows) continue;
-      if (is_q) {
-        uint8_t *at = to_q + r * (D * EB);
-        put4(IN, at, 0, x);
-        put4(IN, at, gap, x + 4);
-      } else if (fmt >= 0) {
-        uint8_t *at = (is_v ? to_v : to_k) + r * head_bytes;
-        put4(fmt, at, 0, x);
-        put4(fmt, at, gap, x + 4);
+        if (turned && !is_v) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float &a = INTERLEAVED ? x[2 * i] : x[i], &b = INTERLEAVED ? x[2 * i + 1] : x[i + 4];
+            const float y = a * cs[i] - b * sn[i];
+            b = b * cs[i] + a * sn[i];
+            a = y;
+          }
+        }
+        if (r >= rows) continue;
+        if (is_q) {
+          uint8_t *at = to_q + r * (D * EB);
+          put4(IN, at, 0, x);
+          put4(IN, at, gap, x + 4);
+        } else if (fmt >= 0) {
+          uint8_t *at = (is_v ? to_v : to_k) + r * head_bytes;
+          put4(fmt, at, 0, x);
+          put4(fmt, at, gap, x + 4);
+        }
       }
     }
   }
 }
 
 template <int IN, bool INTERLEAVED>
-void launch_rope(const RopeParams &p, int tokens, cudaStream_t s) {
+void launch_rope(const RopeParams &p, cudaStream_t s) {
+  const int tokens = (p.num_tokens + p.per - 1) / p.per;
   if (p.c.D == 128)
     rope_kernel<IN, 128, INTERLEAVED><<<tokens, kRopeThreads, 0, s>>>(p);
   else
@@ -250,11 +265,15 @@ cfr_status cfr_qk_norm_rope_append(const cfr_kv_pool *kv, const int32_t *page_ta
   p.eps = eps;
   p.num_q_heads = num_q_heads;
   p.rot = rotary_dim;
+  p.num_tokens = num_tokens;
+  // several tokens a CTA once one each would be eight waves of CTAs on 148 SMs (17K tokens: 101 us with one,
+  // see above with four); a decode step's few tokens get a CTA each
+  p.per = num_tokens >= 4096 ? kRopeTokens : 1;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (in_fmt == CFR_FMT_F32)
-    interleaved ? launch_rope<CFR_FMT_F32, true>(p, num_tokens, s) : launch_rope<CFR_FMT_F32, false>(p, num_tokens, s);
+    interleaved ? launch_rope<CFR_FMT_F32, true>(p, s) : launch_rope<CFR_FMT_F32, false>(p, s);
   else
-    interleaved ? launch_rope<CFR_FMT_BF16, true>(p, num_tokens, s) : launch_rope<CFR_FMT_BF16, false>(p, num_tokens, s);
+    interleaved ? launch_rope<CFR_FMT_BF16, true>(p, s) : launch_rope<CFR_FMT_BF16, false>(p, s);
   return cudaGetLastError() == cudaSuccess ? CFR_OK : CFR_ERR_CUDA;
 }
 
