@@ -58,11 +58,13 @@ __device__ __forceinline__ Chunk chunk_of(const ChunkParams &p, int b) {
 template <int IN>
 constexpr int kWriteResident = IN == CFR_FMT_F32 ? 4 : 8;
 
-// Stores vectors v0, v0 + T, ... (in `buf`) of a page's new rows as codes; vectors near a
-// tie are marked and encoded again with the division behind the loop.
-template <int IN, int DST, int R>
+// Stores vectors v0, v0 + T, ... (in `buf`) of a page's new rows as codes.  Vectors near a
+// tie (a warp nearly always has one) are marked and, behind the loop, read and encoded again with the
+// division, one copy of whose code serves all: unrolled over `buf` it overran the
+// instruction cache, whose refills took a third of the kernel's time.
+template <int IN, int DST, int R, typename Again>
 __device__ __forceinline__ void store_coded(uint8_t *dst, const RawVec<IN> (&buf)[R], int v0, int T, int nvec, float scale,
-                                            bool fast, float r_lo, float r_hi) {
+                                            bool fast, float r_lo, float r_hi, Again again) {
   uint32_t redo = 0u;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
@@ -71,20 +73,21 @@ __device__ __forceinline__ void store_coded(uint8_t *dst, const RawVec<IN> (&buf
     float x[kVec];
     decode_raw<IN>(buf[i], 1.f, x);
     uint32_t tb[kVec];
-    if (!fast || codes8_fast<DST>(x, r_lo, r_hi, tb))
+    const bool near = codes8_fast<DST>(x, r_lo, r_hi, tb);
+    if (near || !fast)
       redo |= 1u << i;
     else
       store_codes8<DST>(dst, v, tb);
   }
-  if (!redo) return;
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    if (!((redo >> i) & 1u)) continue;
+#pragma unroll 1
+  while (redo) {
+    const int v = v0 + (__ffs(redo) - 1) * T;
+    redo &= redo - 1;
     float x[kVec];
-    decode_raw<IN>(buf[i], 1.f, x);
+    decode_raw<IN>(again(v), 1.f, x);
     uint32_t tb[kVec];
     codes8_exact<DST>(x, scale, tb);
-    store_codes8<DST>(dst, v0 + i * T, tb);
+    store_codes8<DST>(dst, v, tb);
   }
 }
 
@@ -134,12 +137,11 @@ __global__ void __launch_bounds__(512, IN == CFR_FMT_F32 ? 1 : 2) write_kernel(c
   uint8_t *page = (kv ? p.c.v_pool[fmt] : p.c.k_pool[fmt]) + row_at(p.c, fmt, slot, g, 0);
   uint8_t *rows = page + static_cast<long long>(tin) * row_bytes(fmt, D);
   RawVec<IN> buf[R];
+  const auto vec = [&](int v) { return load_raw<IN>(src + (v >> vshift) * stride, v & (vpr - 1)); };
   const auto load = [&](int v0) {
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int v = v0 + i * T;
-      if (v < nvec) buf[i] = load_raw<IN>(src + (v >> vshift) * stride, v & (vpr - 1));
-    }
+    for (int i = 0; i < R; ++i)
+      if (v0 + i * T < nvec) buf[i] = vec(v0 + i * T);
   };
   if (!is_quantised(fmt)) {
 #pragma unroll 1
@@ -209,11 +211,11 @@ __global__ void __launch_bounds__(512, IN == CFR_FMT_F32 ? 1 : 2) write_kernel(c
   for (int v0 = tid; v0 < nvec; v0 += R * T) {
     if (!resident) load(v0);
     if (fmt == CFR_FMT_I8)
-      store_coded<IN, CFR_FMT_I8, R>(rows, buf, v0, T, nvec, scale, fast, r_lo, r_hi);
+      store_coded<IN, CFR_FMT_I8, R>(rows, buf, v0, T, nvec, scale, fast, r_lo, r_hi, vec);
     else if (fmt == CFR_FMT_I4)
-      store_coded<IN, CFR_FMT_I4, R>(rows, buf, v0, T, nvec, scale, fast, r_lo, r_hi);
+      store_coded<IN, CFR_FMT_I4, R>(rows, buf, v0, T, nvec, scale, fast, r_lo, r_hi, vec);
     else
-      store_coded<IN, CFR_FMT_FP8, R>(rows, buf, v0, T, nvec, scale, fast, r_lo, r_hi);
+      store_coded<IN, CFR_FMT_FP8, R>(rows, buf, v0, T, nvec, scale, fast, r_lo, r_hi, vec);
   }
 }
 

@@ -166,9 +166,10 @@ __global__ void __launch_bounds__(kRopeThreads, IN == CFR_FMT_F32 ? 3 : 4) rope_
           unpack4(hi[s], x + 4);
         }
         if (p.q_weight || p.k_weight) {
-          float sum = 0.f;
+          float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) sum = fmaf(x[i], x[i], sum);
+          for (int i = 0; i < kVec; i += 2) sq = fma2(make_float2(x[i], x[i + 1]), make_float2(x[i], x[i + 1]), sq);
+          float sum = sq.x + sq.y;
 #pragma unroll
           for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
           const float *w = is_v ? nullptr : is_q ? p.q_weight : p.k_weight;
@@ -177,16 +178,33 @@ __global__ void __launch_bounds__(kRopeThreads, IN == CFR_FMT_F32 ? 3 : 4) rope_
             const float4 w0 = *reinterpret_cast<const float4 *>(w + e0), w1 = *reinterpret_cast<const float4 *>(w + e0 + gap);
             const float wv[kVec] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) x[i] = x[i] * rs * wv[i];
+            for (int i = 0; i < kVec; i += 2) {
+              const float2 y = mul2(mul2(make_float2(x[i], x[i + 1]), make_float2(rs, rs)), make_float2(wv[i], wv[i + 1]));
+              x[i] = y.x;
+              x[i + 1] = y.y;
+            }
           }
         }
         if (turned && !is_v) {
+          if constexpr (INTERLEAVED) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float &a = INTERLEAVED ? x[2 * i] : x[i], &b = INTERLEAVED ? x[2 * i + 1] : x[i + 4];
-            const float y = a * cs[i] - b * sn[i];
-            b = b * cs[i] + a * sn[i];
-            a = y;
+            for (int i = 0; i < 4; ++i) {
+              const float a = x[2 * i], b = x[2 * i + 1];
+              x[2 * i] = a * cs[i] - b * sn[i];
+              x[2 * i + 1] = b * cs[i] + a * sn[i];
+            }
+          } else {
+            // two pairs an instruction
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              const float2 a = make_float2(x[i], x[i + 1]), b = make_float2(x[i + 4], x[i + 5]);
+              const float2 c2 = make_float2(cs[i], cs[i + 1]), s2 = make_float2(sn[i], sn[i + 1]);
+              const float2 y = fma2(a, c2, mul2(b, make_float2(-s2.x, -s2.y))), z = fma2(b, c2, mul2(a, s2));
+              x[i] = y.x;
+              x[i + 1] = y.y;
+              x[i + 4] = z.x;
+              x[i + 5] = z.y;
+            }
           }
         }
         if (r >= rows) continue;
