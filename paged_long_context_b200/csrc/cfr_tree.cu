@@ -101,8 +101,8 @@ __global__ void __launch_bounds__(kGenThreads) tree_general_kernel(const __grid_
   TreeCursor cur;
   const int cta = blockIdx.x;
   const long long W = tree_find<kGenTT, kGenRB>(
-      p, S.scratch, tid, kGenThreads, [&](long long w) { return tree_start(w, cta, p.grid); }, cur);
-  cur.end = tree_start(W, cta + 1, p.grid);
+      p, S.scratch, tid, kGenThreads, [&](long long w) { return TreeCut(w, p.grid).start(cta); }, cur);
+  cur.end = TreeCut(W, p.grid).start(cta + 1);
   TreeItem it;
   while (tree_next<kGenTT, kGenRB>(p, cur, it)) {
     __syncthreads();
@@ -253,19 +253,21 @@ __global__ void __launch_bounds__(kGenThreads) tree_general_kernel(const __grid_
 
 // Partials of the items that several CTAs share.  CTA x stands for the cut
 // between CTAs x and x + 1 of the attention: where that cut is the first inside
-// an item, it merges the item, 8 rows a block, a warp each.  The partials are
-// taken in the order of the tiles, so the result does not depend on timing.
+// an item, it merges the item, 8 rows a block, a warp each.  A warp's lanes first
+// weigh 32 partials at once, then take their sums four at a time.  The partials
+// count in the order of the tiles, so the result does not depend on timing.
 template <int TT, int RB, int D>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeParams p) {
   __shared__ TreeScratch scratch;
   constexpr int DV = D / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  griddep_wait();
   TreeCursor cur;
   const int cut = blockIdx.x + 1;
+  // (the cut comes from the call's inputs: found while the attention is still running)
   const long long W = tree_find<TT, RB>(
-      p, scratch, tid, 256, [&](long long w) { return tree_start(w, cut, p.grid); }, cur);
+      p, scratch, tid, 256, [&](long long w) { return TreeCut(w, p.grid).start(cut); }, cur);
   if (cur.u >= W) return;
+  const TreeCut c(W, p.grid);
   // the item that the cut falls into, and its first unit
   TreeItem it;
   long long first;
@@ -278,25 +280,57 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
   }
   const long long last = first + it.tiles + TREE_ITEM_COST;
   if (tree_tile(cur.u - first) == 0) return;                              // no tiles before the cut
-  const long long before = tree_start(W, cut - 1, p.grid);
+  const long long before = c.start(cut - 1);
   if (before >= first && tree_tile(before - first) > 0) return;           // an earlier cut parts the item too
   const int row = blockIdx.y * 8 + warp;
   if (row >= it.rows) return;
+  griddep_wait();
   float M = -INFINITY, L = 0.f, acc[DV] = {};
-  for (int i = cut - 1; i < p.grid; ++i) {
-    const long long lo = tree_start(W, i, p.grid), hi = tree_start(W, i + 1, p.grid);
-    if (lo >= last) break;
-    const int t0 = lo <= first ? 0 : tree_tile(lo - first), t1 = tree_tile(min(hi, last) - first);
-    if (t0 >= t1) continue;
-    const long long s = (2LL * i + (t0 > 0 ? 0 : 1)) * RB + row;
-    const float m = p.part_m[s], l = p.part_l[s];
-    if (l == 0.f) continue;
-    const float mn = fmaxf(M, m);
-    const float ref = mn == -INFINITY ? 0.f : mn;
-    const float a = exp2_approx(M - ref), b = exp2_approx(m - ref);
-    L = L * a + l * b;
+  for (int i0 = cut - 1; i0 < p.grid && c.start(i0) < last; i0 += 32) {
+    // lane x: the partial that CTA i0 + x left
+    const int i = i0 + lane;
+    float m = -INFINITY, l = 0.f;
+    int slot = 0;
+    if (i < p.grid) {
+      const long long lo = c.start(i), hi = c.start(i + 1);
+      const int t0 = lo <= first ? 0 : tree_tile(lo - first), t1 = tree_tile(min(hi, last) - first);
+      if (lo < last && t0 < t1) {
+        slot = 2 * i + (t0 > 0 ? 0 : 1);
+        m = p.part_m[static_cast<long long>(slot) * RB + row];
+        l = p.part_l[static_cast<long long>(slot) * RB + row];
+      }
+    }
+    if (l == 0.f) m = -INFINITY;
+    float top = m;
 #pragma unroll
-    for (int d = 0; d < DV; ++d) acc[d] = acc[d] * a + p.part_acc[s * D + lane * DV + d] * b;
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float mn = fmaxf(M, top);
+    const float ref = mn == -INFINITY ? 0.f : mn;
+    const float a = exp2_approx(M - ref), b = l == 0.f ? 0.f : exp2_approx(m - ref);
+    float sum = l * b;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    L = L * a + sum;
+#pragma unroll
+    for (int d = 0; d < DV; ++d) acc[d] *= a;
+    uint32_t some = __ballot_sync(0xffffffffu, l != 0.f);
+    while (some) {
+      float v[4][DV], w[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int from = some ? __ffs(some) - 1 : 0;
+        w[x] = some ? __shfl_sync(0xffffffffu, b, from) : 0.f;
+        const int sl = __shfl_sync(0xffffffffu, slot, from);
+        const float *src = p.part_acc + (static_cast<long long>(sl) * RB + row) * D + lane * DV;
+#pragma unroll
+        for (int d = 0; d < DV; ++d) v[x][d] = some ? src[d] : 0.f;
+        some &= some - 1;
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int d = 0; d < DV; ++d) acc[d] = fmaf(v[x][d], w[x], acc[d]);
+    }
     M = mn;
   }
   int i, h;

@@ -105,10 +105,17 @@ struct TreeItem {
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
 };
 
-// First unit of CTA i's stretch.
-__device__ __forceinline__ long long tree_start(long long W, int i, int G) {
-  return W / G * i + W % G * i / G;
-}
+// First unit of CTA i's stretch, W i / G rounded down, from W / G and W % G.
+struct TreeCut {
+  long long each;
+  uint32_t rest, G;
+  __device__ __forceinline__ TreeCut(long long W, int grid) {
+    G = static_cast<uint32_t>(grid);
+    each = W >> 32 ? W / G : static_cast<uint32_t>(W) / G;
+    rest = static_cast<uint32_t>(W - each * G);
+  }
+  __device__ __forceinline__ long long start(int i) const { return each * i + rest * static_cast<uint32_t>(i) / G; }
+};
 
 // Finds the cursor of unit range [lo(W), hi(W)): all NT threads call it, NT a multiple of 32;
 // scratch holds NT / 32 + 2 values.  Returns W; `first` is the wanted unit as a function of W.
@@ -178,7 +185,7 @@ __device__ __forceinline__ bool tree_next(const TreeParams &p, TreeCursor &cur, 
     }
     const int each = s.tiles + TREE_ITEM_COST;
     const long long off = cur.u - cur.base;
-    item = static_cast<int>(off / each);
+    item = off >> 32 ? static_cast<int>(off / each) : static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(each));
     const long long in = off - static_cast<long long>(item) * each;   // units of the item before u
     const long long to = min(static_cast<long long>(each), in + (cur.end - cur.u));
     it.t0 = tree_tile(in);

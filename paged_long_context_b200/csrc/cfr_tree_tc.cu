@@ -129,9 +129,10 @@ struct TtSmem {
   };
   // K scale (times softmax scale and log2 e) and V scale of each token
   alignas(16) float ks[QUANT ? META_RING : 1][QUANT ? TT : 4], vs[QUANT ? META_RING : 1][QUANT ? TT : 4];
-  // joining of the copies (narrow): 16 columns of O of every row, its maximum and sum
-  alignas(16) float join[NM == 1 ? 128 : 1][20];
+  // joining of the copies (narrow): 32 columns of O of every row, its maximum and sum
+  alignas(16) float join[NM == 1 ? 128 : 1][36];
   float2 join_ml[NM == 1 ? 128 : 1];
+  long long join_row[NM == 1 ? 64 : 1];
 };
 
 // D[128 x N] (+)= A (TMEM) . B (shared memory)
@@ -246,7 +247,7 @@ __device__ __forceinline__ bool tt_wait(uint64_t *bar, uint32_t parity, uint32_t
   return false;
 }
 
-// Item k of the CTA, published in place k & 7 by the producer of K one item ahead (walking the cut takes
+// Item k of the CTA, published in place k & 7 by the producer of K as item k - 1 begins (walking the cut takes
 // a few microseconds, which every role would spend between items); false past the last.  A place is
 // used again 8 items later, when its readers are through: the producer is ahead of the others by its
 // slots and two steps, fewer than 8 tiles, and an item has at least one.
@@ -363,7 +364,7 @@ __device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor &cur, bool *timed
     ++published;
   };
   for (;; ++k) {
-    while (KV == 0 && published < k + 2) publish();
+    if (KV == 0 && published == k) publish();   // (the first)
     TreeItem item;
     const bool some = tt_item(p, c.S, k, item, timed_out);
     if (!__all_sync(0xffffffffu, some)) break;
@@ -513,6 +514,7 @@ __device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor &cur, bool *timed
         pend_mi = mi;
         pend_item = k & (META_RING - 1);
       }
+      if (KV == 0 && t == it.t1 - 1) publish();   // the item after this one, once this one is under way
       if (++slot_i == r_end) {
         slot_i = r_first;
         slot_ph ^= 1u;
@@ -1004,7 +1006,8 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
     const int copies = NM == 1 ? 128 / row.width : 1;
     if (NM == 1) {
       c.S.join_ml[r] = make_float2(ref, l);
-      if (!meet()) return false;
+      if (row.copy == 0) c.S.join_row[row.row] = to_row;
+      if (!meet()) return false;   // (nothing below can fail, so the barriers there need no limit)
       for (int i = 0; i < copies; ++i) ref_all = fmaxf(ref_all, c.S.join_ml[row.row + i * row.width].x);
       l_all = 0.f;
       for (int i = 0; i < copies; ++i) {
@@ -1014,19 +1017,18 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
       f = ref_all == -INFINITY ? 1.f : exp2_approx(ref - ref_all);
     }
     if (whole) f = l_all == 0.f ? 0.f : f / l_all;
-    const int share = 16 / copies;   // columns of 16 that a copy's thread puts together
-    long long to4[4];   // (wide) the four lanes' rows, -1: none
+    if constexpr (NM == 2) {
+      long long to4[4];   // the four lanes' rows, -1: none
 #pragma unroll
-    for (int i = 0; i < 4; ++i) to4[i] = __shfl_sync(0xffffffffu, row.real ? to_row : -1ll, (r & 28) + i);
+      for (int i = 0; i < 4; ++i) to4[i] = __shfl_sync(0xffffffffu, row.real ? to_row : -1ll, (r & 28) + i);
 #pragma unroll 1
-    for (int ch = 0; ch < D / 16; ++ch) {
-      float o[16];
-      tt_ld16(o_at + 16 * ch, o);
-      tc_wait_ld();
-      if (noted && row.copy == 0) tt_add_back<D>(p, it, noted, 16 * ch, o);
+      for (int ch = 0; ch < D / 16; ++ch) {
+        float o[16];
+        tt_ld16(o_at + 16 * ch, o);
+        tc_wait_ld();
+        if (noted) tt_add_back<D>(p, it, noted, 16 * ch, o);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[i] = l_all == 0.f ? 0.f : o[i] * f;
-      if (NM == 2) {
+        for (int i = 0; i < 16; ++i) o[i] = l_all == 0.f ? 0.f : o[i] * f;
         tt_turn4(o, r & 31);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -1034,22 +1036,36 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
             const float v[4] = {o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]};
             tt_put<4>(p, !whole, to4[i], 16 * ch + 4 * (r & 3), v);
           }
-      } else {
-        float4 *at = reinterpret_cast<float4 *>(c.S.join[r]);
+      }
+    } else {
+      // 32 columns at a time meet in shared memory; a row's 32 are put together by eight lanes
+      const int sub = r & 7;
+#pragma unroll 1
+      for (int ch = 0; ch < D / 32; ++ch) {
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          float o[16];
+          tt_ld16(o_at + 32 * ch + 16 * q, o);
+          tc_wait_ld();
+          if (noted && row.copy == 0) tt_add_back<D>(p, it, noted, 32 * ch + 16 * q, o);
+          float4 *at = reinterpret_cast<float4 *>(&c.S.join[r][16 * q]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) at[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        if (!meet()) return false;
-        const int col = row.copy * share;
-        for (int half = 0; half < share; half += 4) {
-          float4 t = *reinterpret_cast<const float4 *>(&c.S.join[row.row][col + half]);
+          for (int i = 0; i < 4; ++i)
+            at[i] = l_all == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                 : make_float4(o[4 * i] * f, o[4 * i + 1] * f, o[4 * i + 2] * f, o[4 * i + 3] * f);
+        }
+        named_sync(3, 128);
+#pragma unroll 1
+        for (int x = r >> 3; x < it.rows; x += 16) {
+          float4 t = *reinterpret_cast<const float4 *>(&c.S.join[x][4 * sub]);
           for (int i = 1; i < copies; ++i) {
-            const float4 y = *reinterpret_cast<const float4 *>(&c.S.join[row.row + i * row.width][col + half]);
+            const float4 y = *reinterpret_cast<const float4 *>(&c.S.join[x + i * row.width][4 * sub]);
             t = make_float4(t.x + y.x, t.y + y.y, t.z + y.z, t.w + y.w);
           }
           const float v[4] = {t.x, t.y, t.z, t.w};
-          if (row.real) tt_put<4>(p, !whole, to_row, 16 * ch + col + half, v);
+          tt_put<4>(p, !whole, c.S.join_row[x], 32 * ch + 4 * sub, v);
         }
-        if (!meet()) return false;
+        named_sync(3, 128);
       }
     }
     tc_fence_before();
@@ -1317,6 +1333,10 @@ __global__ void __launch_bounds__((TtCfg<D, NM, QUANT>::THREADS), 1)
     mbar_init(&S.meet, 128);
     fence_mbar_init();
   }
+  if (threadIdx.x == 96 && p.k_pool[CFR_FMT_BF16]) {
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+  }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&S.tmem_base)),
                  "r"(Cfg::TMEM_COLS)
@@ -1327,8 +1347,8 @@ __global__ void __launch_bounds__((TtCfg<D, NM, QUANT>::THREADS), 1)
   TreeCursor cur;
   const long long W = tree_find<TT, Cfg::RB>(
       p, S.scratch, threadIdx.x, Cfg::THREADS,
-      [&](long long w) { return tree_start(w, blockIdx.x, p.grid); }, cur);
-  cur.end = tree_start(W, blockIdx.x + 1, p.grid);
+      [&](long long w) { return TreeCut(w, p.grid).start(blockIdx.x); }, cur);
+  cur.end = TreeCut(W, p.grid).start(blockIdx.x + 1);
   tc_fence_after();   // (tree_find synchronises the block)
   bool timed_out = false;
   const int wg = warp >> 2;
