@@ -861,26 +861,34 @@ __device__ __forceinline__ void tt_show_q(TtCtx<D, NM, QUANT> &c, int m) {
   mbar_arrive(&c.S.q_full[m]);
 }
 
-// values of drafts that the MMA was not shown, back into 16 columns of O
+// Values of drafts that the MMA was not shown, back into the rows of O in TMEM (`noted`: the
+// drafts, for this thread's row).  Called by whole warps.
 template <int D>
-__device__ __forceinline__ void tt_add_back(const TreeParams &p, const TreeItem &it, unsigned long long noted, int col,
-                                            float (&o)[16]) {
+__device__ __noinline__ void tt_add_back(const TreeParams &p, const TreeItem &it, unsigned long long noted, uint32_t o_at) {
 #pragma unroll 1
-  for (int d = 0; d < 64; ++d) {
-    if (!((noted >> d) & 1ull)) continue;
-    const int j = it.n - it.c + d;
-    const long long cell = static_cast<long long>(it.b) * p.max_pages + j / p.P;
-    const int fmt = p.page_fmt ? p.page_fmt[cell] : p.uniform_fmt;
-    const uint8_t *v = p.v_pool[fmt] +
-                       ((p.page_table[cell] * static_cast<long long>(p.Hkv) + it.g) * p.P + j % p.P) * row_bytes(fmt, D);
+  for (int ch = 0; ch < D / 16; ++ch) {
+    float o[16];
+    tt_ld16(o_at + 16 * ch, o);
+    tc_wait_ld();
+#pragma unroll 1
+    for (int d = 0; d < it.c; ++d) {
+      if (!((noted >> d) & 1ull)) continue;
+      const int j = it.n - it.c + d;
+      const long long cell = static_cast<long long>(it.b) * p.max_pages + j / p.P;
+      const int fmt = p.page_fmt ? p.page_fmt[cell] : p.uniform_fmt;
+      const uint8_t *v = p.v_pool[fmt] +
+                         ((p.page_table[cell] * static_cast<long long>(p.Hkv) + it.g) * p.P + j % p.P) * row_bytes(fmt, D);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float y = fmt == CFR_FMT_BF16
-                          ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(v)[col + i]) << 16)
-                          : e4m3_at(v[col + i], 0);
-      if (!(fabsf(y) < INFINITY)) o[i] += y;
+      for (int i = 0; i < 16; ++i) {
+        const float y = fmt == CFR_FMT_BF16
+                            ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(v)[16 * ch + i]) << 16)
+                            : e4m3_at(v[16 * ch + i], 0);
+        if (!(fabsf(y) < INFINITY)) o[i] += y;
+      }
     }
+    tt_st16(o_at + 16 * ch, reinterpret_cast<const uint32_t *>(o));
   }
+  tt_wait_st();
 }
 
 // The 16 values of each of four neighbouring lanes' rows, exchanged so that lane j holds values 4 j .. 4 j + 3
@@ -998,6 +1006,7 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
     if (!wait(&c.S.pv_done[2 * m + ((cnt - 1) & 1)], ((cnt - 1) >> 1) & 1u)) return false;
     tc_fence_after();
     const unsigned long long noted = c.S.nonfinite[item_of & (META_RING - 1)] & row.bits;
+    if (__any_sync(0xffffffffu, noted != 0ull)) tt_add_back<D>(p, it, row.copy == 0 ? noted : 0ull, o_at);
     const bool whole = it.whole();
     const long long slot = (2LL * blockIdx.x + (it.t0 > 0 ? 0 : 1)) * Cfg::RB + row.row;
     const long long to_row = whole ? row.out_row : slot;
@@ -1026,7 +1035,6 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
         float o[16];
         tt_ld16(o_at + 16 * ch, o);
         tc_wait_ld();
-        if (noted) tt_add_back<D>(p, it, noted, 16 * ch, o);
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[i] = l_all == 0.f ? 0.f : o[i] * f;
         tt_turn4(o, r & 31);
@@ -1047,7 +1055,6 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
           float o[16];
           tt_ld16(o_at + 32 * ch + 16 * q, o);
           tc_wait_ld();
-          if (noted && row.copy == 0) tt_add_back<D>(p, it, noted, 32 * ch + 16 * q, o);
           float4 *at = reinterpret_cast<float4 *>(&c.S.join[r][16 * q]);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -1350,6 +1357,7 @@ __global__ void __launch_bounds__((TtCfg<D, NM, QUANT>::THREADS), 1)
       [&](long long w) { return TreeCut(w, p.grid).start(blockIdx.x); }, cur);
   cur.end = TreeCut(W, p.grid).start(blockIdx.x + 1);
   tc_fence_after();   // (tree_find synchronises the block)
+  griddep_launch_dependents();   // the merge may find its cuts meanwhile; it waits for this grid's results
   bool timed_out = false;
   const int wg = warp >> 2;
   if (wg == 0) {
