@@ -1050,25 +1050,24 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
       const int sub = r & 7;
 #pragma unroll 1
       for (int ch = 0; ch < D / 32; ++ch) {
-#pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-          float o[16];
-          tt_ld16(o_at + 32 * ch + 16 * q, o);
-          tc_wait_ld();
-          float4 *at = reinterpret_cast<float4 *>(&c.S.join[r][16 * q]);
+        float o[32];
+        tt_ld32(o_at + 32 * ch, o);
+        tc_wait_ld();
+        float4 *at = reinterpret_cast<float4 *>(c.S.join[r]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            at[i] = l_all == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                 : make_float4(o[4 * i] * f, o[4 * i + 1] * f, o[4 * i + 2] * f, o[4 * i + 3] * f);
-        }
+        for (int i = 0; i < 8; ++i)
+          at[i] = l_all == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                               : make_float4(o[4 * i] * f, o[4 * i + 1] * f, o[4 * i + 2] * f, o[4 * i + 3] * f);
         named_sync(3, 128);
 #pragma unroll 1
         for (int x = r >> 3; x < it.rows; x += 16) {
-          float4 t = *reinterpret_cast<const float4 *>(&c.S.join[x][4 * sub]);
-          for (int i = 1; i < copies; ++i) {
-            const float4 y = *reinterpret_cast<const float4 *>(&c.S.join[x + i * row.width][4 * sub]);
-            t = make_float4(t.x + y.x, t.y + y.y, t.z + y.z, t.w + y.w);
-          }
+          float4 y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            y[i] = i < copies ? *reinterpret_cast<const float4 *>(&c.S.join[x + i * row.width][4 * sub])
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 t = make_float4((y[0].x + y[1].x) + (y[2].x + y[3].x), (y[0].y + y[1].y) + (y[2].y + y[3].y),
+                                       (y[0].z + y[1].z) + (y[2].z + y[3].z), (y[0].w + y[1].w) + (y[2].w + y[3].w));
           const float v[4] = {t.x, t.y, t.z, t.w};
           tt_put<4>(p, !whole, c.S.join_row[x], 32 * ch + 4 * sub, v);
         }
