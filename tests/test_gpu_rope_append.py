@@ -176,3 +176,13 @@ def test_captured_step_sees_new_positions():
     g.replay()
     torch.cuda.synchronize()
     s.check()
+
+
+@pytest.mark.parametrize("T,interleaved,in_fmt", [(4096, False, BF16), (4099, True, BF16), (5001, False, F32)])
+def test_long_steps(T, interleaved, in_fmt):
+    # enough tokens for a block to take several of them, and a last block that is not full
+    s = Step(T=T, Hq=3, Hkv=1, B=4, pages=80, in_fmt=in_fmt, fmts=(in_fmt,), interleaved=interleaved, seed=9, far=70000)
+    s.seq[5], s.tok[T - 1] = -1, -1
+    assert s.run() == 0
+    s.check(written=[t for t in range(T) if t not in (5, T - 1)])
+    assert int(s.err.item()) == 0

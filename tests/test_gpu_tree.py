@@ -31,6 +31,7 @@ CONFIGS = {
     "bf16-p128": dict(P=128),
     "bf16-p512": dict(P=512),
     "bf16-p24": dict(P=24),
+    "bf16-p16-formats-given": dict(use_page_fmt=True),
     "bf16-mha": dict(Hq=4, Hkv=4),
     "bf16-mqa": dict(Hq=9, Hkv=1),
     "i8-p16": dict(fmt="i8"),
