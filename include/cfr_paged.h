@@ -543,7 +543,9 @@ cfr_status cfr_qk_norm_rope_append(const cfr_kv_pool *kv, const int32_t *page_ta
  * not in order or whose tokens pass max_pages * page_tokens
  * (CFR_DEVERR_SEQ_LEN); a page of an unknown format (CFR_DEVERR_PAGE_FMT),
  * without a pool (CFR_DEVERR_POOL) or with a slot outside it
- * (CFR_DEVERR_PAGE_ID).  No two sequences may share a written page.
+ * (CFR_DEVERR_PAGE_ID).  Where offsets are out of order, rows of other sequences may stay
+ * unwritten too.  No written page may be named twice.  Pages of more than 2^24 tokens are
+ * CFR_ERR_UNSUPPORTED.
  */
 cfr_status cfr_write_kv(const cfr_kv_pool *kv, const int32_t *page_table, int32_t max_pages,
                         const uint8_t *page_fmt, int32_t uniform_fmt, int32_t batch,

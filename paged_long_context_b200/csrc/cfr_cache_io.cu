@@ -94,7 +94,7 @@ __device__ __forceinline__ void store_coded(uint8_t *dst, const RawVec<IN> (&buf
 template <int IN>
 __global__ void __launch_bounds__(512, IN == CFR_FMT_F32 ? 1 : 2) write_kernel(const __grid_constant__ ChunkParams p) {
   constexpr int R = kWriteResident<IN>;
-  __shared__ int found[4];   // sequence, its first row, rows, first token
+  __shared__ int found;   // the block's sequence
   __shared__ float red[16];
   const int tid = threadIdx.x, T = blockDim.x;
   const int heads2 = 2 * p.c.Hkv;
@@ -102,23 +102,19 @@ __global__ void __launch_bounds__(512, IN == CFR_FMT_F32 ? 1 : 2) write_kernel(c
   const int seg = blockIdx.x / heads2;
   const int g = which >> 1, kv = which & 1;
   const int P = p.c.P, D = p.c.D;
-  if (tid == 0) found[2] = 0;
+  if (tid == 0) found = -1;
   __syncthreads();
   for (int i = tid; i < p.c.batch; i += T) {
-    const int r0 = p.row_off[i], r1 = p.row_off[i + 1], start = p.starts[i];
-    const int lo = r0 / P + 2 * i;
-    if (lo <= seg && (i + 1 == p.c.batch || r1 / P + 2 * (i + 1) > seg)) {
-      const Chunk k = chunk_of(p, i);
-      found[0] = i;
-      found[1] = r0;
-      found[2] = k.n;
-      found[3] = start;
-    } else if (blockIdx.x == 0) {
-      chunk_of(p, i);   // reports offsets that no other block would look at
-    }
+    const int r0 = p.row_off[i], r1 = p.row_off[i + 1];
+    // (more than one, where offsets are out of order)
+    if (r0 / P + 2 * i <= seg && (i + 1 == p.c.batch || r1 / P + 2 * (i + 1) > seg)) atomicMax(&found, i);
+    if (blockIdx.x == 0) chunk_of(p, i);   // reports offsets that no other block would look at
   }
   __syncthreads();
-  const int b = found[0], r0 = found[1], n = found[2], start = found[3];
+  const int b = found;
+  if (b < 0) return;
+  const Chunk mine = chunk_of(p, b);
+  const int r0 = mine.r0, n = mine.n, start = mine.start;
   if (n == 0) return;
   const long long lp = start / P + (seg - (r0 / P + 2 * b));  // the block's logical page
   const long long t0 = max(static_cast<long long>(start), lp * P);
@@ -333,6 +329,9 @@ __global__ void __launch_bounds__(kReadThreads, 6) read_kernel(const __grid_cons
   read_rows<CFR_FMT_F32, OUT>(p, s, per, row0);
 }
 
+// tokens of a page, whose vectors are counted in 32 bits
+constexpr int kMaxChunkPage = 1 << 24;
+
 // host checks shared by both directions
 cfr_status chunk_params(const cfr_kv_pool *kv, const int32_t *page_table, int32_t max_pages,
                         const uint8_t *page_fmt, int32_t uniform_fmt, int32_t batch,
@@ -343,6 +342,7 @@ cfr_status chunk_params(const cfr_kv_pool *kv, const int32_t *page_table, int32_
                             err_word, &p->c);
   if (st != CFR_OK) return st;
   if (dense_fmt != CFR_FMT_F32 && dense_fmt != CFR_FMT_BF16) return CFR_ERR_INVALID_ARG;
+  if (kv->page_tokens > kMaxChunkPage) return CFR_ERR_UNSUPPORTED;
   if (num_rows < 0 || !row_offsets || !starts) return CFR_ERR_INVALID_ARG;
   if (num_rows > 0 && (!rows_ok(k, k_stride, kv->num_kv_heads, kv->head_dim, dense_fmt) ||
                        !rows_ok(v, v_stride, kv->num_kv_heads, kv->head_dim, dense_fmt)))

@@ -177,7 +177,8 @@ __global__ void __launch_bounds__(kGenThreads) tree_general_kernel(const __grid_
           for (int x = 0; x < 4; ++x) {
             const int i = c0 + 16 * x, k = j0 + i - (it.n - it.c);
             float v = s[y][x] * p.sigma;
-            if (p.cap > 0.f) v = p.cap * tanhf(v / p.cap);
+            // (tanh x is x to 2^-24 of it below 2^-12; a large cap's quotient would be denormal)
+            if (p.cap > 0.f && !(fabsf(v) < p.cap * 0x1p-12f)) v = p.cap * tanhf(v / p.cap);
             v = v * kLog2e - S.slope[r] * static_cast<float>(S.pos[r] - S.tok_pos[i]);
             const bool sees = S.tok_fmt[i] >= 0 && (k < 0 || ((S.bits[r] >> k) & 1ull));
             S.s[r][i] = sees ? v : -INFINITY;
@@ -256,6 +257,8 @@ __global__ void __launch_bounds__(kGenThreads) tree_general_kernel(const __grid_
 // an item, it merges the item, 8 rows a block, a warp each.  A warp's lanes first
 // weigh 32 partials at once, then take their sums four at a time.  The partials
 // count in the order of the tiles, so the result does not depend on timing.
+// Block (0, 0) waits for the attention's end whatever it has to merge: were all blocks
+// gone before it, what follows in the stream could start under the attention.
 template <int TT, int RB, int D>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeParams p) {
   __shared__ TreeScratch scratch;
@@ -266,7 +269,10 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
   // (the cut comes from the call's inputs: found while the attention is still running)
   const long long W = tree_find<TT, RB>(
       p, scratch, tid, 256, [&](long long w) { return TreeCut(w, p.grid).start(cut); }, cur);
-  if (cur.u >= W) return;
+  const auto leave = [] {
+    if (blockIdx.x == 0 && blockIdx.y == 0) griddep_wait();
+  };
+  if (cur.u >= W) return leave();
   const TreeCut c(W, p.grid);
   // the item that the cut falls into, and its first unit
   TreeItem it;
@@ -276,14 +282,14 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
     const int each = s.tiles + TREE_ITEM_COST;
     first = cur.base + (cur.u - cur.base) / each * each;
     TreeCursor all{first, first + each, cur.base, cur.b};
-    if (!tree_next<TT, RB>(p, all, it)) return;
+    if (!tree_next<TT, RB>(p, all, it)) return leave();
   }
   const long long last = first + it.tiles + TREE_ITEM_COST;
-  if (tree_tile(cur.u - first) == 0) return;                              // no tiles before the cut
+  if (tree_tile(cur.u - first) == 0) return leave();                           // no tiles before the cut
   const long long before = c.start(cut - 1);
-  if (before >= first && tree_tile(before - first) > 0) return;           // an earlier cut parts the item too
+  if (before >= first && tree_tile(before - first) > 0) return leave();         // an earlier cut parts the item too
   const int row = blockIdx.y * 8 + warp;
-  if (row >= it.rows) return;
+  if (row >= it.rows) return leave();
   griddep_wait();
   float M = -INFINITY, L = 0.f, acc[DV] = {};
   for (int i0 = cut - 1; i0 < p.grid && c.start(i0) < last; i0 += 32) {
@@ -439,6 +445,8 @@ cfr_status cfr_paged_decode_tree(const void *q, int32_t q_fmt, const cfr_kv_pool
   if (num_queries > CFR_TREE_MAX_QUERIES || num_q_heads > kMaxQHeads) return CFR_ERR_UNSUPPORTED;
   if (!(softmax_scale >= 0.f) || softmax_scale == INFINITY) return CFR_ERR_INVALID_ARG;
   if (!(logit_cap >= 0.f) || logit_cap == INFINITY) return CFR_ERR_INVALID_ARG;
+  // (tokens are counted past the last one's tile)
+  if (static_cast<long long>(max_pages) * kv->page_tokens > INT_MAX - 1024) return CFR_ERR_OVERFLOW;
   if (!head_map && num_q_heads % kv->num_kv_heads != 0) return CFR_ERR_INVALID_ARG;
   TreeParams p;
   std::memset(&p, 0, sizeof(p));

@@ -1397,9 +1397,12 @@ cudaError_t launch_general_or_plain(const TreeParams &p, const CUtensorMap &k, c
 
 }  // namespace
 
-// Whether the tensor-core kernel takes the call: bf16 queries, no fp32 pages, pages a multiple of 8 tokens.
+// Whether the tensor-core kernel takes the call: bf16 queries, no fp32 pages, pages a multiple of 8 tokens, and
+// a cap up to 2^10: its form of the tanh (see tt_cap) is off by 2^-22 of the cap, whatever the score, which at
+// 2^10 is still below the rounding of P.
 bool tree_tc_supported(const TreeParams &p) {
   if (p.q_fmt != CFR_FMT_BF16 || p.P % 8 != 0 || p.P > (1 << 24)) return false;
+  if (p.cap > 0.f && !(p.cap >= 0x1p-10f && p.cap <= 0x1p10f)) return false;
   if (p.page_fmt ? p.k_pool[CFR_FMT_F32] != nullptr : p.uniform_fmt == CFR_FMT_F32) return false;
   return p.pool_pages[CFR_FMT_BF16] * p.Hkv <= 0x7fffffffLL / p.P;   // rows of a tensor map
 }

@@ -162,3 +162,12 @@ def test_binding_checks_what_the_abi_cannot_see():
                 dict(k_weight=torch.zeros((64,), dtype=torch.bfloat16))):
         with pytest.raises(ValueError):
             binding.qk_norm_rope_append(pl, **{**good, **bad})
+
+
+def test_pages_and_tables_that_32_bits_cannot_count(lib):
+    for fn in (lib.cfr_write_kv, lib.cfr_read_kv):
+        assert chunk(fn, pool(page_tokens=(1 << 24) + 8), mp=1) == UNSUP
+    big = pool(page_tokens=1 << 20)
+    big.pool_pages[BF16] = 1
+    assert tree(lib, big, mp=2047) != OVERFLOW
+    assert tree(lib, pool(page_tokens=(1 << 30) - 8), mp=2) == OVERFLOW

@@ -329,3 +329,17 @@ def test_offsets_beyond_32_bits():
     # half a step of the page's scale, max|x| / 127 with |x| below 6
     assert (out[0] - k.float()).abs().max() <= 6 / 127 / 2 * 1.001
     assert kp[pages - 1].any() and not kp[1:pages - 1].any()
+
+
+def test_offsets_that_fit_several_sequences_stay_inside_the_rows():
+    # out of order, so that one block's place fits three sequences, of different lengths: rows of the
+    # one that is in order are its own or untouched, and no row from outside the chunk is stored
+    c = Cache(4, 1, 64, 8, 8, [I8], seed=22)
+    k, v = chunk(60, 1, 64, torch.bfloat16, 23)
+    before = c.host()
+    assert c.write(k, v, [0, 60, 0, 40, 3], [0, 0, 0, 0]) == 0
+    assert int(c.err.item()) == binding.DEVERR_SEQ_LEN
+    after = c.host()
+    for b in (1, 3):
+        for p in range(8):
+            assert np.array_equal(before[0][I8][c.table[b, p]], after[0][I8][c.table[b, p]])

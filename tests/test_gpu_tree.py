@@ -338,3 +338,24 @@ def test_scores_that_grow_along_the_sequence(name):
     call = TreeCall(case)
     assert call.run() == 0
     call.check()
+
+
+@pytest.mark.parametrize("name", ["bf16-p16", "i8-p16", "f32-p16"])
+@pytest.mark.parametrize("cap", [1e-30, 2.0 ** -10, 700.0, 1024.0])
+def test_small_and_large_caps(name, cap):
+    case = tree_case(LENS, 5, **CONFIGS[name])
+    masks, depths = trees(len(LENS), 5, 20)
+    call = TreeCall(case, masks, depths, cap=cap)
+    assert call.run() == 0
+    call.check()
+
+
+@pytest.mark.parametrize("name", ["bf16-p16", "tiered-p128", "f32-p16"])
+@pytest.mark.parametrize("cap", [1e7, 3e38])
+def test_caps_far_above_the_scores_change_nothing(name, cap):
+    case = tree_case(LENS, 5, **CONFIGS[name])
+    masks, depths = trees(len(LENS), 5, 21)
+    call = TreeCall(case, masks, depths, cap=cap)
+    assert call.run() == 0
+    call.cap = 0.0    # a score of 30 is 1e-10 off under a cap of 1e7: the formula's and the bounds without one
+    call.check()
