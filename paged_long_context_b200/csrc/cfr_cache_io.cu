@@ -10,8 +10,7 @@
 // over the page's new rows and pass 2 codes them, from registers when the rows fit them.  Which pages
 // are touched stands in device memory only, so the grid covers the most pages
 // that `num_rows` rows of `batch` sequences can touch: sequence b's k-th touched page is CTA
-// row_offsets[b] / P + 2 b + k, and a CTA finds its b by comparing all of them
-// at once.  (L rows touch at most L / P + 2 pages of P, wherever they start, so
+// row_offsets[b] / P + 2 b + k, and a CTA finds its b by search.  (L rows touch at most L / P + 2 pages of P, wherever they start, so
 // the numbers never collide.)
 //
 // Read-back.  One CTA per few rows of the output; the rows' places are
@@ -19,6 +18,8 @@
 // eight values.
 //
 // Both are bound by HBM: dense rows once, stored rows once.
+#include <type_traits>
+
 #include "cfr_cells.cuh"
 
 namespace cfr {
@@ -38,9 +39,8 @@ struct ChunkParams {
 struct Chunk {
   int r0, n, start;
 };
-__device__ __forceinline__ Chunk chunk_of(const ChunkParams &p, int b) {
-  Chunk k{p.row_off[b], 0, p.starts[b]};
-  const int r1 = p.row_off[b + 1];
+__device__ __forceinline__ Chunk chunk_of(const ChunkParams &p, int r0, int r1, int start) {
+  Chunk k{r0, 0, start};
   if (k.r0 == r1 && k.r0 >= 0 && r1 <= p.num_rows) return k;
   if (k.r0 < 0 || r1 < k.r0 || r1 > p.num_rows || k.start < 0 ||
       static_cast<long long>(k.start) + (r1 - k.r0) > static_cast<long long>(p.c.max_pages) * p.c.P) {
@@ -50,169 +50,195 @@ __device__ __forceinline__ Chunk chunk_of(const ChunkParams &p, int b) {
   k.n = r1 - k.r0;
   return k;
 }
+__device__ __forceinline__ Chunk chunk_of(const ChunkParams &p, int b) {
+  return chunk_of(p, p.row_off[b], p.row_off[b + 1], p.starts[b]);
+}
 
 // ---- write -------------------------------------------------------------------
 
-// vectors a thread holds between the passes: 512 threads hold a page of 256 tokens x 128 bf16 values, with
-// two blocks on an SM, so that one's loads run under the other's encoding
-template <int IN>
-constexpr int kWriteResident = IN == CFR_FMT_F32 ? 4 : 8;
+// A block's new rows wait in shared memory between the passes, up to 64 KiB of them (a page of 256 tokens x 128
+// bf16 values; three such blocks fit an SM, so that one's loads run under the others' encoding).
+constexpr int kWriteStage = 65536;
+constexpr int kWriteThreads = 256;
+constexpr int kTeamVectors = 8;        // vectors of a page for each thread of a team, up to the block's threads
 
-// Stores vectors v0, v0 + T, ... (in `buf`) of a page's new rows as codes.  Vectors near a
-// tie (a warp nearly always has one) are marked and, behind the loop, read and encoded again with the
-// division, one copy of whose code serves all: unrolled over `buf` it overran the
-// instruction cache, whose refills took a third of the kernel's time.
-template <int IN, int DST, int R, typename Again>
-__device__ __forceinline__ void store_coded(uint8_t *dst, const RawVec<IN> (&buf)[R], int v0, int T, int nvec, float scale,
-                                            bool fast, float r_lo, float r_hi, Again again) {
-  uint32_t redo = 0u;
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int v = v0 + i * T;
-    if (v >= nvec) continue;
-    float x[kVec];
-    decode_raw<IN>(buf[i], 1.f, x);
-    uint32_t tb[kVec];
-    const bool near = codes8_fast<DST>(x, r_lo, r_hi, tb);
-    if (near || !fast)
-      redo |= 1u << i;
-    else
-      store_codes8<DST>(dst, v, tb);
-  }
+// Eight values of vector v stored as codes: by the quotients where the scale allows it, else (and where a NaN is
+// among integers) with the division.
+template <int DST, bool CLAMP>
+__device__ __forceinline__ void store_coded(uint8_t *dst, int v, const float (&x)[kVec], float scale, float r, bool fast) {
+  if (!fast || !store_quotients8<DST, CLAMP>(dst, v, x, r, scale)) store8(DST, dst, static_cast<long long>(v) * kVec, scale, x);
+}
+
+__device__ __forceinline__ void copy_async16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))), "l"(src)
+               : "memory");
+}
+
+// the kept rows of a page (nvec vectors) under a new scale
+template <int FMT>
+__device__ __forceinline__ void store_kept(uint8_t *page, int tid, int T, int nvec, float old, float scale, float r, bool fast) {
 #pragma unroll 1
-  while (redo) {
-    const int v = v0 + (__ffs(redo) - 1) * T;
-    redo &= redo - 1;
+  for (int v = tid; v < nvec; v += T) {
     float x[kVec];
-    decode_raw<IN>(again(v), 1.f, x);
-    uint32_t tb[kVec];
-    codes8_exact<DST>(x, scale, tb);
-    store_codes8<DST>(dst, v, tb);
+    decode_raw<FMT>(load_raw<FMT>(page, v), old, x);
+    store_coded<FMT, true>(page, v, x, scale, r, fast);
   }
 }
 
-template <int IN>
-__global__ void __launch_bounds__(512, IN == CFR_FMT_F32 ? 1 : 2) write_kernel(const __grid_constant__ ChunkParams p) {
-  constexpr int R = kWriteResident<IN>;
-  __shared__ int found;   // the block's sequence
-  __shared__ float red[16];
-  const int tid = threadIdx.x, T = blockDim.x;
-  const int heads2 = 2 * p.c.Hkv;
-  const int which = blockIdx.x % heads2;
-  const int seg = blockIdx.x / heads2;
-  const int g = which >> 1, kv = which & 1;
-  const int P = p.c.P, D = p.c.D;
-  if (tid == 0) found = -1;
-  __syncthreads();
-  for (int i = tid; i < p.c.batch; i += T) {
-    const int r0 = p.row_off[i], r1 = p.row_off[i + 1];
-    // (more than one, where offsets are out of order)
-    if (r0 / P + 2 * i <= seg && (i + 1 == p.c.batch || r1 / P + 2 * (i + 1) > seg)) atomicMax(&found, i);
-    if (blockIdx.x == 0) chunk_of(p, i);   // reports offsets that no other block would look at
-  }
-  __syncthreads();
-  const int b = found;
-  if (b < 0) return;
-  const Chunk mine = chunk_of(p, b);
-  const int r0 = mine.r0, n = mine.n, start = mine.start;
-  if (n == 0) return;
-  const long long lp = start / P + (seg - (r0 / P + 2 * b));  // the block's logical page
-  const long long t0 = max(static_cast<long long>(start), lp * P);
-  const long long t1 = min(static_cast<long long>(start) + n, (lp + 1) * P);
-  if (t0 >= t1) return;
+// T = 32 .. 256 threads, a team, take a page of one kv head, K or V: an eighth of its vectors,
+// so that what a page costs before its values (finding the sequence, resolving the page, joining the
+// maxima) is spread over eight vectors a thread.
+//
+// Warp 0 works out the block's page, once for all.
+struct WritePage {
+  long long slot, src_row;   // of the first new row, in the dense rows
+  int fmt, tin, rows;        // fmt -1: nothing to write; first new row of the page, new rows
+  int which;                 // first (kv head, K or V) of the block
+};
+
+__device__ __forceinline__ void find_page(const ChunkParams &p, int blocks, int each, WritePage *at) {
+  const int lane = threadIdx.x, P = p.c.P;
+  const int seg = blockIdx.x / blocks;
+  // the last sequence whose first touched page is numbered seg or less, 32 probes at a time; its offsets
+  // and start come with the probes, not behind them
+  int lo = 0, hi = p.c.batch, r0, r1, start;
+  do {
+    const int step = (hi - lo + 31) >> 5;
+    const int i = static_cast<int>(min(lo + static_cast<long long>(lane) * step, hi - 1LL));
+    r0 = p.row_off[i];
+    r1 = p.row_off[i + 1];
+    start = p.starts[i];
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, lane == 0 || (lo + static_cast<long long>(lane) * step < hi &&
+                                                                         r0 / P + 2LL * i <= seg)));
+    r0 = __shfl_sync(0xffffffffu, r0, last);
+    r1 = __shfl_sync(0xffffffffu, r1, last);
+    start = __shfl_sync(0xffffffffu, start, last);
+    lo += last * step;
+    hi = min(hi, lo + step);
+  } while (hi - lo > 1);
+  if (lane > 0) return;
+  at->fmt = -1;
+  at->which = (blockIdx.x - seg * blocks) * each;
+  const Chunk mine = chunk_of(p, r0, r1, start);
+  const int k = seg - (mine.r0 / P + 2 * lo);   // page of the sequence's touched ones
+  if (mine.n == 0 || k < 0) return;
+  const long long lp = mine.start / P + static_cast<long long>(k);
+  const long long t0 = max(static_cast<long long>(mine.start), lp * P);
+  const long long t1 = min(static_cast<long long>(mine.start) + mine.n, (lp + 1) * P);
   int fmt;
   long long slot;
-  if (!resolve_page(p.c, b, static_cast<int>(lp), kAllFormats, fmt, slot)) return;
-  const int tin = static_cast<int>(t0 - lp * P);  // first new row of the page
+  if (t0 >= t1 || !resolve_page(p.c, lo, static_cast<int>(lp), kAllFormats, fmt, slot)) return;
+  at->fmt = fmt;
+  at->slot = slot;
+  at->src_row = mine.r0 + (t0 - mine.start);
+  at->tin = static_cast<int>(t0 - lp * P);
+  at->rows = static_cast<int>(t1 - t0);
+}
+
+// `blocks`: blocks of a touched page; 1 << shift: threads of a team; team_stage: its bytes of shared memory
+template <int IN>
+__global__ void __launch_bounds__(kWriteThreads, 3) write_kernel(const __grid_constant__ ChunkParams p, int blocks, int shift, int team_stage) {
+  extern __shared__ __align__(16) uint8_t stage[];
+  __shared__ WritePage page_of;
+  __shared__ float red[kWriteThreads / 32];
+  const int T = 1 << shift, team = threadIdx.x >> shift, tid = threadIdx.x & (T - 1);
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < p.c.batch; i += blockDim.x) chunk_of(p, i);   // reports all that are out of order
+  if (threadIdx.x < 32) find_page(p, blocks, blockDim.x >> shift, &page_of);
+  __syncthreads();
+  const int fmt = page_of.fmt, which = page_of.which + team;
+  if (fmt < 0 || which >= 2 * p.c.Hkv) return;   // (only barriers of a team below)
+  const int g = which >> 1, kv = which & 1, D = p.c.D;
+  const long long slot = page_of.slot;
+  const int tin = page_of.tin;
   const int vshift = D == 128 ? 4 : 3, vpr = 1 << vshift;   // vectors of a row
-  const int nvec = static_cast<int>(t1 - t0) << vshift;
+  const int nvec = page_of.rows << vshift;
   constexpr int EB = IN == CFR_FMT_F32 ? 4 : 2;
   const long long stride = (kv ? p.v_stride : p.k_stride) * EB;
-  const uint8_t *src = static_cast<const uint8_t *>(kv ? p.v_in : p.k_in) + (r0 + (t0 - start)) * stride +
+  const uint8_t *src = static_cast<const uint8_t *>(kv ? p.v_in : p.k_in) + page_of.src_row * stride +
                        static_cast<long long>(g) * D * EB;
   uint8_t *page = (kv ? p.c.v_pool[fmt] : p.c.k_pool[fmt]) + row_at(p.c, fmt, slot, g, 0);
   uint8_t *rows = page + static_cast<long long>(tin) * row_bytes(fmt, D);
-  RawVec<IN> buf[R];
-  const auto vec = [&](int v) { return load_raw<IN>(src + (v >> vshift) * stride, v & (vpr - 1)); };
-  const auto load = [&](int v0) {
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (v0 + i * T < nvec) buf[i] = vec(v0 + i * T);
-  };
+  constexpr int VB = kVec * EB;   // bytes of a vector
+  // a thread's vectors are tid, tid + T, ...: the same place of rows T / vpr apart
+  src += (tid >> vshift) * stride + (tid & (vpr - 1)) * VB;
+  const long long step = (T >> vshift) * stride;
   if (!is_quantised(fmt)) {
-#pragma unroll 1
-  for (int v0 = tid; v0 < nvec; v0 += R * T) {
-      load(v0);
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const int v = v0 + i * T;
-        if (v >= nvec) continue;
-        float x[kVec];
-        decode_raw<IN>(buf[i], 1.f, x);
-        store8(fmt, rows, static_cast<long long>(v) * kVec, 1.f, x);
-      }
+#pragma unroll 4
+    for (int v = tid; v < nvec; v += T, src += step) {
+      float x[kVec];
+      decode_raw<IN>(load_raw<IN>(src, 0), 1.f, x);
+      store8(fmt, rows, static_cast<long long>(v) * kVec, 1.f, x);
     }
     return;
   }
-  // pass 1: max|x| of the new rows
+  // the new rows, each vector by the thread that takes it in both passes
+  const int held = min(nvec, team_stage / VB);   // those that shared memory has room for (the others are read twice)
+  uint8_t *mine = stage + team * team_stage;
+  const uint8_t *at = src;
+#pragma unroll 4
+  for (int v = tid; v < held; v += T, at += step) {
+    copy_async16(mine + v * VB, at);
+    if (VB == 32) copy_async16(mine + v * VB + 16, at + 16);
+  }
   float *stored = p.c.scales[fmt] + (slot * p.c.Hkv + g) * 2 + kv;
   const float old = *stored;
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  // pass 1: max|x| of the new rows
   float amax = 0.f;
-#pragma unroll 1
-  for (int v0 = tid; v0 < nvec; v0 += R * T) {
-    load(v0);
-    uint32_t m = 0u;
+  uint32_t m = 0u;
+  const auto take = [&](const RawVec<IN> &raw) {
+    if constexpr (IN == CFR_FMT_BF16) {
+      m = absmax_acc(absmax_acc(absmax_acc(absmax_acc(m, raw.a.x), raw.a.y), raw.a.z), raw.a.w);
+    } else {
+      float x[kVec];
+      decode_raw<IN>(raw, 1.f, x);
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      if (v0 + i * T >= nvec) continue;
-      if constexpr (IN == CFR_FMT_BF16) {
-        m = absmax_acc(absmax_acc(absmax_acc(absmax_acc(m, buf[i].a.x), buf[i].a.y), buf[i].a.z), buf[i].a.w);
-      } else {
-        float x[kVec];
-        decode_raw<IN>(buf[i], 1.f, x);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) amax = fmaxf(amax, fabsf(x[e]));
-      }
+      for (int e = 0; e < kVec; ++e) amax = fmaxf(amax, fabsf(x[e]));
     }
-    if (IN == CFR_FMT_BF16) amax = fmaxf(amax, absmax_value(m));
-  }
+  };
+#pragma unroll 4
+  for (int v = tid; v < held; v += T) take(load_raw<IN>(mine, v));
+  const int first_far = tid + (held - tid + T - 1) / T * T;   // the thread's first vector past those (held >= T or all)
+#pragma unroll 1
+  for (int v = first_far; v < nvec; v += T, at += step) take(load_raw<IN>(at, 0));
+  if (IN == CFR_FMT_BF16) amax = absmax_value(m);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if ((tid & 31) == 0) red[tid >> 5] = amax;
-  __syncthreads();  // every thread has read the old scale by here
-  amax = red[0];
-  for (int w = 1; w < T / 32; ++w) amax = fmaxf(amax, red[w]);
+  // (every thread has read the old scale once it is past the barrier)
+  if (T == 32) {
+    __syncwarp();
+  } else {
+    float *mine_red = red + team * (T / 32);
+    if ((tid & 31) == 0) mine_red[tid >> 5] = amax;
+    named_sync(1 + team, T);
+    amax = mine_red[tid & (T / 32 - 1)];
+#pragma unroll
+    for (int o = kWriteThreads / 64; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  }
   float scale = __fdiv_rn(amax, qmax_of(fmt));
-  if (tin > 0) {
-    scale = fmaxf(scale, old);
-    if (scale != old) {  // the kept rows, each vector by one thread
-      for (int v = tid; v < tin << vshift; v += T) {
-        float x[kVec];
-        if (fmt == CFR_FMT_I8)
-          decode_raw<CFR_FMT_I8>(load_raw<CFR_FMT_I8>(page, v), old, x);
-        else if (fmt == CFR_FMT_I4)
-          decode_raw<CFR_FMT_I4>(load_raw<CFR_FMT_I4>(page, v), old, x);
-        else
-          decode_raw<CFR_FMT_FP8>(load_raw<CFR_FMT_FP8>(page, v), old, x);
-        store8(fmt, page, static_cast<long long>(v) * kVec, scale, x);
-      }
-    }
-  }
+  if (tin > 0) scale = fmaxf(scale, old);
   if (tid == 0) *stored = scale;
-  // pass 2: codes, from the registers where the rows fit them
-  const bool fast = scale >= 1.17549435e-38f && scale <= 3.40282347e+38f;  // normal and finite
-  const float r = __frcp_rn(scale), r_lo = __fmul_rn(r, 1.f - 0x1p-20f), r_hi = __fmul_rn(r, 1.f + 0x1p-20f);
-  const bool resident = nvec <= R * T;
+  const bool fast = scale >= kQuotientMin && scale <= kQuotientMax;
+  const float r = __frcp_rn(scale);
+  // the kept rows under the new scale; pass 2: codes of the new ones
+  const int kept = tin > 0 && scale != old ? tin << vshift : 0;
+  const auto store = [&](auto dst) {
+    constexpr int DST = decltype(dst)::value;
+    store_kept<DST>(page, tid, T, kept, old, scale, r, fast);
 #pragma unroll 1
-  for (int v0 = tid; v0 < nvec; v0 += R * T) {
-    if (!resident) load(v0);
-    if (fmt == CFR_FMT_I8)
-      store_coded<IN, CFR_FMT_I8, R>(rows, buf, v0, T, nvec, scale, fast, r_lo, r_hi, vec);
-    else if (fmt == CFR_FMT_I4)
-      store_coded<IN, CFR_FMT_I4, R>(rows, buf, v0, T, nvec, scale, fast, r_lo, r_hi, vec);
-    else
-      store_coded<IN, CFR_FMT_FP8, R>(rows, buf, v0, T, nvec, scale, fast, r_lo, r_hi, vec);
-  }
+    for (int v = tid; v < nvec; v += T, src += step) {
+      float x[kVec];
+      decode_raw<IN>(v < held ? load_raw<IN>(mine, v) : load_raw<IN>(src, 0), 1.f, x);
+      store_coded<DST, false>(rows, v, x, scale, r, fast);
+    }
+  };
+  if (fmt == CFR_FMT_I8)
+    store(std::integral_constant<int, CFR_FMT_I8>());
+  else if (fmt == CFR_FMT_I4)
+    store(std::integral_constant<int, CFR_FMT_I4>());
+  else
+    store(std::integral_constant<int, CFR_FMT_FP8>());
 }
 
 // ---- read --------------------------------------------------------------------
@@ -375,20 +401,25 @@ cfr_status cfr_write_kv(const cfr_kv_pool *kv, const int32_t *page_table, int32_
                                starts, k_new, k_stride, v_new, v_stride, new_fmt, num_rows, err_word, &p);
   if (st != CFR_OK) return st;
   const long long segs = static_cast<long long>(num_rows) / kv->page_tokens + 2LL * batch;
-  const long long blocks = segs * kv->num_kv_heads * 2;
-  if (blocks > INT_MAX) return CFR_ERR_OVERFLOW;
+  const int vectors = kv->page_tokens * (kv->head_dim / kVec), heads2 = 2 * kv->num_kv_heads;
+  int shift = 5;
+  while (1 << shift < kWriteThreads && kTeamVectors << shift < vectors) ++shift;
+  const int each = kWriteThreads >> shift;
+  const int page_blocks = (heads2 + each - 1) / each;
+  const long long blocks = segs * page_blocks;
+  if (segs > INT_MAX / 2 || blocks > INT_MAX) return CFR_ERR_OVERFLOW;
   if (num_rows == 0) return CFR_OK;
   p.k_in = k_new;
   p.v_in = v_new;
-  // threads for one vector each of a small page, up to 512
-  int threads = kv->page_tokens * (kv->head_dim / kVec);
-  threads = threads < 64 ? 64 : threads > 512 ? 512 : (threads + 31) / 32 * 32;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (new_fmt == CFR_FMT_F32)
-    write_kernel<CFR_FMT_F32><<<static_cast<unsigned>(blocks), threads, 0, s>>>(p);
-  else
-    write_kernel<CFR_FMT_BF16><<<static_cast<unsigned>(blocks), threads, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? CFR_OK : CFR_ERR_CUDA;
+  const int room = kWriteStage / each, vector_bytes = new_fmt == CFR_FMT_F32 ? 32 : 16;
+  const int team_stage = vectors < room / vector_bytes ? vectors * vector_bytes : room;
+  const auto launch = [&](auto kernel) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWriteStage) != cudaSuccess) return CFR_ERR_CUDA;
+    kernel<<<static_cast<unsigned>(blocks), kWriteThreads, each * team_stage, static_cast<cudaStream_t>(stream)>>>(
+        p, page_blocks, shift, team_stage);
+    return cudaGetLastError() == cudaSuccess ? CFR_OK : CFR_ERR_CUDA;
+  };
+  return new_fmt == CFR_FMT_F32 ? launch(write_kernel<CFR_FMT_F32>) : launch(write_kernel<CFR_FMT_BF16>);
 }
 
 cfr_status cfr_read_kv(const cfr_kv_pool *kv, const int32_t *page_table, int32_t max_pages,

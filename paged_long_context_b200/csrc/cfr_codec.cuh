@@ -251,4 +251,73 @@ __device__ __forceinline__ void codes8_exact(const float (&x)[kVec], float scale
   }
 }
 
+// The same codes from the quotients themselves, correctly rounded without a division: with r = fl(1 / scale),
+//   q0 = fl(x r),  q1 = fl(q0 + r fl(x - q0 scale)),  f = fl(q1 + r (x - q1 scale)).
+// q0 is within 1.5 ulp of x / scale and q1 within one, so the second remainder is exact (a
+// multiple of ulp(q1) ulp(scale), below 2^24 of them) and f = fl(x / scale) (P. Markstein's theorem, for r
+// correctly rounded).  No remainder that matters underflows while scale >= 2^-64 (a quotient below 2^-11 has
+// code 0 in every format, however its last bits fall) and r is a normal number up to 2^64.
+constexpr float kQuotientMin = 0x1p-64f, kQuotientMax = 0x1p64f;
+
+__device__ __forceinline__ float2 quotients(float2 x, float2 r, float2 minus_scale) {
+  const float2 q0 = mul2(x, r), q1 = fma2(fma2(q0, minus_scale, x), r, q0);
+  return fma2(fma2(q1, minus_scale, x), r, q1);
+}
+__device__ __forceinline__ float with_sign(float f, float x) {   // (-0 comes out of the sums as +0)
+  return __uint_as_float((__float_as_uint(f) & 0x7FFFFFFFu) | (__float_as_uint(x) & 0x80000000u));
+}
+
+// Stores the codes of eight values as vector v of the block.  Quotients below -Q, which only codes that no encoder writes
+// lead to (-128, -8), are clamped where CLAMP says so.  Returns false, and what it stored is to be stored again,
+// where an integer format meets a NaN.
+template <int DST, bool CLAMP>
+__device__ __forceinline__ bool store_quotients8(uint8_t *dst, int v, const float (&x)[kVec], float r, float scale) {
+  const auto clamp = [](float2 q) {
+    constexpr float least = DST == CFR_FMT_I8 ? -127.f : -7.f;
+    return CLAMP ? make_float2(q.x < least ? least : q.x, q.y < least ? least : q.y) : q;
+  };
+  const float2 rr = make_float2(r, r), ms = make_float2(-scale, -scale);
+  if constexpr (DST == CFR_FMT_FP8) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float2 q = quotients(make_float2(x[2 * k], x[2 * k + 1]), rr, ms);
+      q.x = with_sign(q.x, x[2 * k]);
+      q.y = with_sign(q.y, x[2 * k + 1]);
+      w[k] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+    }
+    reinterpret_cast<uint2 *>(dst)[v] = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+    return true;
+  } else if constexpr (DST == CFR_FMT_I4) {
+    // of two elements, one sum: 1.5 * 2^23 + (c0 + 8) + 16 (c1 + 8), whose low byte with its signs
+    // put back is the byte of both
+    const float2 one = make_float2(kRintMagic, kRintMagic), both = make_float2(kRintMagic + 136.f, kRintMagic + 136.f);
+    const float2 sixteen = make_float2(16.f, 16.f), minus = make_float2(-kRintMagic, -kRintMagic);
+    uint32_t t[4];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {   // bytes 2 k and 2 k + 1
+      const float2 e = add2(clamp(quotients(make_float2(x[4 * k], x[4 * k + 2]), rr, ms)), both);
+      const float2 o = add2(add2(clamp(quotients(make_float2(x[4 * k + 1], x[4 * k + 3]), rr, ms)), one), minus);
+      const float2 y = fma2(o, sixteen, e);
+      t[2 * k] = __float_as_uint(y.x);
+      t[2 * k + 1] = __float_as_uint(y.y);
+    }
+    reinterpret_cast<uint32_t *>(dst)[v] =
+        __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410) ^ 0x88888888u;
+    return !((t[0] | t[1] | t[2] | t[3]) & 0x30000000u);   // (of 0x4B4000xx or a NaN's 0x7FFFFFFF)
+  } else {
+    const float2 one = make_float2(kRintMagic, kRintMagic);
+    uint32_t tb[kVec], any = 0u;
+#pragma unroll
+    for (int k = 0; k < kVec; k += 2) {
+      const float2 q = add2(clamp(quotients(make_float2(x[k], x[k + 1]), rr, ms)), one);
+      tb[k] = __float_as_uint(q.x);
+      tb[k + 1] = __float_as_uint(q.y);
+      any |= tb[k] | tb[k + 1];
+    }
+    store_codes8<DST>(dst, v, tb);
+    return !(any & 0x30000000u);
+  }
+}
+
 }  // namespace cfr

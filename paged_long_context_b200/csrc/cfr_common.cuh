@@ -197,6 +197,11 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// barrier `id` of a block, among n threads
+__device__ __forceinline__ void named_sync(int id, int n) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
 // two fp32 operations in one instruction
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
