@@ -343,3 +343,44 @@ def test_offsets_that_fit_several_sequences_stay_inside_the_rows():
     for b in (1, 3):
         for p in range(8):
             assert np.array_equal(before[0][I8][c.table[b, p]], after[0][I8][c.table[b, p]])
+
+
+@pytest.mark.parametrize("fmt", [I8, I4, FP8])
+@pytest.mark.parametrize("top", [1.0, 2.9921875, 0.671875, 2.0 ** -60 * 1.1171875, 2.0 ** -64 * 0.9921875, 2.0 ** 70 * 1.6640625, 2.0 ** -126,
+                                 2.0 ** -133, 3.3895314e38, float("inf")])
+def test_codes_of_every_bfloat16(fmt, top):
+    # every value up to `top`, which sets the scale, signs, zeros, subnormals and NaN among them
+    every = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    t = torch.tensor([top]).to(torch.bfloat16)
+    every = torch.where(every.abs() > t, t, every)
+    x = every.view(512, 1, 128).cuda()
+    c = Cache(1, 1, 128, 512, 1, [fmt], seed=24)
+    state = c.host()
+    assert c.write(x, x.flip(0), [0, 512], [0]) == 0
+    with np.errstate(all="ignore"):
+        c.expect_write(state, x, x.flip(0), [0, 512], [0])
+    c.same(state)
+
+
+@pytest.mark.parametrize("fmt", [I8, I4, FP8])
+@pytest.mark.parametrize("top", [448.0, 1.2345678, 3.1415927e-15, 7.7e12])
+def test_codes_beside_the_ties(fmt, top):
+    # fp32 values a few units in the last place around every tie's multiple of the scale
+    rng = np.random.default_rng(25)
+    scale = np.float32(top) / np.float32(QMAX[fmt])
+    if fmt == FP8:
+        codes = torch.arange(0x7F, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+        ties = (codes[1:] + codes[:-1]) / 2
+    else:
+        ties = np.arange(int(QMAX[fmt])) + 0.5
+    at = (ties[rng.integers(0, len(ties), 64 * 2 * 128)] * float(scale)).astype(np.float32)
+    x = (at.view(np.int32) + rng.integers(-3, 4, at.shape).astype(np.int32)).view(np.float32) * rng.choice([-1, 1], at.shape).astype(np.float32)
+    x = np.minimum(np.abs(x), np.float32(top)) * np.sign(x)
+    x = torch.from_numpy(x.astype(np.float32)).view(64, 2, 128)
+    x[0, :, 0] = top
+    k, v = x.cuda(), x.neg().cuda()
+    c = Cache(1, 2, 128, 64, 1, [fmt], seed=26)
+    state = c.host()
+    assert c.write(k, v, [0, 64], [0]) == 0
+    c.expect_write(state, k, v, [0, 64], [0])
+    c.same(state)
