@@ -66,6 +66,13 @@ constexpr int ITEM_RING = 8;   // items published
 constexpr int MAX_PIECES = 17; // pages (of 8 tokens or more) that a tile can touch
 constexpr float RESCALE_STEP = 8.f;
 
+// How scores become probabilities.  PLAIN: scaled only.  GENERAL_SCORES: capped, less a distance, or both.
+// FIXED_REFERENCE: capped scores lie within +- cap, so that the exponentials of every row can be taken against
+// one number, with no maximum and a single pass over the scores: 2^(s - 30) of |s| <= 80 (in units of log2 e,
+// caps up to 55) is between 2^-110 and 2^50, and its products and sums stay normal in bf16 and fp32.
+enum TtMode { PLAIN, GENERAL_SCORES, FIXED_REFERENCE };
+constexpr float TT_FIXED_CAP = 80.f, TT_FIXED_REF = 30.f;
+
 template <int D, int NM, bool QUANT>
 struct TtCfg {
   static constexpr int RB = NM == 1 ? 64 : 256;  // rows of an item
@@ -558,11 +565,15 @@ __device__ __forceinline__ void expand_word(uint32_t w, uint32_t *o) {
 // 64 values of a row, N 16-byte pieces of codes in the order (x + turn) mod N, into one half
 // of a slot; `row` is the row's place there and `swz` its swizzle, (row mod 8) * 16.
 template <int FMT, int N>
-__device__ __forceinline__ void expand_half(uint32_t row, uint32_t swz, int turn, const uint4 (&raw)[N]) {
+__device__ __forceinline__ void expand_half(uint32_t row, uint32_t swz, int turn, uint4 (&raw)[N]) {
+  // in two rounds of half the pieces, the second's moved to the first's registers: unrolled over all of them the code of
+  // the formats fell out of the instruction cache
+#pragma unroll 1
+  for (int x0 = 0; x0 < N; x0 += N / 2) {
 #pragma unroll
-  for (int x = 0; x < N; ++x) {
+  for (int x = 0; x < N / 2; ++x) {
     const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
-    const uint32_t at = static_cast<uint32_t>((x + turn) & (N - 1)) * (128 / N);   // its first byte in the row
+    const uint32_t at = static_cast<uint32_t>((x0 + x + turn) & (N - 1)) * (128 / N);   // its first byte in the row
 #pragma unroll
     for (int y = 0; y < 8 / N; ++y) {   // 16 bytes of bf16
       uint32_t o[4];
@@ -576,6 +587,9 @@ __device__ __forceinline__ void expand_half(uint32_t row, uint32_t swz, int turn
                    "r"(o[2]), "r"(o[3])
                    : "memory");
     }
+  }
+#pragma unroll
+  for (int x = 0; x < N / 2; ++x) raw[x] = raw[x + N / 2];
   }
 }
 __device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
@@ -928,10 +942,24 @@ __device__ __forceinline__ void tt_put(const TreeParams &p, bool part, long long
   }
 }
 
-// cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)), in units of log2 e; k1 takes x to 2 s / cap
-// in those units, c2 = cap log2 e
-__device__ __forceinline__ float tt_cap(float x, float k1, float c2) {
-  return fmaf(-2.f * c2, rcp_approx(1.f + exp2_approx(x * k1)), c2);
+// Caps: c2 tanh(u) of u = s / cap, c2 = cap log2 e (scores are in units of log2 e from here on).
+// Up to |u| = 3/4 tanh(u) = u + u z q(z), z = u^2, q of degree 4 with the least greatest relative
+// error of the whole (2^-24.9, found by exchange): multiply-adds, where the closed form below takes two of the 16
+// special functions a clock and SM, three with the exponential that follows, which bound a capped call (eight
+// sequences of 32K tokens in tiers: 360 us with the closed form alone, 267 without a cap, SUM_FIG with this).
+constexpr float TT_CAP_NEAR = 0.75f;
+__device__ __forceinline__ float2 tt_cap_near(float2 u, float c2) {
+  const float2 z = mul2(u, u), w = mul2(u, make_float2(c2, c2));
+  float2 q = make_float2(-0.0047694905661046505f, -0.0047694905661046505f);
+  q = fma2(q, z, make_float2(0.019664913415908813f, 0.019664913415908813f));
+  q = fma2(q, z, make_float2(-0.0533902570605278f, -0.0533902570605278f));
+  q = fma2(q, z, make_float2(0.13326521217823029f, 0.13326521217823029f));
+  q = fma2(q, z, make_float2(-0.3333306908607483f, -0.3333306908607483f));
+  return fma2(mul2(w, z), q, w);
+}
+// c2 - 2 c2 / (1 + e^(2 u)), off by 2^-22 of c2
+__device__ __forceinline__ float tt_cap_far(float u, float c2) {
+  return fmaf(-2.f * c2, rcp_approx(1.f + exp2_approx(u * (2.f * kLog2e))), c2);
 }
 
 // Finishes, in TMEM, the scores of a step that has tokens which a row does not see.  Out
@@ -941,7 +969,7 @@ __device__ __forceinline__ float tt_cap(float x, float k1, float c2) {
 template <bool GENERAL>
 __device__ __noinline__ void tt_masked(const TreeParams &p, uint32_t s_at, int width, unsigned long long seen,
                                        const float *ks, float scale, float slope, int pos, int pre, int off, int c, int b) {
-  const float k1 = 2.f / p.cap, c2 = p.cap * kLog2e;
+  const float to_u = 1.f / (p.cap * kLog2e), c2 = p.cap * kLog2e;
 #pragma unroll 1
   for (int ch = 0; ch < width; ch += 16) {
     float x[16];
@@ -951,7 +979,10 @@ __device__ __noinline__ void tt_masked(const TreeParams &p, uint32_t s_at, int w
     for (int i = 0; i < 16; ++i) {
       const int d = ch + i - off;   // draft
       float y = x[i] * (ks ? ks[ch + i] : scale);
-      if (GENERAL && p.cap > 0.f) y = tt_cap(y, k1, c2);
+      if (GENERAL && p.cap > 0.f) {
+        const float u = y * to_u;
+        y = fabsf(u) <= TT_CAP_NEAR ? tt_cap_near(make_float2(u, u), c2).x : tt_cap_far(u, c2);
+      }
       if (GENERAL && p.slopes) {
         int far = pre + d - pos;
         if (d >= 0 && d < c && p.depths) far = pre + p.depths[static_cast<long long>(b) * p.nq + d] - pos;
@@ -964,9 +995,10 @@ __device__ __noinline__ void tt_masked(const TreeParams &p, uint32_t s_at, int w
   tt_wait_st();
 }
 
-template <int D, int NM, bool QUANT, bool GENERAL>
+template <int D, int NM, bool QUANT, int MODE>
 __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
   using Cfg = TtCfg<D, NM, QUANT>;
+  constexpr bool GENERAL = MODE != PLAIN, FIXED = MODE == FIXED_REFERENCE;
   const TreeParams &p = c.p;
   const int m = NM == 2 ? (threadIdx.x - Cfg::SOFTMAX_T0) >> 7 : 0;
   const int r = threadIdx.x & 127;
@@ -1161,70 +1193,80 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
         tt_masked<GENERAL>(p, s_at, row.width, seen, scaled ? ks : nullptr, scale, row.slope, row.pos, pre, off, it.c, it.b);
         sc = 1.f;
       }
-      // CH tokens at a time, the last first; the second pass then begins with the
-      // ones that are in registers
-      const bool finish_here = !masked && ((QUANT && scaled && !one_page) || (GENERAL && (p.cap > 0.f || p.slopes)));
+      const bool finish_here = !masked && ((QUANT && scaled && !one_page) || (GENERAL && (p.cap > 0.f || (!FIXED && p.slopes))));
       const float sc_in = sc;
       if (finish_here) sc = 1.f;
       const bool half = CH == 64 && row.width == 32;   // (the rest of x is not used then)
       float x[CH], top = -INFINITY;
-#pragma unroll 1
-      for (int ch = half ? 0 : row.width - CH; ch >= 0; ch -= CH) {
+      const auto load = [&](int ch) {
         tt_ld32(s_at + ch, x);
         if (CH == 64 && !half) tt_ld32(s_at + ch + 32, x + CH - 32);
         tc_wait_ld();
-        if ((QUANT || GENERAL) && finish_here) {
-          float mul = sc_in;   // what is still to be multiplied
-          if (QUANT && scaled && !one_page) {
+      };
+      const auto complete = [&](int ch) {
+        float mul = sc_in;   // what is still to be multiplied
+        if (QUANT && scaled && !one_page) {
 #pragma unroll
-            for (int i = 0; i < CH; i += 4) {
-              if (i == 32 && half) break;
-              const float4 k4 = *reinterpret_cast<const float4 *>(ks + ch + i);
-              const float2 y = mul2(make_float2(x[i], x[i + 1]), make_float2(k4.x, k4.y));
-              const float2 z = mul2(make_float2(x[i + 2], x[i + 3]), make_float2(k4.z, k4.w));
-              x[i] = y.x;
-              x[i + 1] = y.y;
-              x[i + 2] = z.x;
-              x[i + 3] = z.y;
-            }
-            mul = 1.f;
+          for (int i = 0; i < CH; i += 4) {
+            if (i == 32 && half) break;
+            const float4 k4 = *reinterpret_cast<const float4 *>(ks + ch + i);
+            const float2 y = mul2(make_float2(x[i], x[i + 1]), make_float2(k4.x, k4.y));
+            const float2 z = mul2(make_float2(x[i + 2], x[i + 3]), make_float2(k4.z, k4.w));
+            x[i] = y.x;
+            x[i + 1] = y.y;
+            x[i + 2] = z.x;
+            x[i + 3] = z.y;
           }
-          if (GENERAL && p.cap > 0.f) {
-            const float c2 = p.cap * kLog2e;
-            const float2 k1 = make_float2(mul * 2.f / p.cap, mul * 2.f / p.cap);
-#pragma unroll
-            for (int i = 0; i < CH; i += 2) {
-              if (i == 32 && half) break;
-              const float2 y = mul2(make_float2(x[i], x[i + 1]), k1);
-              const float2 z = add2(make_float2(exp2_approx(y.x), exp2_approx(y.y)), make_float2(1.f, 1.f));
-              const float2 w = fma2(make_float2(rcp_approx(z.x), rcp_approx(z.y)), make_float2(-2.f * c2, -2.f * c2), make_float2(c2, c2));
-              x[i] = w.x;
-              x[i + 1] = w.y;
-            }
-            mul = 1.f;
-          }
-          if (GENERAL && p.slopes) {
-            const float base = row.slope * static_cast<float>(pre - off + ch - row.pos);
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-              if (i == 32 && half) break;
-              x[i] = fmaf(x[i], mul, fmaf(row.slope, static_cast<float>(i), base));
-            }
-          }
-          if (CH == 32 && ch > 0) tt_st32(s_at + ch, reinterpret_cast<const uint32_t *>(x));
+          mul = 1.f;
         }
-        float mx[4] = {x[0], x[1], x[2], x[3]};
+        if (GENERAL && p.cap > 0.f) {
+          const float c2 = p.cap * kLog2e, to_u = mul / c2;
+          const float2 k1 = make_float2(to_u * 2.f * kLog2e, to_u * 2.f * kLog2e);
 #pragma unroll
-        for (int i = 4; i < CH; i += 4) {
-          if (i == 32 && half) break;
-#pragma unroll
-          for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], x[i + y]);
+          for (int i = 0; i < CH; i += 2) {
+            if (i == 32 && half) break;
+            const float2 y = mul2(make_float2(x[i], x[i + 1]), k1);
+            const float2 z = add2(make_float2(exp2_approx(y.x), exp2_approx(y.y)), make_float2(1.f, 1.f));
+            const float2 w = fma2(make_float2(rcp_approx(z.x), rcp_approx(z.y)), make_float2(-2.f * c2, -2.f * c2), make_float2(c2, c2));
+            x[i] = w.x;
+            x[i + 1] = w.y;
+          }
+          mul = 1.f;
         }
-        top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+        if (GENERAL && !FIXED && p.slopes) {
+          const float base = row.slope * static_cast<float>(pre - off + ch - row.pos);
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            if (i == 32 && half) break;
+            x[i] = fmaf(x[i], mul, fmaf(row.slope, static_cast<float>(i), base));
+          }
+        }
+      };
+      if constexpr (!FIXED) {
+        // CH tokens at a time, the last first; the second pass then begins with the
+        // ones that are in registers
+#pragma unroll 1
+        for (int ch = half ? 0 : row.width - CH; ch >= 0; ch -= CH) {
+          load(ch);
+          if ((QUANT || GENERAL) && finish_here) {
+            complete(ch);
+            if (CH == 32 && ch > 0) tt_st32(s_at + ch, reinterpret_cast<const uint32_t *>(x));
+          }
+          float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int i = 4; i < CH; i += 4) {
+            if (i == 32 && half) break;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], x[i + y]);
+          }
+          top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+        }
+        if (CH == 32 && (QUANT || GENERAL) && finish_here) tt_wait_st();
       }
-      if (CH == 32 && (QUANT || GENERAL) && finish_here) tt_wait_st();
       top *= sc;
-      if (s == 0) {
+      if (FIXED) {
+        ref = TT_FIXED_REF;
+      } else if (s == 0) {
         ref = top;
       } else if (__any_sync(0xffffffffu, top > ref + RESCALE_STEP)) {
         // O of the steps so far moves to the new reference
@@ -1254,33 +1296,32 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
       const float2 less2 = make_float2(less, less), sc2 = make_float2(sc, sc);
       float2 sum[2] = {};
       const uint32_t p_at = lanes + Cfg::p_col(m, b) + first / 2;
-      const auto exps = [&](auto by_token) {
-#pragma unroll 1
-        for (int ch = 0; ch < row.width; ch += CH) {
-          if (ch > 0) {
-            tt_ld32(s_at + ch, x);
-            tc_wait_ld();
-          }
+      const auto exps = [&](int ch, auto by_token) {
 #pragma unroll
-          for (int i0 = 0; i0 < CH; i0 += 32) {
-            if (i0 == 32 && half) break;
-            uint32_t w[16];
+        for (int i0 = 0; i0 < CH; i0 += 32) {
+          if (i0 == 32 && half) break;
+          uint32_t w[16];
 #pragma unroll
-            for (int i = i0; i < i0 + 32; i += 2) {
-              const float2 y = fma2(make_float2(x[i], x[i + 1]), sc2, less2);
-              float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-              sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], e);
-              if (decltype(by_token)::value) e = mul2(e, *reinterpret_cast<const float2 *>(vs + ch + i));
-              w[(i - i0) >> 1] = pack_bf16(e.x, e.y);
-            }
-            tt_st16(p_at + (ch + i0) / 2, w);   // (over columns of S that were read before)
+          for (int i = i0; i < i0 + 32; i += 2) {
+            const float2 y = fma2(make_float2(x[i], x[i + 1]), sc2, less2);
+            float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+            sum[(i >> 1) & 1] = add2(sum[(i >> 1) & 1], e);
+            if (decltype(by_token)::value) e = mul2(e, *reinterpret_cast<const float2 *>(vs + ch + i));
+            w[(i - i0) >> 1] = pack_bf16(e.x, e.y);
           }
+          tt_st16(p_at + (ch + i0) / 2, w);   // (over columns of S that were read before)
         }
       };
-      if (QUANT && scaled && !one_page)
-        exps(std::true_type());
-      else
-        exps(std::false_type());
+      const bool by_token = QUANT && scaled && !one_page;
+#pragma unroll 1
+      for (int ch = 0; ch < row.width; ch += CH) {
+        if (FIXED || ch > 0) load(ch);
+        if (FIXED && finish_here) complete(ch);
+        if (QUANT && by_token)
+          exps(ch, std::true_type());
+        else
+          exps(ch, std::false_type());
+      }
       const float2 s01 = add2(sum[0], sum[1]);
       l += (s01.x + s01.y) * back;
       tt_wait_st();
@@ -1305,7 +1346,7 @@ constexpr size_t tt_smem() {
   return tt_head<D, NM, QUANT>() + static_cast<size_t>(NM + Cfg::NS) * Cfg::ROW_TILE + 1024;
 }
 
-template <int D, int NM, bool QUANT, bool GENERAL>
+template <int D, int NM, bool QUANT, int MODE>
 __global__ void __launch_bounds__((TtCfg<D, NM, QUANT>::THREADS), 1)
     tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap) {
@@ -1366,7 +1407,7 @@ __global__ void __launch_bounds__((TtCfg<D, NM, QUANT>::THREADS), 1)
       tt_issue<D, NM, QUANT>(c, &timed_out, warp - 1);
     }
   } else if (wg <= NM) {
-    tt_softmax<D, NM, QUANT, GENERAL>(c, &timed_out);
+    tt_softmax<D, NM, QUANT, MODE>(c, &timed_out);
   } else if constexpr (QUANT) {
     tt_expand<D, NM>(c, &timed_out, Cfg::LOADERS == 1 ? 2 : wg - NM - 1);
   }
@@ -1379,10 +1420,10 @@ __global__ void __launch_bounds__((TtCfg<D, NM, QUANT>::THREADS), 1)
   }
 }
 
-template <int D, int NM, bool QUANT, bool GENERAL>
+template <int D, int NM, bool QUANT, int MODE>
 cudaError_t launch(const TreeParams &p, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t s) {
   using Cfg = TtCfg<D, NM, QUANT>;
-  auto kernel = tree_tc_kernel<D, NM, QUANT, GENERAL>;
+  auto kernel = tree_tc_kernel<D, NM, QUANT, MODE>;
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(tt_smem<D, NM, QUANT>()));
   if (e != cudaSuccess) return e;
@@ -1391,18 +1432,18 @@ cudaError_t launch(const TreeParams &p, const CUtensorMap &k, const CUtensorMap 
 }
 
 template <int D, int NM, bool QUANT>
-cudaError_t launch_general_or_plain(const TreeParams &p, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t s) {
-  return p.cap > 0.f || p.slopes ? launch<D, NM, QUANT, true>(p, k, v, s) : launch<D, NM, QUANT, false>(p, k, v, s);
+cudaError_t launch_mode(const TreeParams &p, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t s) {
+  if (p.cap > 0.f && !p.slopes && p.cap * kLog2e <= TT_FIXED_CAP) return launch<D, NM, QUANT, FIXED_REFERENCE>(p, k, v, s);
+  return p.cap > 0.f || p.slopes ? launch<D, NM, QUANT, GENERAL_SCORES>(p, k, v, s) : launch<D, NM, QUANT, PLAIN>(p, k, v, s);
 }
 
 }  // namespace
 
 // Whether the tensor-core kernel takes the call: bf16 queries, no fp32 pages, pages a multiple of 8 tokens, and
-// a cap up to 2^10: its form of the tanh (see tt_cap) is off by 2^-22 of the cap, whatever the score, which at
-// 2^10 is still below the rounding of P.
+// a cap between 2^-10 and 2^40 (the products with it and its inverse stay far from the borders of fp32).
 bool tree_tc_supported(const TreeParams &p) {
   if (p.q_fmt != CFR_FMT_BF16 || p.P % 8 != 0 || p.P > (1 << 24)) return false;
-  if (p.cap > 0.f && !(p.cap >= 0x1p-10f && p.cap <= 0x1p10f)) return false;
+  if (p.cap > 0.f && !(p.cap >= 0x1p-10f && p.cap <= 0x1p40f)) return false;
   if (p.page_fmt ? p.k_pool[CFR_FMT_F32] != nullptr : p.uniform_fmt == CFR_FMT_F32) return false;
   return p.pool_pages[CFR_FMT_BF16] * p.Hkv <= 0x7fffffffLL / p.P;   // rows of a tensor map
 }
@@ -1425,12 +1466,12 @@ cudaError_t launch_tree_tc(const TreeParams &p, int rb, cudaStream_t s) {
   if (p.page_fmt) quant = p.k_pool[CFR_FMT_I8] || p.k_pool[CFR_FMT_I4] || p.k_pool[CFR_FMT_FP8];
   if (p.D == 128) {
     if (rb == 64)
-      return quant ? launch_general_or_plain<128, 1, true>(p, k, v, s) : launch_general_or_plain<128, 1, false>(p, k, v, s);
-    return quant ? launch_general_or_plain<128, 2, true>(p, k, v, s) : launch_general_or_plain<128, 2, false>(p, k, v, s);
+      return quant ? launch_mode<128, 1, true>(p, k, v, s) : launch_mode<128, 1, false>(p, k, v, s);
+    return quant ? launch_mode<128, 2, true>(p, k, v, s) : launch_mode<128, 2, false>(p, k, v, s);
   }
   if (rb == 64)
-    return quant ? launch_general_or_plain<64, 1, true>(p, k, v, s) : launch_general_or_plain<64, 1, false>(p, k, v, s);
-  return quant ? launch_general_or_plain<64, 2, true>(p, k, v, s) : launch_general_or_plain<64, 2, false>(p, k, v, s);
+    return quant ? launch_mode<64, 1, true>(p, k, v, s) : launch_mode<64, 1, false>(p, k, v, s);
+  return quant ? launch_mode<64, 2, true>(p, k, v, s) : launch_mode<64, 2, false>(p, k, v, s);
 }
 
 }  // namespace cfr
