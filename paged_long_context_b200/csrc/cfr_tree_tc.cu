@@ -69,7 +69,8 @@ constexpr float RESCALE_STEP = 8.f;
 // How scores become probabilities.  PLAIN: scaled only.  GENERAL_SCORES: capped, less a distance, or both.
 // FIXED_REFERENCE: capped scores lie within +- cap, so that the exponentials of every row can be taken against
 // one number, with no maximum and a single pass over the scores: 2^(s - 30) of |s| <= 80 (in units of log2 e,
-// caps up to 55) is between 2^-110 and 2^50, and its products and sums stay normal in bf16 and fp32.
+// caps up to 55) is between 2^-110 and 2^50, and its products and sums stay normal in bf16 and fp32.  (Eight
+// sequences of 32K tiered tokens, capped at 50: 279 us, and 360 in two passes.)
 enum TtMode { PLAIN, GENERAL_SCORES, FIXED_REFERENCE };
 constexpr float TT_FIXED_CAP = 80.f, TT_FIXED_REF = 30.f;
 
@@ -197,6 +198,12 @@ __device__ __forceinline__ void tt_wait_st() { asm volatile("tcgen05.wait::st.sy
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -944,9 +951,9 @@ __device__ __forceinline__ void tt_put(const TreeParams &p, bool part, long long
 
 // Caps: c2 tanh(u) of u = s / cap, c2 = cap log2 e (scores are in units of log2 e from here on).
 // Up to |u| = 3/4 tanh(u) = u + u z q(z), z = u^2, q of degree 4 with the least greatest relative
-// error of the whole (2^-24.9, found by exchange): multiply-adds, where the closed form below takes two of the 16
-// special functions a clock and SM, three with the exponential that follows, which bound a capped call (eight
-// sequences of 32K tokens in tiers: 360 us with the closed form alone, 267 without a cap, SUM_FIG with this).
+// error of the whole (2^-24.9, found by exchange): multiply-adds, where the closed form takes two of the 16
+// special functions a clock and SM, three with the exponential that follows (the ragged batch of 64 drafts,
+// capped at 50: 576 us with the closed form, 497 with this).
 constexpr float TT_CAP_NEAR = 0.75f;
 __device__ __forceinline__ float2 tt_cap_near(float2 u, float c2) {
   const float2 z = mul2(u, u), w = mul2(u, make_float2(c2, c2));
@@ -1005,6 +1012,8 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
   const uint32_t lanes = c.S.tmem_base + (static_cast<uint32_t>(r & 96) << 16);   // this warp's TMEM lanes
   const uint32_t o_at = lanes + Cfg::O_COL + m * 128;
   const float scale = p.sigma * kLog2e;
+  // caps: c2 tanh(s / cap), s / cap in units of log2 e / 2 being the score times cap_k1 (see tt_cap_far)
+  const float c2 = p.cap * kLog2e, cap_k1 = GENERAL ? 2.f / p.cap : 0.f;
   // scores that a thread holds at once: a step's 64 where the code for them fits the instruction cache beside
   // the other roles (in registers throughout: 1M tokens 764 us against 865), 32 with the expansion of codes
   constexpr int CH = QUANT ? 32 : 64;
@@ -1220,16 +1229,50 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
           mul = 1.f;
         }
         if (GENERAL && p.cap > 0.f) {
-          const float c2 = p.cap * kLog2e, to_u = mul / c2;
-          const float2 k1 = make_float2(to_u * 2.f * kLog2e, to_u * 2.f * kLog2e);
+          if constexpr (QUANT) {
+            // the closed form throughout: with the polynomial's code beside the expansion's, fetching instructions
+            // took longer than the special functions (tiers of 32K tokens: 356 us against 318)
+            const float2 k1 = make_float2(mul * cap_k1, mul * cap_k1);
 #pragma unroll
-          for (int i = 0; i < CH; i += 2) {
-            if (i == 32 && half) break;
-            const float2 y = mul2(make_float2(x[i], x[i + 1]), k1);
-            const float2 z = add2(make_float2(exp2_approx(y.x), exp2_approx(y.y)), make_float2(1.f, 1.f));
-            const float2 w = fma2(make_float2(rcp_approx(z.x), rcp_approx(z.y)), make_float2(-2.f * c2, -2.f * c2), make_float2(c2, c2));
-            x[i] = w.x;
-            x[i + 1] = w.y;
+            for (int i = 0; i < CH; i += 2) {
+              const float2 y = mul2(make_float2(x[i], x[i + 1]), k1);
+              const float2 z = add2(make_float2(exp2_approx(y.x), exp2_approx(y.y)), make_float2(1.f, 1.f));
+              x[i] = rcp_approx(z.x);
+              x[i + 1] = rcp_approx(z.y);
+              if (!FIXED) {   // (else with the reference, below)
+                const float2 w = fma2(make_float2(x[i], x[i + 1]), make_float2(-2.f * c2, -2.f * c2), make_float2(c2, c2));
+                x[i] = w.x;
+                x[i + 1] = w.y;
+              }
+            }
+          } else {
+            const float to_u = mul * cap_k1 * (0.5f / kLog2e);
+            const float2 u2 = make_float2(to_u, to_u);
+            float most[2] = {0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < CH; i += 2) {
+              if (i == 32 && half) break;
+              const float2 u = mul2(make_float2(x[i], x[i + 1]), u2);
+              x[i] = u.x;
+              x[i + 1] = u.y;
+              most[0] = fmaxf(most[0], fabsf(u.x));
+              most[1] = fmaxf(most[1], fabsf(u.y));
+            }
+            if (__any_sync(0xffffffffu, fmaxf(most[0], most[1]) > TT_CAP_NEAR)) {
+#pragma unroll
+              for (int i = 0; i < CH; ++i) {
+                if (i == 32 && half) break;
+                x[i] = tt_cap_far(x[i], c2);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < CH; i += 2) {
+                if (i == 32 && half) break;
+                const float2 y = tt_cap_near(make_float2(x[i], x[i + 1]), c2);
+                x[i] = y.x;
+                x[i + 1] = y.y;
+              }
+            }
           }
           mul = 1.f;
         }
@@ -1290,8 +1333,12 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
       // p = 2^(s - ref), its sum, and P as the MMA's operand
       float less = ref == -INFINITY ? 0.f : -ref, back = 1.f;
       if (QUANT && one_page) {
-        less += log2f(vs[0]);
-        back = 1.f / vs[0];
+        less += lg2_approx(vs[0]);   // (2^-22 off, like the exponential itself)
+        back = rcp_approx(vs[0]);
+      }
+      if (FIXED && QUANT && finish_here) {
+        less += c2;
+        sc = -2.f * c2;
       }
       const float2 less2 = make_float2(less, less), sc2 = make_float2(sc, sc);
       float2 sum[2] = {};
@@ -1440,10 +1487,11 @@ cudaError_t launch_mode(const TreeParams &p, const CUtensorMap &k, const CUtenso
 }  // namespace
 
 // Whether the tensor-core kernel takes the call: bf16 queries, no fp32 pages, pages a multiple of 8 tokens, and
-// a cap between 2^-10 and 2^40 (the products with it and its inverse stay far from the borders of fp32).
+// a cap between 2^-10 and 2^10 (the closed form of the tanh, see tt_cap_far, is off by 2^-22 of the cap, whatever the
+// score, which at 2^10 is still below the rounding of P).
 bool tree_tc_supported(const TreeParams &p) {
   if (p.q_fmt != CFR_FMT_BF16 || p.P % 8 != 0 || p.P > (1 << 24)) return false;
-  if (p.cap > 0.f && !(p.cap >= 0x1p-10f && p.cap <= 0x1p40f)) return false;
+  if (p.cap > 0.f && !(p.cap >= 0x1p-10f && p.cap <= 0x1p10f)) return false;
   if (p.page_fmt ? p.k_pool[CFR_FMT_F32] != nullptr : p.uniform_fmt == CFR_FMT_F32) return false;
   return p.pool_pages[CFR_FMT_BF16] * p.Hkv <= 0x7fffffffLL / p.P;   // rows of a tensor map
 }
