@@ -359,3 +359,32 @@ def test_caps_far_above_the_scores_change_nothing(name, cap):
     assert call.run() == 0
     call.cap = 0.0    # a score of 30 is 1e-10 off under a cap of 1e7: the formula's and the bounds without one
     call.check()
+
+
+@pytest.mark.parametrize("name", ["bf16-p16", "tiered-p128", "f32-p16"])
+@pytest.mark.parametrize("cap,lean", [(30.0, -1.0), (55.0, -1.0), (55.0, 1.0), (55.0, 0.0), (60.0, -1.0)])
+def test_scores_at_both_ends_of_the_cap(name, cap, lean):
+    # queries so long that most scores stand at one end of the cap (all of them below, all above, or both)
+    case = tree_case((133, 700), 5, **CONFIGS[name])
+    call = TreeCall(case, *trees(2, 5, 22), cap=cap)
+    if lean:
+        if "tiered" in name:    # codes of one sign: each row's scores lean one way by the queries' sign
+            for f in case.k_pool:
+                if f == synth.BF16:
+                    case.k_pool[f].copy_(case.k_pool[f].view(torch.bfloat16).abs().view(case.k_pool[f].dtype).view_as(case.k_pool[f]))
+                elif f == synth.I8:
+                    case.k_pool[f].bitwise_and_(0x3F)
+                elif f == synth.I4:
+                    case.k_pool[f].bitwise_and_(0x77)
+                else:
+                    case.k_pool[f].bitwise_and_(0x7F)
+        else:
+            dt = torch.float32 if name.startswith("f32") else torch.bfloat16
+            for f in case.k_pool:
+                k = case.k_pool[f].view(dt)
+                k.copy_(k.abs())
+        call.q.copy_(call.q.abs() * lean * 60)
+    else:
+        call.q.mul_(60)
+    assert call.run() == 0
+    call.check()
