@@ -6,18 +6,22 @@
 //   scale' = max(kept ? scale : 0, max|x| / Q),
 //   kept rows: code <- nearest(code * scale / scale') when scale' > scale,
 //   new rows:  code  = nearest(x / scale').
-// One CTA per (touched page of a sequence, kv head, K or V): pass 1 takes max|x|
-// over the page's new rows and pass 2 codes them, from registers when the rows fit them.  Which pages
-// are touched stands in device memory only, so the grid covers the most pages
-// that `num_rows` rows of `batch` sequences can touch: sequence b's k-th touched page is CTA
-// row_offsets[b] / P + 2 b + k, and a CTA finds its b by search.  (L rows touch at most L / P + 2 pages of P, wherever they start, so
-// the numbers never collide.)
+// A team of 32 to 256 threads takes one (touched page of a sequence, kv head, K or V):
+// its new rows come into shared memory by asynchronous copies, pass 1 takes max|x|
+// over them and pass 2 codes them.  Which pages are touched stands in device memory
+// only, so the grid covers the most pages that `num_rows` rows of `batch`
+// sequences can touch: sequence b's k-th touched page is number
+// row_offsets[b] / P + 2 b + k, and a CTA finds its b by search.  (L rows touch at
+// most L / P + 2 pages of P, wherever they start, so the numbers never collide.)
 //
 // Read-back.  One CTA per few rows of the output; the rows' places are
 // resolved once, one row a thread, and every thread then expands vectors of
 // eight values.
 //
-// Both are bound by HBM: dense rows once, stored rows once.
+// Floor of both: HBM, dense rows once and stored rows once.  The write comes to 3.1 TB/s (34K bf16 tokens of 8
+// heads of 128 into int4 pages: 52 us): about ten instructions a value take half the
+// issue slots, and a page's two passes leave gaps that three blocks an SM do not
+// close.  Read-back runs at the copy rate (8 x 32K tokens of tiers to bf16: 176 us, 6.1 TB/s).
 #include <type_traits>
 
 #include "cfr_cells.cuh"
@@ -60,7 +64,7 @@ __device__ __forceinline__ Chunk chunk_of(const ChunkParams &p, int b) {
 // bf16 values; three such blocks fit an SM, so that one's loads run under the others' encoding).
 constexpr int kWriteStage = 65536;
 constexpr int kWriteThreads = 256;
-constexpr int kTeamVectors = 8;        // vectors of a page for each thread of a team, up to the block's threads
+constexpr int kTeamVectors = 16;       // vectors of a page for each thread of a team, up to the block's threads
 
 // Eight values of vector v stored as codes: by the quotients where the scale allows it, else (and where a NaN is
 // among integers) with the division.
@@ -85,9 +89,10 @@ __device__ __forceinline__ void store_kept(uint8_t *page, int tid, int T, int nv
   }
 }
 
-// T = 32 .. 256 threads, a team, take a page of one kv head, K or V: an eighth of its vectors,
+// T = 32 .. 256 threads, a team, take a page of one kv head, K or V: a sixteenth of its vectors,
 // so that what a page costs before its values (finding the sequence, resolving the page, joining the
-// maxima) is spread over eight vectors a thread.
+// maxima) is spread over sixteen vectors a thread.  (34K tokens into pages of 32 as int4, written and read back:
+// 96 us with sixteen, 100 with eight, 160 with two; into pages of 64: 97 with sixteen, 123 with thirty-two.)
 //
 // Warp 0 works out the block's page, once for all.
 struct WritePage {
@@ -435,7 +440,8 @@ cfr_status cfr_read_kv(const cfr_kv_pool *kv, const int32_t *page_table, int32_t
   p.k_out = k_out;
   p.v_out = v_out;
   // rows of a block: 32 where that leaves a block for every SM several times over, fewer for
-  // short chunks (a few hundred rows have to reach all SMs)
+  // short chunks, which have to reach all SMs (8 x 32K tokens of tiers: 178 us with 32, 203 with 4; 333 int8
+  // tokens: 7.8 us with 32, 3.1 with 4)
   int per = 32;
   while (per > 4 && num_rows < per * 600) per >>= 1;
   const unsigned blocks = static_cast<unsigned>((static_cast<long long>(num_rows) + per - 1) / per);

@@ -8,12 +8,17 @@
 // ulp of 0.06 rad); its sine and cosine, the norm's sum and the products are
 // fp32, rounded once where the row is stored.
 //
-// A CTA takes one token of a short step, four of a long one (kRopeTokens): their
-// cosines and sines are computed once, a thread each, behind one barrier, and serve
-// all query and key rows, the first token's values being on their way meanwhile.  A row is head_dim / 8 lanes of eight values: where
-// pairs lie half a rotation apart, four values of each half, so that a rotation
-// needs no other lane; the row's sum of squares is the only thing that travels
-// by shuffles.  Bound by HBM: every value is read once and written once.
+// A CTA takes one token of a short step, four of a long one: their cosines and
+// sines are computed once, a thread each, behind one barrier, and serve all query
+// and key rows, the first token's values being on their way meanwhile.  A row is
+// head_dim / 8 lanes of eight values: where pairs lie half a rotation apart, four
+// values of each half, so that a rotation needs no other lane; the row's sum of
+// squares is the only thing that travels by shuffles.
+//
+// Bound by HBM (every value is read once and written once) as far as the loads of
+// a token hide each other: 17K tokens of 32 + 2 x 8 bf16 heads of 128 take 95 us,
+// 4.5 TB/s; a decode step of one token 3.4 us of GPU time, the launch and one chain
+// of lookups.
 #include "cfr_cells.cuh"
 
 namespace cfr {
@@ -284,9 +289,9 @@ cfr_status cfr_qk_norm_rope_append(const cfr_kv_pool *kv, const int32_t *page_ta
   p.num_q_heads = num_q_heads;
   p.rot = rotary_dim;
   p.num_tokens = num_tokens;
-  // several tokens a CTA once one each would be eight waves of CTAs on 148 SMs (17K tokens: 101 us with one,
-  // see above with four); a decode step's few tokens get a CTA each
-  p.per = num_tokens >= 4096 ? kRopeTokens : 1;
+  // several tokens a CTA once that leaves every SM a CTA or two (17K tokens: 108 us with one, 95 with four; 1.5K fp32
+  // tokens 15.6 and 14.3); a short step's few tokens get a CTA each
+  p.per = num_tokens >= 1024 ? kRopeTokens : 1;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (in_fmt == CFR_FMT_F32)
     interleaved ? launch_rope<CFR_FMT_F32, true>(p, s) : launch_rope<CFR_FMT_F32, false>(p, s);

@@ -5,7 +5,7 @@
 // rows); it spans the ceil(n_b / TT) token tiles of the sequence.  The tiles of
 // all items, in that order, are one line of W units, and CTA i of G takes the
 // units [W i / G, W (i + 1) / G): every CTA gets the same number of tiles
-// whatever the lengths (an item counts as TREE_ITEM_COST tiles more than it has, for what beginning and
+// whatever the lengths (an item counts as tree_item_cost tiles more than it has, for what beginning and
 // ending one takes; those units come before its first tile).  A CTA's stretch covers at most one item's end, whole
 // items, and one item's beginning, so it leaves at most two partials: slot 2 i
 // for an item that began in an earlier CTA, 2 i + 1 for one that goes on in a
@@ -17,7 +17,10 @@
 
 namespace cfr {
 
-constexpr int TREE_ITEM_COST = 2;
+// In tiles.  Items of 256 rows end with 64 KiB to write (16 ragged sequences, 64 drafts: 377 us with 0, 343 with
+// 2, 330 with 6, 342 with 10); smaller ones end sooner (5 drafts: 254 us with 2, 259 with 6).
+template <int RB>
+constexpr int tree_item_cost = RB == 256 ? 6 : 2;
 
 struct TreeParams {
   const void *q;
@@ -61,11 +64,13 @@ __device__ __forceinline__ int tree_blocks(const TreeParams &p, int c, int g) {
 }
 
 // Units of a sequence's items, and the tile at unit `off` of an item.
+template <int RB>
 __device__ __forceinline__ long long tree_units(const TreeSeq &s) {
-  return static_cast<long long>(s.blocks) * (s.tiles + TREE_ITEM_COST);
+  return static_cast<long long>(s.blocks) * (s.tiles + tree_item_cost<RB>);
 }
+template <int RB>
 __device__ __forceinline__ int tree_tile(long long off) {
-  return off > TREE_ITEM_COST ? static_cast<int>(off - TREE_ITEM_COST) : 0;
+  return off > tree_item_cost<RB> ? static_cast<int>(off - tree_item_cost<RB>) : 0;
 }
 
 template <int TT, int RB>
@@ -134,7 +139,7 @@ __device__ __forceinline__ long long tree_find(const TreeParams &p, TreeScratch 
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
     const TreeSeq q = tree_seq<TT, RB>(p, b);
-    mine += tree_units(q);
+    mine += tree_units<RB>(q);
   }
   long long incl = mine;
   const int lane = tid & 31;
@@ -157,7 +162,7 @@ __device__ __forceinline__ long long tree_find(const TreeParams &p, TreeScratch 
     int b = b0;
     for (;; ++b) {
       const TreeSeq q = tree_seq<TT, RB>(p, b);
-      const long long units = tree_units(q);
+      const long long units = tree_units<RB>(q);
       if (u < at + units) break;
       at += units;
     }
@@ -179,17 +184,17 @@ __device__ __forceinline__ bool tree_next(const TreeParams &p, TreeCursor &cur, 
   do {
     if (cur.u >= cur.end) return false;
     s = tree_seq<TT, RB>(p, cur.b);
-    while (cur.u >= cur.base + tree_units(s)) {
-      cur.base += tree_units(s);
+    while (cur.u >= cur.base + tree_units<RB>(s)) {
+      cur.base += tree_units<RB>(s);
       s = tree_seq<TT, RB>(p, ++cur.b);
     }
-    const int each = s.tiles + TREE_ITEM_COST;
+    const int each = s.tiles + tree_item_cost<RB>;
     const long long off = cur.u - cur.base;
     item = off >> 32 ? static_cast<int>(off / each) : static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(each));
     const long long in = off - static_cast<long long>(item) * each;   // units of the item before u
     const long long to = min(static_cast<long long>(each), in + (cur.end - cur.u));
-    it.t0 = tree_tile(in);
-    it.t1 = tree_tile(to);
+    it.t0 = tree_tile<RB>(in);
+    it.t1 = tree_tile<RB>(to);
     cur.u += to - in;
   } while (it.t0 == it.t1);
   it.tiles = s.tiles;
