@@ -617,10 +617,11 @@ size_t cfr_paged_decode_tree_workspace_size(int32_t batch, int32_t num_queries,
  *  workspace   device, >= cfr_paged_decode_tree_workspace_size(...) bytes, 256-byte
  *              aligned; as for cfr_paged_decode.
  * Everything else (pools, page table, formats, softmax_scale, err_word) as for
- * cfr_paged_decode.  A sequence with q_lens[b] outside [0, num_queries] (taken as num_queries), or with
+ * cfr_paged_decode; max_pages * page_tokens is at most 2^31 - 1025.  A sequence with q_lens[b] outside [0, num_queries] (taken as num_queries), or with
  * n_b < q_lens[b], n_b < 1 or n_b > max_pages * page_tokens and drafts, gets out = 0 and
  * lse = -inf in its drafts' rows and sets CFR_DEVERR_SEQ_LEN.  A drafted token's non-finite
- * K or V reaches only the rows that see it.
+ * K or V reaches only the rows that see it (a non-finite scale of a quantised page may reach
+ * every row of its sequence).
  */
 cfr_status cfr_paged_decode_tree(const void *q, int32_t q_fmt, const cfr_kv_pool *kv,
                                  const int32_t *page_table, int32_t max_pages,
