@@ -419,7 +419,7 @@ cfr_status cfr_write_kv(const cfr_kv_pool *kv, const int32_t *page_table, int32_
   const int room = kWriteStage / each, vector_bytes = new_fmt == CFR_FMT_F32 ? 32 : 16;
   const int team_stage = vectors < room / vector_bytes ? vectors * vector_bytes : room;
   const auto launch = [&](auto kernel) {
-    if (each * team_stage > 48 * 1024 &&
+    if (each * team_stage > 47 * 1024 &&   // (48 KiB without, the block's fixed shared memory among them)
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWriteStage) != cudaSuccess)
       return CFR_ERR_CUDA;
     kernel<<<static_cast<unsigned>(blocks), kWriteThreads, each * team_stage, static_cast<cudaStream_t>(stream)>>>(

@@ -1047,6 +1047,7 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
   TreeItem it, next;
   TtRow row{}, next_row{};
   float ref = -INFINITY, l = 0.f;
+  float v_ref = 1.f, v_log = 0.f;      // the V scale that P and O are relative to, and its logarithm
   uint32_t item_of = 0;                // its number
   // joins the copies and writes an item's rows, or its partials
   const auto finish = [&]() {
@@ -1073,6 +1074,7 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
       f = ref_all == -INFINITY ? 1.f : exp2_approx(ref - ref_all);
     }
     if (whole) f = l_all == 0.f ? 0.f : f / l_all;
+    if (QUANT) f *= v_ref;
     if constexpr (NM == 2) {
       long long to4[4];   // the four lanes' rows, -1: none
 #pragma unroll
@@ -1338,9 +1340,19 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
       }
       // p = 2^(s - ref), its sum, and P as the MMA's operand
       float less = ref == -INFINITY ? 0.f : -ref, back = 1.f;
-      if (QUANT && one_page) {
-        less += lg2_approx(vs[0]);   // (2^-22 off, like the exponential itself)
-        back = rcp_approx(vs[0]);
+      if constexpr (QUANT) {
+        // V scales are taken relative to the newest page's.  A row's largest exponential is often 1, which bf16 holds,
+        // but not its product with a scale, and in a row that one token rules that rounding is the row's (int4
+        // pages with steep ALiBi: outputs 0.0030 off in the mean square, 0.0019 so; 0.0017 is their own rounding)
+        const float vs0 = one_page ? vs[0] : 1.f, vs0_log = lg2_approx(vs0);   // (2^-22 off, like the exponential)
+        if (s == 0) {
+          const bool some = scaled && seen != 0ull;
+          const float newest = one_page ? vs0 : some ? vs[63 - __clzll(static_cast<long long>(seen))] : 1.f;
+          v_ref = newest >= 0x1p-20f && newest <= 0x1p20f ? newest : 1.f;
+          v_log = lg2_approx(v_ref);
+        }
+        less += vs0_log - v_log;
+        back = vs0 == v_ref ? 1.f : v_ref * rcp_approx(vs0);
       }
       if (FIXED && QUANT && finish_here) {
         less += c2;
