@@ -45,7 +45,7 @@
 //    not see the draft) and added back at the end to the rows that see it.
 //
 // What bounds it.  64 rows of a kv head over 1M bf16 tokens: HBM (654 us, the copy
-// rate).  256 rows (64 drafts, 16 ragged sequences): the softmax, one exponential a
+// rate; sustained, the power cap lowers SM clocks to 1.44 GHz and it takes 716).  256 rows (64 drafts, 16 ragged sequences): the softmax, one exponential a
 // score at 16 a clock and SM with its TMEM reads and writes around it (330 us, of 171 for
 // the bytes and 131 for the MMAs).  Quantised pages: instruction fetch and issue, since
 // the expansion, the softmax and the copies together fill the instruction cache, so hot loops are
