@@ -19,7 +19,7 @@
 // eight values.
 //
 // Floor of both: HBM, dense rows once and stored rows once.  The write comes to 3.1 TB/s (34K bf16 tokens of 8
-// heads of 128 into int4 pages: 52 us): about ten instructions a value take half the
+// heads of 128 into int4 pages: 52 us): about twelve instructions a value take half the
 // issue slots, and a page's two passes leave gaps that three blocks an SM do not
 // close.  Read-back runs at the copy rate (8 x 32K tokens of tiers to bf16: 176 us, 6.1 TB/s).
 #include <type_traits>
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kWriteThreads, 3) write_kernel(const __grid_co
   const int kept = tin > 0 && scale != old ? tin << vshift : 0;
   const auto store = [&](auto dst) {
     constexpr int DST = decltype(dst)::value;
-    store_kept<DST>(page, tid, T, kept, old, scale, r, fast);
+    store_kept<DST>(page, tid, T, kept, old, scale, r, fast && fabsf(old) <= scale);   // (|code * old| <= Q scale but for -Q - 1)
 #pragma unroll 1
     for (int v = tid; v < nvec; v += T, src += step) {
       float x[kVec];

@@ -384,3 +384,26 @@ def test_codes_beside_the_ties(fmt, top):
     assert c.write(k, v, [0, 64], [0]) == 0
     c.expect_write(state, k, v, [0, 64], [0])
     c.same(state)
+
+
+@pytest.mark.parametrize("old", [-5.0, float("nan"), 0.0, 2.0 ** -140])
+@pytest.mark.parametrize("fmt", [I8, I4, FP8])
+def test_kept_rows_under_scales_that_no_write_leaves(fmt, old):
+    c = Cache(1, 2, 64, 16, 1, [fmt], seed=27)
+    c.scales[fmt].fill_(old)
+    state = c.host()
+    k, v = chunk(4, 2, 64, torch.bfloat16, 28)
+    assert c.write(k, v, [0, 4], [9]) == 0
+    with np.errstate(all="ignore"):
+        for w, rows in enumerate((k, v)):       # max(old, max|x| / Q), where a NaN is left out
+            for g in range(2):
+                x = rows[:, g].float().cpu().numpy()
+                scale = np.float32(np.abs(x).max()) / np.float32(QMAX[fmt])
+                page = state[w][fmt][int(c.table[0, 0]), g]
+                page[:9] = encode(decode_rows(page[:9].copy(), fmt, 64).astype(np.float32) * np.float32(old), fmt, scale)
+                page[9:13] = encode(x, fmt, scale)
+                state[2][fmt][int(c.table[0, 0]), g, w] = scale
+    # (slots that hold no page keep `old`, a NaN among them)
+    for w, pool in enumerate((c.k, c.v)):
+        assert np.array_equal(pool[fmt].cpu().numpy(), state[w][fmt])
+    assert np.array_equal(c.scales[fmt].cpu().numpy(), state[2][fmt], equal_nan=True)
