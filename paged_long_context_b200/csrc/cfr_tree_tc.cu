@@ -129,10 +129,10 @@ struct TtSmem {
   // by row tile and, where two steps can be under way, by the step's parity: a wait by
   // parity must begin no earlier than one phase before the one it is for
   uint64_t s_full[2 * NM], p_full[2 * NM], pv_done[2 * NM], q_full[NM], o_free[NM];
-  uint64_t meta_full[META_RING], drain[NM], meet, item_full[ITEM_RING];
+  uint64_t meta_full[META_RING], drain[NM], meet, item_full[ITEM_RING], item_free[ITEM_RING];
   uint32_t tmem_base;
   int flag[NS], expand_go[2][2];
-  unsigned long long nonfinite[META_RING];  // of item k & 7: drafts whose V was repaired
+  unsigned long long nonfinite[ITEM_RING];  // of item k & 7: drafts whose V was repaired
   int direct[NS];                           // the slot's tile needs no expansion or repair
   TreeItem item[ITEM_RING];
   typename std::conditional<QUANT, TtMeta, TtNoMeta>::type meta[QUANT ? META_RING : 1];
@@ -268,9 +268,11 @@ __device__ __forceinline__ bool tt_wait(uint64_t *bar, uint32_t parity, uint32_t
 }
 
 // Item k of the CTA, published in place k & 7 by the producer of K as item k - 1 begins (walking the cut takes
-// a few microseconds, which every role would spend between items); false past the last.  A place is
-// used again 8 items later, when its readers are through: the producer is ahead of the others by its
-// slots and two steps, fewer than 8 tiles, and an item has at least one.
+// a few microseconds, which every role would spend between items); false past the last.  A place, and the
+// notes of the item's repaired drafts in `nonfinite`, are used again 8 items later.  Roles that hold or
+// hand on K/V slots are through by then: the producer is ahead of them by its slots and two
+// steps, fewer than 8 tiles, and an item has at least one.  A softmax warpgroup holds none where its row tile has no
+// rows, so those say themselves when they are through, by item_free.
 template <typename Smem>
 __device__ __forceinline__ bool tt_item(const TreeParams &p, Smem &S, uint32_t k, TreeItem &it, bool *timed_out) {
   const int i = k & (ITEM_RING - 1);
@@ -375,11 +377,19 @@ __device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor &cur, bool *timed
   // (the producer of K) the CTA's next item to the other roles
   uint32_t published = 0;
   const auto publish = [&]() {
+    const int i = published & (ITEM_RING - 1);
+    if (published >= ITEM_RING) {
+      tt_wait(&c.S.item_free[i], (published / ITEM_RING - 1) & 1u, p.err, timed_out);
+      if (__any_sync(0xffffffffu, *timed_out)) {
+        *timed_out = true;
+        return;
+      }
+    }
     if (lane == 0) {
       TreeItem x;
       if (!tree_next<TT, Cfg::RB>(p, cur, x)) x.rows = 0;
-      c.S.item[published & (ITEM_RING - 1)] = x;
-      mbar_arrive(&c.S.item_full[published & (ITEM_RING - 1)]);
+      c.S.item[i] = x;
+      mbar_arrive(&c.S.item_full[i]);
     }
     ++published;
   };
@@ -389,7 +399,7 @@ __device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor &cur, bool *timed
     const bool some = tt_item(p, c.S, k, item, timed_out);
     if (!__all_sync(0xffffffffu, some)) break;
     const TreeItem it = item;
-    if (!QUANT && KV == 1 && lane == 0) c.S.nonfinite[k & (META_RING - 1)] = 0ull;
+    if (!QUANT && KV == 1 && lane == 0) c.S.nonfinite[k & (ITEM_RING - 1)] = 0ull;
     if (KV == 0 && lane == 0 && it.bad) set_err(p.err, CFR_DEVERR_SEQ_LEN);
     pre = it.n - it.c;
     const long long table = static_cast<long long>(it.b) * p.max_pages;
@@ -532,7 +542,7 @@ __device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor &cur, bool *timed
         pend_slot = slot_i;
         pend_j0 = j0;
         pend_mi = mi;
-        pend_item = k & (META_RING - 1);
+        pend_item = k & (ITEM_RING - 1);
       }
       if (KV == 0 && t == it.t1 - 1) publish();   // the item after this one, once this one is under way
       if (++slot_i == r_end) {
@@ -633,7 +643,7 @@ __device__ void tt_expand(TtCtx<D, NM, true> &c, bool *timed_out, const int whic
     TreeItem it;
     if (!tt_item(p, c.S, k, it, timed_out)) return;
     const int pre = it.n - it.c;
-    if (i == 0 && which) c.S.nonfinite[k & (META_RING - 1)] = 0ull;
+    if (i == 0 && which) c.S.nonfinite[k & (ITEM_RING - 1)] = 0ull;
     for (int t = it.t1 - 1; t >= it.t0; --t, ++tile) {
       const int mi = tile & (META_RING - 1);
       const TtMeta &m = c.S.meta[mi];
@@ -714,7 +724,7 @@ __device__ void tt_expand(TtCtx<D, NM, true> &c, bool *timed_out, const int whic
           }
           // a V row without a token, or of a draft (int8 and int4 codes are finite)
           if (kv == 1 && (eight || four ? fmt == CFR_FMT_FP8 && draft >= 0 : !valid || draft >= 0))
-            tt_repair_row<D>(op, i, valid, draft, &c.S.nonfinite[k & (META_RING - 1)]);
+            tt_repair_row<D>(op, i, valid, draft, &c.S.nonfinite[k & (ITEM_RING - 1)]);
           fence_async_smem();
         }
         named_sync(bar, 128);
@@ -1037,6 +1047,11 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
     mbar_arrive(&c.S.meet);
     return wait(&c.S.meet, met++ & 1u);
   };
+  // this warp is through with the place of item k, and with its notes
+  const auto leave = [&](uint32_t k) {
+    __syncwarp();
+    if ((r & 31) == 0) mbar_arrive(&c.S.item_free[k & (ITEM_RING - 1)]);
+  };
   // reads the next item: 0 if there is none, 1 if it has rows for this row tile, 2 if not
   const auto peek = [&](TreeItem &x) {
     const bool some = tt_item(p, c.S, next_k, x, timed_out);
@@ -1053,7 +1068,8 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
   const auto finish = [&]() {
     if (!wait(&c.S.pv_done[2 * m + ((cnt - 1) & 1)], ((cnt - 1) >> 1) & 1u)) return false;
     tc_fence_after();
-    const unsigned long long noted = c.S.nonfinite[item_of & (META_RING - 1)] & row.bits;
+    const unsigned long long noted = c.S.nonfinite[item_of & (ITEM_RING - 1)] & row.bits;
+    leave(item_of);
     if (__any_sync(0xffffffffu, noted != 0ull)) tt_add_back<D>(p, it, row.copy == 0 ? noted : 0ull, o_at);
     const bool whole = it.whole();
     const long long slot = (2LL * blockIdx.x + (it.t0 > 0 ? 0 : 1)) * Cfg::RB + row.row;
@@ -1140,6 +1156,7 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
   for (;;) {
     if (look == 2) {
       do {
+        if (next_k > 0) leave(next_k - 1);
         tile += next.t1 - next.t0;
         look = peek(next);
       } while (look == 2);
@@ -1441,7 +1458,10 @@ __global__ void __launch_bounds__((TtCfg<D, NM, QUANT>::THREADS), 1)
       mbar_init(&S.drain[i], 1);
     }
     for (int i = 0; i < META_RING; ++i) mbar_init(&S.meta_full[i], 1);
-    for (int i = 0; i < ITEM_RING; ++i) mbar_init(&S.item_full[i], 1);
+    for (int i = 0; i < ITEM_RING; ++i) {
+      mbar_init(&S.item_full[i], 1);
+      mbar_init(&S.item_free[i], 4 * NM);   // the softmax warps
+    }
     mbar_init(&S.meet, 128);
     fence_mbar_init();
   }

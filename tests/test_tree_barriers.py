@@ -1,0 +1,365 @@
+"""A model of the barriers of the tcgen05 tree-attention kernel (csrc/cfr_tree_tc.cu), run on the
+CPU under random schedules and with each role slowed in turn.
+
+Every role of a CTA (producers of K and V, MMA issuers, softmax warpgroups, expanding
+warpgroups) is a coroutine that takes its waits and arrivals in the kernel's order; copies and
+MMAs complete behind them in their own time.  A wait by parity has to begin at most one phase
+away from the one it is for, and whatever a role reads has to be what the tile, the step or the
+item in its hands put there: both are asserted at every step.
+"""
+import random
+
+import pytest
+
+ITEM_RING = 8
+META_RING = 8
+# row tiles, quantised pages, K slots, V slots: the kernel's variants for heads of 128 and of 64
+VARIANTS = {"narrow-128": (1, False, 2, 3), "wide-128": (2, False, 2, 3), "narrow-64": (1, False, 4, 6),
+            "wide-64": (2, False, 4, 6), "narrow-quant-128": (1, True, 2, 3), "wide-quant-128": (2, True, 2, 2),
+            "narrow-quant-64": (1, True, 4, 6), "wide-quant-64": (2, True, 4, 4)}
+
+
+class Broken(Exception):
+    """A phase was lost, something was overwritten under its reader, or nobody can go on."""
+
+
+def need(ok, *what):
+    if not ok:
+        raise Broken(what)
+
+
+class Bar:
+    """An mbarrier: arrivals and bytes that its phase still waits for."""
+
+    def __init__(self, name, count):
+        self.name, self.count, self.pending, self.tx, self.phase = name, count, count, 0, 0
+
+    def arrive(self, tx=0):
+        self.tx += tx
+        self.pending -= 1
+        need(self.pending >= 0, "too many arrivals", self.name)
+        self._turn()
+
+    def complete(self, tx):
+        self.tx -= tx
+        self._turn()
+
+    def _turn(self):
+        if self.pending == 0 and self.tx == 0:
+            self.phase += 1
+            self.pending = self.count
+
+    def wait(self, n):
+        """For the end of phase n, by its parity."""
+        need(self.phase >= n, "wait begins early", self.name, self.phase, n)
+        while True:
+            need(self.phase <= n + 1, "phase lost", self.name, self.phase, n)
+            if self.phase == n + 1:
+                return
+            yield
+
+
+class Model:
+    def __init__(self, variant, seed, slow=None, item_free=True):
+        self.NM, self.QUANT, self.NK, self.NV = VARIANTS[variant]
+        self.rng, self.item_free_on = random.Random(seed), item_free
+        r = self.rng
+        # (tiles, row tiles with rows) of the CTA's items
+        self.items = [(r.choice([1, 1, 1, 1, 2, 3, 7]), r.choice([1, 1, 1, 2]) if self.NM == 2 else 1)
+                      for _ in range(r.randint(1, 40))]
+        bars = lambda name, n, count: [Bar(f"{name}{i}", count) for i in range(n)]  # noqa: E731
+        NS, NM = self.NK + self.NV, self.NM
+        self.full, self.raw = bars("full", NS, 1), bars("raw", NS, 1)
+        self.empty = bars("empty", NS, NM + (1 if self.QUANT else 0))
+        self.s_full, self.p_full, self.pv = bars("s", 2 * NM, 1), bars("p", 2 * NM, 1), bars("pv", 2 * NM, 1)
+        self.q_full, self.o_free = bars("q", NM, 1), bars("o", NM, 1)
+        self.meta_full = bars("meta", META_RING, 1)
+        self.item_full, self.item_free = bars("item", ITEM_RING, 1), bars("item_free", ITEM_RING, NM)
+        self.slot, self.direct = [None] * NS, [None] * NS
+        self.meta, self.nonfinite, self.ring = [None] * META_RING, [None] * ITEM_RING, [None] * ITEM_RING
+        self.S, self.P, self.O, self.Q = [None] * (2 * NM), [None] * (2 * NM), [None] * NM, [None] * NM
+        self.published, self.raw_uses, self.hot = 0, {}, {}
+        self.mmas, self.copies, self.read, self.done = [], [], set(), set()
+        roles = {"k": self.producer(0), "v": self.producer(1)}
+        for m in range(NM):
+            roles[f"i{m}"], roles[f"s{m}"] = self.issuer(m), self.softmax(m)
+        if self.QUANT and NM == 2:
+            roles["x"] = self.expand((0, 1))
+        elif self.QUANT:
+            roles["x"], roles["y"] = self.expand((0,)), self.expand((1,))
+        self.roles = roles
+        back = {"mma": self.mma_pipe(), "copy": self.copy_engine()}
+        if slow:
+            weight = {n: 1 if n == slow else 40 for n in list(roles) + list(back)}
+        else:
+            weight = {n: r.choice([1, 1, 5, 30]) for n in roles} | {n: r.choice([1, 5, 30]) for n in back}
+        turns = 0
+        while roles:
+            names = list(roles) + list(back)
+            n = r.choices(names, [weight[x] for x in names])[0]
+            if n in back:
+                next(back[n])
+            elif next(roles[n], self) is self:   # (exhausted)
+                del roles[n]
+            turns += 1
+            need(turns < 2000000, "nobody goes on", list(roles))
+
+    def place(self, kv, t):
+        """Slot of tile t and the use of it that the tile is."""
+        return (t % self.NK, t // self.NK) if kv == 0 else (self.NK + t % self.NV, t // self.NV)
+
+    def item(self, k):
+        yield from self.item_full[k % ITEM_RING].wait(k // ITEM_RING)
+        need(self.ring[k % ITEM_RING] == k, "item overwritten", self.ring[k % ITEM_RING], k)
+        yield
+        need(self.ring[k % ITEM_RING] == k, "item overwritten", self.ring[k % ITEM_RING], k)
+
+    def publish(self):
+        n = self.published
+        if self.item_free_on and n >= ITEM_RING:
+            yield from self.item_free[n % ITEM_RING].wait(n // ITEM_RING - 1)
+        self.ring[n % ITEM_RING] = n
+        self.item_full[n % ITEM_RING].arrive()
+        self.published += 1
+
+    def producer(self, kv):
+        t, waiting = 0, None
+
+        def repair():
+            s, tile, use = waiting
+            yield from self.raw[s].wait(use)
+            yield
+            need(self.slot[s][:2] == (1, tile), "V overwritten")
+            self.slot[s] = (1, tile, True)
+            self.full[s].arrive()
+
+        for k, (tiles, _) in enumerate(self.items):
+            if kv == 0 and self.published == k:
+                yield from self.publish()
+                yield
+            yield from self.item(k)
+            if kv == 1 and not self.QUANT:
+                self.nonfinite[k % ITEM_RING] = k
+            for j in range(tiles):
+                s, use = self.place(kv, t)
+                if use > 0:
+                    yield from self.empty[s].wait(use - 1)
+                hot = self.hot.setdefault(t, self.rng.random() < 0.5)   # no quantised page in the tile
+                direct = hot or not self.QUANT
+                if kv == 1:   # (an item's first tile, the newest, holds drafts)
+                    direct = direct and j > 0 and self.rng.random() < 0.7
+                if kv == 0:
+                    self.meta[t % META_RING] = t
+                    if not self.QUANT:
+                        self.meta_full[t % META_RING].arrive()
+                self.direct[s] = direct
+                yield
+                if direct and self.QUANT:
+                    self.raw[s].arrive()
+                yield
+                bar = self.full[s] if direct else self.raw[s]
+                n = self.raw_uses.get(s, 0)
+                if not direct:
+                    self.raw_uses[s] = n + 1
+                bar.arrive(tx=1)
+                self.copies.append((bar, s, (kv, t, direct)))
+                yield
+                if kv == 0 and j == 0:
+                    yield from self.publish()
+                if kv == 1 and not self.QUANT:
+                    if waiting:
+                        yield from repair()
+                    waiting = None if direct else (s, t, n)
+                t += 1
+            if waiting:
+                yield from repair()
+                waiting = None
+
+    def expand(self, which):
+        t = 0
+        for k, (tiles, _) in enumerate(self.items):
+            yield from self.item(k)
+            if 1 in which:
+                self.nonfinite[k % ITEM_RING] = k
+            for _ in range(tiles):
+                for kv in which:
+                    s, use = self.place(kv, t)
+                    if which == (1,):
+                        yield from self.meta_full[t % META_RING].wait(t // META_RING)
+                    yield from self.raw[s].wait(use)
+                    direct = self.direct[s]
+                    need(self.meta[t % META_RING] == t, "description overwritten")
+                    yield
+                    need(self.meta[t % META_RING] == t, "description overwritten")
+                    if not direct:
+                        need(self.slot[s][:2] == (kv, t), "slot overwritten")
+                        self.slot[s] = (kv, t, True)
+                        self.full[s].arrive()
+                    if kv == 0:
+                        self.meta_full[t % META_RING].arrive()
+                    yield
+                    self.empty[s].arrive()
+                t += 1
+
+    def issuer(self, m):
+        t = kt = steps_done = items_done = 0
+        H = self.NM   # steps of a tile
+        for k, (tiles, row_tiles) in enumerate(self.items):
+            yield from self.item(k)
+            if m >= row_tiles:
+                for _ in range(tiles):
+                    for kv in (0, 1):
+                        s, use = self.place(kv, t)
+                        yield from self.full[s].wait(use)
+                        self.empty[s].arrive()
+                    t, kt = t + 1, kt + 1
+                continue
+            yield from self.q_full[m].wait(items_done)
+            for step in range(-1, tiles * H):
+                if step + 1 < tiles * H:
+                    s, use = self.place(0, kt)
+                    if (step + 1) % H == 0:
+                        yield from self.full[s].wait(use)
+                    n = steps_done + (step >= 0)
+
+                    def scores(s=s, kt=kt, n=n, k=k):
+                        need(self.slot[s] == (0, kt, True) and self.Q[m] == k, "K or Q overwritten")
+                        need(n < 2 or (m, n - 2) in self.read, "scores overwritten")
+                        self.S[2 * m + (n & 1)] = n
+                        if self.NM == 2:
+                            self.P[2 * m + (n & 1)] = None
+                    self.mmas += [scores, self.s_full[2 * m + (n & 1)].arrive]
+                    if (step + 1) % H == H - 1:
+                        self.mmas.append(self.empty[s].arrive)
+                        kt += 1
+                if step < 0:
+                    continue
+                s, use = self.place(1, t)
+                b = 2 * m + (steps_done & 1)
+                if step % H == 0:
+                    yield from self.full[s].wait(use)
+                if step == 0 and items_done > 0:
+                    yield from self.o_free[m].wait(items_done - 1)
+                yield from self.p_full[b].wait(steps_done >> 1)
+
+                def product(b=b, n=steps_done, s=s, t=t, step=step, k=k):
+                    need(self.slot[s] == (1, t, True) and self.P[b] == n, "V or P overwritten")
+                    need(step > 0 or self.O[m] in (None, "free"), "O overwritten")
+                    self.O[m] = (k, step)
+                    self.done.add((m, n))
+                self.mmas += [product, self.pv[b].arrive]
+                steps_done += 1
+                yield
+                if step % H == H - 1:
+                    self.mmas.append(self.empty[s].arrive)
+                    t += 1
+            items_done += 1
+
+    def softmax(self, m):
+        H, cnt, tile, next_k = self.NM, 0, 0, 0
+        state = {}
+
+        def peek():   # reads the next item: None at the end, else whether it has rows here
+            nonlocal next_k
+            yield from self.item(next_k)
+            state["item"] = next_k
+            if next_k == len(self.items):
+                state["look"] = None
+                return
+            state["look"] = m < self.items[next_k][1]
+            next_k += 1
+
+        state["look"] = False
+        skipped = 0   # tiles of the item that was looked at and has no rows here
+        while True:
+            if state["look"] is False:
+                while state["look"] is False:
+                    if next_k > 0:
+                        self.item_free[(next_k - 1) % ITEM_RING].arrive()
+                    tile += skipped
+                    yield from peek()
+                    skipped = self.items[state["item"]][0] if state["look"] is False else 0
+                if state["look"]:
+                    self.Q[m] = state["item"]
+                    yield
+                    self.q_full[m].arrive()
+            if state["look"] is None:
+                return
+            k = state["item"]
+            steps = self.items[k][0] * H
+            yield from peek()
+            skipped = self.items[state["item"]][0] if state["look"] is False else 0
+            for step in range(steps):
+                b = 2 * m + (cnt & 1)
+                yield from self.s_full[b].wait(cnt >> 1)
+                if step % H == 0:
+                    yield from self.meta_full[tile % META_RING].wait(tile // META_RING)
+                if state["look"] and step == steps - 1:
+                    self.Q[m] = state["item"]
+                need(self.S[b] == cnt and self.meta[tile % META_RING] == tile, "scores or description overwritten")
+                yield
+                need(self.S[b] == cnt and self.meta[tile % META_RING] == tile, "scores or description overwritten")
+                self.read.add((m, cnt))
+                if step > 0 and self.rng.random() < 0.5:   # the reference moves
+                    yield from self.pv[2 * m + ((cnt - 1) & 1)].wait((cnt - 1) >> 1)
+                    need(self.O[m] == (k, step - 1), "O under way")
+                    yield
+                    need(self.O[m] == (k, step - 1), "O under way")
+                need(cnt < 2 or (m, cnt - 2) in self.done, "P overwritten")
+                self.P[b] = cnt
+                self.p_full[b].arrive()
+                cnt += 1
+                if step % H == H - 1:
+                    tile += 1
+            if state["look"]:
+                yield
+                self.q_full[m].arrive()
+            yield from self.pv[2 * m + ((cnt - 1) & 1)].wait((cnt - 1) >> 1)
+            yield
+            need(self.nonfinite[k % ITEM_RING] == k, "notes of repaired drafts overwritten", self.nonfinite[k % ITEM_RING], k)
+            self.item_free[k % ITEM_RING].arrive()
+            yield
+            need(self.O[m] == (k, steps - 1), "O overwritten")
+            self.O[m] = "free"
+            self.o_free[m].arrive()
+            yield
+
+    def mma_pipe(self):
+        while True:
+            if self.mmas:
+                self.mmas.pop(0)()
+            yield
+
+    def copy_engine(self):
+        while True:
+            if self.copies:
+                bar, s, what = self.copies.pop(self.rng.randrange(len(self.copies)))
+                self.slot[s] = what
+                bar.complete(1)
+            yield
+
+
+def roles_of(variant):
+    NM, QUANT = VARIANTS[variant][:2]
+    return ["k", "v"] + [f"{w}{m}" for m in range(NM) for w in "is"] + (["x", "y"][:3 - NM] if QUANT else [])
+
+
+@pytest.mark.parametrize("variant", list(VARIANTS))
+def test_random_schedules(variant):
+    for seed in range(12):
+        Model(variant, seed)
+
+
+@pytest.mark.parametrize("variant,slow", [(v, r) for v in VARIANTS for r in roles_of(v) if r[0] != "y"])
+def test_a_slow_role_loses_nothing(variant, slow):
+    for seed in range(8):
+        Model(variant, seed, slow)
+
+
+@pytest.mark.parametrize("variant", [v for v in VARIANTS if "wide" in v])
+def test_items_need_a_barrier_for_their_places(variant):
+    # without it nothing holds the producer back for the second softmax warpgroup of the wide variants, whose
+    # issuer passes over the slots of items that have no rows there
+    with pytest.raises(Broken, match="overwritten|lost"):
+        for seed in range(40):
+            Model(variant, seed, "s1", item_free=False)
