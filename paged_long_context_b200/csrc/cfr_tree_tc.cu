@@ -67,7 +67,6 @@ namespace cfr {
 namespace {
 
 constexpr int TT = 128;        // tokens of a tile
-constexpr int META_RING = 8;   // tiles whose description is kept (see tt_producer)
 constexpr int ITEM_RING = 8;   // items published
 constexpr int MAX_PIECES = 17; // pages (of 8 tokens or more) that a tile can touch
 constexpr float RESCALE_STEP = 8.f;
@@ -93,6 +92,9 @@ struct TtCfg {
   static constexpr int NS = NK + NV;
   // expanding warpgroups: K and V in turn by one where registers allow no more, else one for each
   static constexpr int LOADERS = QUANT ? (NM == 1 ? 2 : 1) : 0;
+  // tiles whose description is kept, a power of two (see tt_producer)
+  static constexpr int META = LOADERS == 2 && NK + NV + 1 >= 8 ? 16 : 8;
+  static_assert(NK <= 4 && (LOADERS < 2 || NK + NV + 1 < META), "a tile's description outlives its readers");
   static constexpr int WGS = 1 + NM + LOADERS;
   static constexpr int THREADS = 128 * WGS;
   static constexpr int SOFTMAX_T0 = 128;
@@ -123,26 +125,26 @@ struct TtNoMeta {
   int tin0, scaled;
 };
 
-template <int NS, int NM, bool QUANT>
+template <int NS, int NM, bool QUANT, int META>
 struct TtSmem {
   uint64_t slot_full[NS], slot_empty[NS], raw_full[NS];
   // by row tile and, where two steps can be under way, by the step's parity: a wait by
   // parity must begin no earlier than one phase before the one it is for
   uint64_t s_full[2 * NM], p_full[2 * NM], pv_done[2 * NM], q_full[NM], o_free[NM];
-  uint64_t meta_full[META_RING], drain[NM], meet, item_full[ITEM_RING], item_free[ITEM_RING];
+  uint64_t meta_full[META], drain[NM], meet, item_full[ITEM_RING], item_free[ITEM_RING];
   uint32_t tmem_base;
   int flag[NS], expand_go[2][2];
   unsigned long long nonfinite[ITEM_RING];  // of item k & 7: drafts whose V was repaired
   int direct[NS];                           // the slot's tile needs no expansion or repair
   TreeItem item[ITEM_RING];
-  typename std::conditional<QUANT, TtMeta, TtNoMeta>::type meta[QUANT ? META_RING : 1];
-  uint32_t valid[META_RING][4], v_valid[META_RING][4];
+  typename std::conditional<QUANT, TtMeta, TtNoMeta>::type meta[QUANT ? META : 1];
+  uint32_t valid[META][4], v_valid[META][4];
   union {
     TtPages pages[2];
     TreeScratch scratch;   // (before the roles begin)
   };
   // K scale (times softmax scale and log2 e) and V scale of each token
-  alignas(16) float ks[QUANT ? META_RING : 1][QUANT ? TT : 4], vs[QUANT ? META_RING : 1][QUANT ? TT : 4];
+  alignas(16) float ks[QUANT ? META : 1][QUANT ? TT : 4], vs[QUANT ? META : 1][QUANT ? TT : 4];
   // joining of the copies (narrow): 32 columns of O of every row, its maximum and sum
   alignas(16) float join[NM == 1 ? 128 : 1][36];
   float2 join_ml[NM == 1 ? 128 : 1];
@@ -245,7 +247,7 @@ __device__ __forceinline__ uint32_t repair_pair(uint32_t w) {
 template <int D, int NM, bool QUANT>
 struct TtCtx {
   using Cfg = TtCfg<D, NM, QUANT>;
-  using Smem = TtSmem<Cfg::NS, NM, QUANT>;
+  using Smem = TtSmem<Cfg::NS, NM, QUANT, Cfg::META>;
   const TreeParams &p;
   const CUtensorMap &kmap, &vmap;
   Smem &S;
@@ -329,10 +331,13 @@ __device__ __noinline__ void tt_repair_row(uint8_t *v, int i, bool valid, int dr
 // Tiles go from the newest to the oldest: with ALiBi, or any attention that favours the
 // recent, the running maximum is then found at once and O is hardly ever rescaled.
 //
-// The description of the CTA's tile t is kept in place t & 7.  It may be overwritten by
+// The description of the CTA's tile t is kept in place t mod META.  It may be overwritten by
 // tile t + 8 because K's slot of tile t + 8 is free only when the scores of a
 // tile t + 4 or later were issued (there are at most 4 slots of K), which is after the softmax of
-// tile t handed over its P.
+// tile t handed over its P.  A warpgroup that expands V alone reads it too, and only the slots of V hold the
+// others back for it: with tile t in its hands (and tiles of bf16 pages, which need no expansion, behind it), V is
+// there up to tile t + NV - 1, scores are issued up to tile t + NV + 1 and K comes up to tile
+// t + NK + NV + 1.  Heads of 64 have 6 slots of V there and keep 16 descriptions for it.
 template <int D, int NM, bool QUANT>
 __device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor &cur, bool *timed_out, const int KV) {
   using Cfg = TtCfg<D, NM, QUANT>;
@@ -475,7 +480,7 @@ __device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor &cur, bool *timed
           if (lane == w) valid = any;
         }
       }
-      const int mi = tile & (META_RING - 1);
+      const int mi = tile & (Cfg::META - 1);
       const bool direct = !any_quant && (KV == 0 || (full && j0 + TT <= pre));
       tt_wait(&c.S.slot_empty[slot_i], slot_ph ^ 1u, p.err, timed_out);
       if (__any_sync(0xffffffffu, *timed_out)) {
@@ -645,7 +650,7 @@ __device__ void tt_expand(TtCtx<D, NM, true> &c, bool *timed_out, const int whic
     const int pre = it.n - it.c;
     if (i == 0 && which) c.S.nonfinite[k & (ITEM_RING - 1)] = 0ull;
     for (int t = it.t1 - 1; t >= it.t0; --t, ++tile) {
-      const int mi = tile & (META_RING - 1);
+      const int mi = tile & (Cfg::META - 1);
       const TtMeta &m = c.S.meta[mi];
 #pragma unroll 1
       for (int kv = which == 1 ? 1 : 0; kv < (which == 0 ? 1 : 2); ++kv) {
@@ -653,7 +658,7 @@ __device__ void tt_expand(TtCtx<D, NM, true> &c, bool *timed_out, const int whic
         const uint32_t ph = kv ? vr.ph : kr.ph;
         if (i == 0) {
           // (the description of the tile is K's; the warpgroup of V has it by meta_full)
-          bool got = which != 1 || tt_wait(&c.S.meta_full[mi], (tile / META_RING) & 1u, p.err, timed_out);
+          bool got = which != 1 || tt_wait(&c.S.meta_full[mi], (tile / Cfg::META) & 1u, p.err, timed_out);
           got = got && tt_wait(&c.S.raw_full[slot], ph, p.err, timed_out);
           c.S.flag[slot] = got ? 1 : 0;
         }
@@ -663,7 +668,7 @@ __device__ void tt_expand(TtCtx<D, NM, true> &c, bool *timed_out, const int whic
           return;
         }
         (void)mbar_try_wait(&c.S.raw_full[slot], ph);
-        if (which == 1) (void)mbar_try_wait(&c.S.meta_full[mi], (tile / META_RING) & 1u);
+        if (which == 1) (void)mbar_try_wait(&c.S.meta_full[mi], (tile / Cfg::META) & 1u);
         const bool direct = c.S.direct[slot];
         const bool any4 = m.scaled & 2;   // 4-bit rows among the tile's
         const bool valid = (c.S.valid[mi][i >> 5] >> (i & 31)) & 1u;
@@ -1193,12 +1198,12 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
     const int steps = (it.t1 - it.t0) * Cfg::STEPS;
     for (int s = 0; s < steps; ++s, ++cnt) {
       const int b = cnt & 1, h = s % Cfg::STEPS;
-      const int mi = tile & (META_RING - 1);
-      // (scores first: they say that the tile 8 before this one was described, whatever tiles this
+      const int mi = tile & (Cfg::META - 1);
+      // (scores first: they say that the tile META before this one was described, whatever tiles this
       // warpgroup passed over)
       if (!wait(&c.S.s_full[2 * m + b], (cnt >> 1) & 1u)) return;
       if (look == 1 && s + 1 == steps) tt_load_q<D, NM, QUANT>(c, m, r, next_row);
-      if (h == 0 && !wait(&c.S.meta_full[mi], (tile / META_RING) & 1u)) return;
+      if (h == 0 && !wait(&c.S.meta_full[mi], (tile / Cfg::META) & 1u)) return;
       tc_fence_after();
       if (idle) {   // a warp without rows: what it leaves in P reaches no other row
         tc_fence_before();
@@ -1420,7 +1425,7 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
 
 template <int D, int NM, bool QUANT>
 constexpr size_t tt_head() {
-  return (sizeof(TtSmem<TtCfg<D, NM, QUANT>::NS, NM, QUANT>) + 1023) / 1024 * 1024;
+  return (sizeof(typename TtCtx<D, NM, QUANT>::Smem) + 1023) / 1024 * 1024;
 }
 template <int D, int NM, bool QUANT>
 constexpr size_t tt_smem() {
@@ -1433,7 +1438,7 @@ __global__ void __launch_bounds__((TtCfg<D, NM, QUANT>::THREADS), 1)
     tree_tc_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap) {
   using Cfg = TtCfg<D, NM, QUANT>;
-  using Smem = TtSmem<Cfg::NS, NM, QUANT>;
+  using Smem = TtSmem<Cfg::NS, NM, QUANT, Cfg::META>;
   static_assert(tt_smem<D, NM, QUANT>() <= 227 * 1024, "shared memory of a block");
   extern __shared__ uint8_t raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) / 1024 * 1024);
@@ -1457,7 +1462,7 @@ __global__ void __launch_bounds__((TtCfg<D, NM, QUANT>::THREADS), 1)
       mbar_init(&S.o_free[i], 128);
       mbar_init(&S.drain[i], 1);
     }
-    for (int i = 0; i < META_RING; ++i) mbar_init(&S.meta_full[i], 1);
+    for (int i = 0; i < Cfg::META; ++i) mbar_init(&S.meta_full[i], 1);
     for (int i = 0; i < ITEM_RING; ++i) {
       mbar_init(&S.item_full[i], 1);
       mbar_init(&S.item_free[i], 4 * NM);   // the softmax warps
