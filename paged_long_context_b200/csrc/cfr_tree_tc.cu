@@ -404,7 +404,8 @@ __device__ void tt_producer(TtCtx<D, NM, QUANT> &c, TreeCursor &cur, bool *timed
     const bool some = tt_item(p, c.S, k, item, timed_out);
     if (!__all_sync(0xffffffffu, some)) break;
     const TreeItem it = item;
-    if (!QUANT && KV == 1 && lane == 0) c.S.nonfinite[k & (ITEM_RING - 1)] = 0ull;
+    // (here and not by the warps that expand V: tiles that need no expansion do not wait for those)
+    if (KV == 1 && lane == 0) c.S.nonfinite[k & (ITEM_RING - 1)] = 0ull;
     if (KV == 0 && lane == 0 && it.bad) set_err(p.err, CFR_DEVERR_SEQ_LEN);
     pre = it.n - it.c;
     const long long table = static_cast<long long>(it.b) * p.max_pages;
@@ -648,7 +649,6 @@ __device__ void tt_expand(TtCtx<D, NM, true> &c, bool *timed_out, const int whic
     TreeItem it;
     if (!tt_item(p, c.S, k, it, timed_out)) return;
     const int pre = it.n - it.c;
-    if (i == 0 && which) c.S.nonfinite[k & (ITEM_RING - 1)] = 0ull;
     for (int t = it.t1 - 1; t >= it.t0; --t, ++tile) {
       const int mi = tile & (Cfg::META - 1);
       const TtMeta &m = c.S.meta[mi];

@@ -51,8 +51,10 @@ def check_all(call, out, lse, skip=()):
                 assert (np.abs(out[:, b, i, h] - o) <= to).all() and (np.abs(lse[:, b, i, h] - l) <= tl).all(), (b, i, h)
 
 
+TIERS = [(0.5, "i8"), (0.5, "bf16")]
 # heads of 64 and of 128, each format; four query heads of a kv head: 64 drafts are 256 rows, 32 are 128, 33 are 132
-FORMS = {"bf16-p16": dict(), "bf16-p16-d64": dict(d=64), "i8-p16": dict(fmt="i8"), "fp8-p64-d64": dict(fmt="fp8", P=64, d=64)}
+FORMS = {"bf16-p16": dict(), "bf16-p16-d64": dict(d=64), "i8-p16": dict(fmt="i8"), "fp8-p64-d64": dict(fmt="fp8", P=64, d=64),
+         "tiered-p16": dict(fmt="tiered", tiers=TIERS), "tiered-p16-d64": dict(fmt="tiered", tiers=TIERS, d=64)}
 
 
 @pytest.mark.parametrize("copies", [40, 300])
@@ -72,7 +74,7 @@ def test_small_trees_only(name):
     check_all(call, *repeated(call, 600))
 
 
-@pytest.mark.parametrize("name", ["bf16-p16", "bf16-p16-d64", "fp8-p64-d64"])
+@pytest.mark.parametrize("name", ["bf16-p16", "bf16-p16-d64", "fp8-p64-d64", "tiered-p16"])
 def test_values_added_back_beside_many_small_trees(name):
     # drafts whose V is not finite, seen by rows of the second row tile only, then small trees
     lens, q_lens = (70, 5, 9, 33, 12, 20, 7, 30, 6, 8, 10, 40), [64] + [3, 5, 1, 7, 4, 2, 8, 3, 4, 5, 6]
@@ -82,6 +84,9 @@ def test_values_added_back_beside_many_small_trees(name):
     first = 48
     for i in range(first, 64):
         j = lens[0] - 64 + i
+        if case.page_fmt is not None:
+            f = int(case.page_fmt[0, j // P])
+            assert f == synth.BF16
         slot = int(case.page_table[0, j // P])
         if f == synth.FP8:
             case.v_pool[f][slot, :, j % P, i] = 0x7F
@@ -92,3 +97,21 @@ def test_values_added_back_beside_many_small_trees(name):
     for i in range(first, 64):   # element e is NaN in the rows from draft e on
         got = torch.isnan(out[:, 0, i])
         assert got[..., first:i + 1].all() and not got[..., :first].any() and not got[..., i + 1:].any()
+
+
+@pytest.mark.parametrize("Q", [3, 40], ids=["12rows", "160rows"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_stretches_of_bf16_tiles_in_a_tiered_cache(d, Q):
+    # most tiles need no expansion, and most stretches of a long sequence hold nothing else; the newest pages are coded
+    case = tree_case((20000, 9001, 130), Q, Hq=4, Hkv=1, d=d, P=16, fmt="tiered", tiers=[(0.9, "bf16"), (0.1, "fp8")])
+    call = TreeCall(case, q_lens=[Q, Q - 1, Q])
+    P = case.page_tokens
+    j = 20000 - 2
+    f, slot = int(case.page_fmt[0, j // P]), int(case.page_table[0, j // P])
+    assert f == synth.FP8
+    case.v_pool[f][slot, :, j % P, 5] = 0x7F
+    assert call.run() == 0
+    call.check(skip={(0, i, h) for i in (Q - 2, Q - 1) for h in range(4)})
+    got = torch.isnan(call.out[0, Q - 2:])
+    assert got[..., 5].all() and not got[..., :5].any() and not got[..., 6:].any()
+    assert int(call.err.item()) == 0
