@@ -1470,7 +1470,7 @@ __global__ void __launch_bounds__((TtCfg<D, NM, QUANT>::THREADS), 1)
     mbar_init(&S.meet, 128);
     fence_mbar_init();
   }
-  if (threadIdx.x == 96 && p.k_pool[CFR_FMT_BF16]) {
+  if (threadIdx.x == 96 && p.pool_pages[CFR_FMT_BF16] > 0) {   // (the host encodes no map of an empty pool)
     prefetch_map(&kmap);
     prefetch_map(&vmap);
   }
