@@ -752,11 +752,11 @@ __device__ void tc_producer(TcCtx<NCOL, INTP, FEAT, IMMA> &c, bool *timed_out, i
   const int pages_per_tile = P < TC_T ? TC_T / P : 0;
   int stage = 0;
   uint32_t phase = 0;
-  if (lane == 0 && p.k_pool[CFR_FMT_BF16]) {
+  if (lane == 0 && p.pool_pages[CFR_FMT_BF16] > 0) {   // (the host encodes no map of an empty pool)
     prefetch_map(&c.maps.k);
     prefetch_map(&c.maps.v);
   }
-  if (IMMA && lane == 0 && p.k_pool[CFR_FMT_I8]) {
+  if (IMMA && lane == 0 && p.pool_pages[CFR_FMT_I8] > 0) {
     prefetch_map(&c.maps.k8);
     prefetch_map(&c.maps.v8);
   }

@@ -3,7 +3,8 @@ without it."""
 import pytest
 import torch
 
-from paged_long_context_b200 import synth
+from paged_long_context_b200 import binding, synth
+from tests._gpu import check, run
 from tests._tree import TreeCall, tree_case
 
 pytestmark = pytest.mark.gpu
@@ -44,7 +45,6 @@ def test_tree_attention(form, Q):
 
 def test_tree_attention_of_pages_in_an_empty_pool():
     # bf16 pages are named, none is there: every token is left out and reported
-    from paged_long_context_b200 import binding
     case = tree_case((50, 130), 3, fmt="bf16")
     call = TreeCall(case)
     call.pool.pool_pages[synth.BF16] = 0
@@ -52,3 +52,22 @@ def test_tree_attention_of_pages_in_an_empty_pool():
     torch.cuda.synchronize()
     assert int(call.err.item()) == binding.DEVERR_PAGE_ID
     assert (call.out == 0).all() and torch.isneginf(call.lse).all()
+
+
+@pytest.mark.parametrize("form", [dict(fmt="i8", P=64), dict(fmt="i4", P=16), dict(fmt="fp8", P=64), dict(fmt="i8", P=16, d=64)],
+                         ids=["i8", "i4", "fp8", "i8-d64"])
+def test_decode(form, monkeypatch):
+    case = tree_case((700, 41, 130), 1, **form)
+    assert binding.decode_path(case) == 2
+    plain = binding.kv_pool_struct
+
+    def with_empty_pools(c):
+        pool = plain(c)
+        add_empty_pools(pool)
+        return pool
+
+    monkeypatch.setattr(binding, "kv_pool_struct", with_empty_pools)
+    assert binding.decode_path(case) == 2
+    out, lse, err = run(case)
+    check(case, out, lse, host_case=case.to("cpu"))
+    assert err == 0
