@@ -610,7 +610,9 @@ size_t cfr_paged_decode_tree_workspace_size(int32_t batch, int32_t num_queries,
  *  depths      device int32 [batch][num_queries] or NULL: depths i (a chain); read
  *              only with alibi_slopes.
  *  head_map    host, as for cfr_paged_decode.
- *  logit_cap   0 (none) or > 0, finite.
+ *  logit_cap   0 (none) or > 0, finite.  With a cap of up to 55 and bf16 queries the magnitudes of V, and the V
+ *              scales of quantised pages, are to lie between 2^-36 and 2^28 or be 0 (smaller ones may be
+ *              lost, larger ones overflow, in rows whose scores all stand at one end of the cap).
  *  out         device [batch][num_queries][num_q_heads][head_dim], F32 or BF16 (out_fmt),
  *              16-byte aligned, written; lse device float [batch][num_queries][num_q_heads]
  *              or NULL.

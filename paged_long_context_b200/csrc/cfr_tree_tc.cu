@@ -73,11 +73,20 @@ constexpr float RESCALE_STEP = 8.f;
 
 // How scores become probabilities.  PLAIN: scaled only.  GENERAL_SCORES: capped, less a distance, or both.
 // FIXED_REFERENCE: capped scores lie within +- cap, so that the exponentials of every row can be taken against
-// one number, with no maximum and a single pass over the scores: 2^(s - 30) of |s| <= 80 (in units of log2 e,
-// caps up to 55) is between 2^-110 and 2^50, and its products and sums stay normal in bf16 and fp32.  (Eight
+// one number, with no maximum and a single pass over the scores: 2^(s - 10) of |s| <= 80 (in units of log2 e,
+// caps up to 55) is between 2^-90 and 2^70, which leaves normal numbers for V, or the V scales of quantised
+// pages, between 2^-36 and 2^28 (of 2^20 tokens that all stand at the cap).  (Eight
 // sequences of 32K tiered tokens, capped at 50: 279 us, and 360 in two passes.)
 enum TtMode { PLAIN, GENERAL_SCORES, FIXED_REFERENCE };
-constexpr float TT_FIXED_CAP = 80.f, TT_FIXED_REF = 30.f;
+constexpr float TT_FIXED_CAP = 80.f, TT_FIXED_REF = 10.f;
+
+// P and O of quantised pages are relative to one V scale, v_ref: the newest page's, or 1 where that is out of the
+// ordinary or the reference is fixed.  A page's scale goes into the exponent of its tokens, from where their sum is
+// taken back, only while its ratio to v_ref lies between FOLD_LEAST and FOLD_MOST: the smallest exponential
+// that counts, 2^-90, then stays normal and the sum whole (with wider bounds, rows whose scores stood at -cap lost
+// the pages of small V scales from their sums).  Other pages' scales multiply the probabilities token by
+// token, behind the sum.
+constexpr float TT_V_LEAST = 0x1p-20f, TT_V_MOST = 0x1p20f, TT_FOLD_LEAST = 0x1p-32f, TT_FOLD_MOST = 0x1p16f;
 
 template <int D, int NM, bool QUANT>
 struct TtCfg {
@@ -1220,15 +1229,22 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
       const bool scaled = QUANT && c.S.meta[QUANT ? mi : 0].scaled;
       // scales of one page serve the whole step where it lies in one; the V scale then goes into the exponent
       const float *ks = &c.S.ks[QUANT ? mi : 0][QUANT ? in_tile : 0], *vs = &c.S.vs[QUANT ? mi : 0][QUANT ? in_tile : 0];
-      const bool one_page = QUANT && scaled && in_one && ks[0] > 0.f && ks[0] < 1e30f && vs[0] > 1e-30f && vs[0] < 1e30f;
+      if (masked)   // tokens before the drafts, and the drafts of the row's bits
+        seen &= off >= 64 ? ~0ull : off > 0 ? (row.bits << off) | ((1ull << off) - 1ull) : off > -64 ? row.bits >> -off : 0ull;
+      if (QUANT && !FIXED && s == 0) {
+        const float newest = !scaled ? 1.f : in_one ? vs[0] : seen ? vs[63 - __clzll(static_cast<long long>(seen))] : 1.f;
+        v_ref = newest >= TT_V_LEAST && newest <= TT_V_MOST ? newest : 1.f;
+        v_log = lg2_approx(v_ref);
+      }
+      // (the same for the whole warp: TMEM instructions depend on it)
+      const bool one_page = QUANT && scaled && in_one && ks[0] > 0.f && ks[0] < 1e30f &&
+                            __all_sync(0xffffffffu, vs[0] >= v_ref * TT_FOLD_LEAST && vs[0] <= v_ref * TT_FOLD_MOST);
       // Scores as they enter the exponential, in units of log2 e: times the softmax scale
       // (left to the exponential where nothing else is to be done), the pages' scales,
       // capped, less the distance, -inf where the row does not see the token.  Steps with
       // unseen tokens, one or two of an item, are finished out of line.
       float sc = one_page ? ks[0] : scale;
       if (masked) {
-        // tokens before the drafts, and the drafts of the row's bits
-        seen &= off >= 64 ? ~0ull : off > 0 ? (row.bits << off) | ((1ull << off) - 1ull) : off > -64 ? row.bits >> -off : 0ull;
         tt_masked<GENERAL>(p, s_at, row.width, seen, scaled ? ks : nullptr, scale, row.slope, row.pos, pre, off, it.c, it.b);
         sc = 1.f;
       }
@@ -1367,12 +1383,6 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
         // but not its product with a scale, and in a row that one token rules that rounding is the row's (int4
         // pages with steep ALiBi: outputs 0.0030 off in the mean square, 0.0019 so; 0.0017 is their own rounding)
         const float vs0 = one_page ? vs[0] : 1.f, vs0_log = lg2_approx(vs0);   // (2^-22 off, like the exponential)
-        if (s == 0) {
-          const bool some = scaled && seen != 0ull;
-          const float newest = one_page ? vs0 : some ? vs[63 - __clzll(static_cast<long long>(seen))] : 1.f;
-          v_ref = newest >= 0x1p-20f && newest <= 0x1p20f ? newest : 1.f;
-          v_log = lg2_approx(v_ref);
-        }
         less += vs0_log - v_log;
         back = vs0 == v_ref ? 1.f : v_ref * rcp_approx(vs0);
       }
