@@ -913,9 +913,11 @@ __device__ __forceinline__ void tt_show_q(TtCtx<D, NM, QUANT> &c, int m) {
 }
 
 // Values of drafts that the MMA was not shown, back into the rows of O in TMEM (`noted`: the
-// drafts, for this thread's row).  Called by whole warps.
+// drafts, for this thread's row, whose tokens from `first` on, `width` of a tile, are its copy's: another copy's weight
+// beside the draft's may be 0, and its 0 * infinity NaN).  Called by whole warps.
 template <int D>
-__device__ __noinline__ void tt_add_back(const TreeParams &p, const TreeItem &it, unsigned long long noted, uint32_t o_at) {
+__device__ __noinline__ void tt_add_back(const TreeParams &p, const TreeItem &it, unsigned long long noted, int first, int width,
+                                         uint32_t o_at) {
 #pragma unroll 1
   for (int ch = 0; ch < D / 16; ++ch) {
     float o[16];
@@ -925,6 +927,7 @@ __device__ __noinline__ void tt_add_back(const TreeParams &p, const TreeItem &it
     for (int d = 0; d < it.c; ++d) {
       if (!((noted >> d) & 1ull)) continue;
       const int j = it.n - it.c + d;
+      if (static_cast<uint32_t>((j & (TT - 1)) - first) >= static_cast<uint32_t>(width)) continue;
       const long long cell = static_cast<long long>(it.b) * p.max_pages + j / p.P;
       const int fmt = p.page_fmt ? p.page_fmt[cell] : p.uniform_fmt;
       const uint8_t *v = p.v_pool[fmt] +
@@ -1084,7 +1087,7 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
     tc_fence_after();
     const unsigned long long noted = c.S.nonfinite[item_of & (ITEM_RING - 1)] & row.bits;
     leave(item_of);
-    if (__any_sync(0xffffffffu, noted != 0ull)) tt_add_back<D>(p, it, row.copy == 0 ? noted : 0ull, o_at);
+    if (__any_sync(0xffffffffu, noted != 0ull)) tt_add_back<D>(p, it, noted, row.copy * row.width, NM == 1 ? row.width : TT, o_at);
     const bool whole = it.whole();
     const long long slot = (2LL * blockIdx.x + (it.t0 > 0 ? 0 : 1)) * Cfg::RB + row.row;
     const long long to_row = whole ? row.out_row : slot;
