@@ -35,7 +35,7 @@ struct ChunkParams {
   const void *k_in, *v_in;  // write
   void *k_out, *v_out;      // read
   long long k_stride, v_stride;
-  int dense_fmt, num_rows;
+  int num_rows;
 };
 
 // the chunk of sequence b: its dense rows [r0, r0 + n) and first token; n = 0,
@@ -382,7 +382,6 @@ cfr_status chunk_params(const cfr_kv_pool *kv, const int32_t *page_table, int32_
   p->starts = starts;
   p->k_stride = k_stride;
   p->v_stride = v_stride;
-  p->dense_fmt = dense_fmt;
   p->num_rows = num_rows;
   p->k_in = p->v_in = nullptr;
   p->k_out = p->v_out = nullptr;

@@ -1239,9 +1239,10 @@ __device__ void tt_softmax(TtCtx<D, NM, QUANT> &c, bool *timed_out) {
         v_ref = newest >= TT_V_LEAST && newest <= TT_V_MOST ? newest : 1.f;
         v_log = lg2_approx(v_ref);
       }
-      // (the same for the whole warp: TMEM instructions depend on it)
-      const bool one_page = QUANT && scaled && in_one && ks[0] > 0.f && ks[0] < 1e30f &&
-                            __all_sync(0xffffffffu, vs[0] >= v_ref * TT_FOLD_LEAST && vs[0] <= v_ref * TT_FOLD_MOST);
+      // (the same for the whole warp, TMEM instructions depend on it: v_ref may differ between rows)
+      bool one_page = QUANT && scaled && in_one && ks[0] > 0.f && ks[0] < 1e30f && vs[0] >= v_ref * TT_FOLD_LEAST &&
+                      vs[0] <= v_ref * TT_FOLD_MOST;
+      if (QUANT && !FIXED) one_page = __all_sync(0xffffffffu, one_page);
       // Scores as they enter the exponential, in units of log2 e: times the softmax scale
       // (left to the exponential where nothing else is to be done), the pages' scales,
       // capped, less the distance, -inf where the row does not see the token.  Steps with
