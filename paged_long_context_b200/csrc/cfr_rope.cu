@@ -4,9 +4,9 @@
 //   y <- y * rsqrt(mean(y^2) + eps) * w,   (a, b) <- (a c - b s, b c + a s)
 //
 // with c, s the cosine and sine of position * inv_freq.  The angle is reduced to
-// one turn in fp64 (a position of a million times a frequency of 1 has an fp32
-// ulp of 0.06 rad); its sine and cosine, the norm's sum and the products are
-// fp32, rounded once where the row is stored.
+// an eighth of a turn either way in fp64 (a position of a million times a frequency of 1 has an fp32
+// ulp of 0.06 rad, and half a turn in fp32 is still 2^-26 of a turn off); its sine and cosine, the norm's sum
+// and the products are fp32, rounded once where the row is stored.
 //
 // A CTA takes one token of a short step, four of a long one: their cosines and
 // sines are computed once, a thread each, behind one barrier, and serve all query
@@ -110,11 +110,14 @@ __global__ void __launch_bounds__(kRopeThreads, IN == CFR_FMT_F32 ? 3 : 4) rope_
     const int k = i / pairs, f = i - k * pairs;
     constexpr double kInvTurn = 0.15915494309189533577;  // 1 / (2 pi)
     const double turns = static_cast<double>(p.rope_pos[first_t + k]) * p.inv_freq[f] * kInvTurn;
-    const float r = static_cast<float>(turns - rint(turns));
+    const double quarters = rint(4. * turns);
+    const float r = static_cast<float>(turns - 0.25 * quarters);
     float s, c;
     sincospif(2.f * r, &s, &c);
-    cosines[k][f] = c;
-    sines[k][f] = s;
+    // turned back by the quarters
+    const int n = static_cast<int>(static_cast<long long>(quarters) & 3);
+    cosines[k][f] = n == 0 ? c : n == 1 ? -s : n == 2 ? -c : s;
+    sines[k][f] = n == 0 ? s : n == 1 ? c : n == 2 ? -s : -c;
   }
   if (tid >= kRopeThreads - tokens) {   // (the last threads have no sine of one token to compute)
     const int k = kRopeThreads - 1 - tid;

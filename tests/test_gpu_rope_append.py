@@ -186,3 +186,20 @@ def test_long_steps(T, interleaved, in_fmt):
     assert s.run() == 0
     s.check(written=[t for t in range(T) if t not in (5, T - 1)])
     assert int(s.err.item()) == 0
+
+
+@pytest.mark.parametrize("interleaved", [False, True], ids=["half", "pairs"])
+@pytest.mark.parametrize("far", [0, 130000, 1000000])
+def test_sines_and_cosines(far, interleaved):
+    # rows of ones against zeros come back as the cosines and sines themselves: each within the functions' one unit in
+    # the last place (2^-24 at most) and the rounding of an angle of an eighth of a turn (2^-28 of a turn)
+    s = Step(T=1500, Hq=2, Hkv=1, d=128, P=512, B=1, pages=4, in_fmt=F32, fmts=(F32,), norm=False, interleaved=interleaved, far=far)
+    i, j = (slice(0, 128, 2), slice(1, 128, 2)) if interleaved else (slice(0, 64), slice(64, 128))
+    s.q[..., i], s.q[..., j] = 1.0, 0.0
+    assert s.run() == 0
+    torch.cuda.synchronize()
+    a = (s.pos.double().cpu()[:, None] * s.inv.cpu()[None])[:, None]
+    got = s.q_out.double().cpu()
+    tol = 2.0 ** -24 + 2 * np.pi * 2.0 ** -28 + 1e-9
+    assert (got[..., i] - a.cos()).abs().max() <= tol
+    assert (got[..., j] - a.sin()).abs().max() <= tol
