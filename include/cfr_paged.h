@@ -619,7 +619,15 @@ size_t cfr_paged_decode_tree_workspace_size(int32_t batch, int32_t num_queries,
  *  workspace   device, >= cfr_paged_decode_tree_workspace_size(...) bytes, 256-byte
  *              aligned; as for cfr_paged_decode.
  * Everything else (pools, page table, formats, softmax_scale, err_word) as for
- * cfr_paged_decode; max_pages * page_tokens is at most 2^31 - 1025.  A sequence with q_lens[b] outside [0, num_queries] (taken as num_queries), or with
+ * cfr_paged_decode; max_pages * page_tokens is at most 2^31 - 1025.
+ *
+ * Precision is chosen by q_fmt.  With BF16 queries over pages that are not F32 each probability is rounded once
+ * to bf16, the type of the tensor cores' operands (sums, maxima and lse are fp32): an output
+ * element is off by up to 2^-8 of sum_j p_j |v_j|, 0.0015 in the mean square, whatever out_fmt (a chain in
+ * cfr_paged_decode_multi keeps 2^-16).  With F32 queries, or F32 pages, everything is fp32, on a kernel that is some
+ * ten times slower or more.
+ *
+ * A sequence with q_lens[b] outside [0, num_queries] (taken as num_queries), or with
  * n_b < q_lens[b], n_b < 1 or n_b > max_pages * page_tokens and drafts, gets out = 0 and
  * lse = -inf in its drafts' rows and sets CFR_DEVERR_SEQ_LEN.  A drafted token's non-finite
  * K or V reaches only the rows that see it (a non-finite scale of a quantised page may reach

@@ -453,7 +453,8 @@ def paged_decode_tree(pool: KvPool, q, page_table, seq_lens, out, lse, workspace
                       logit_cap: float = 0.0, err=None, stream=None) -> int:
     """cfr_paged_decode_tree: attention of drafted tokens (q is [batch][queries][heads][head_dim])
     over the cache, under a tree mask of int64 bit rows [batch][queries]; returns the status.
-    head_map is a host int32 tensor."""
+    head_map is a host int32 tensor.  bf16 queries have their probabilities rounded to bf16 once, fp32
+    queries keep them in fp32 (on a slower kernel)."""
     dev = _device()
     if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.shape[3] != pool.head_dim:
         raise ValueError("q: a tensor [batch][queries][heads][head_dim] is wanted")
