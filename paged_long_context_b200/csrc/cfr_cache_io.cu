@@ -21,7 +21,8 @@
 // Floor of both: HBM, dense rows once and stored rows once.  The write comes to 3.1 TB/s (34K bf16 tokens of 8
 // heads of 128 into int4 pages: 52 us): about twelve instructions a value take half the
 // issue slots, and a page's two passes leave gaps that three blocks an SM do not
-// close.  Read-back runs at the copy rate (8 x 32K tokens of tiers to bf16: 176 us, 6.1 TB/s).
+// close.  Read-back of long chunks runs near the copy rate (eight sequences of 9K to 32K tokens of tiers to bf16: 176
+// us, 6.1 TB/s); shorter ones are a wave or two of blocks (34K int4 tokens to bf16: 43 us, 4.1 TB/s; 8K: 11 us).
 #include <type_traits>
 
 #include "cfr_cells.cuh"
@@ -440,9 +441,9 @@ cfr_status cfr_read_kv(const cfr_kv_pool *kv, const int32_t *page_table, int32_t
   if (num_rows == 0) return CFR_OK;
   p.k_out = k_out;
   p.v_out = v_out;
-  // rows of a block: 32 where that leaves a block for every SM several times over, fewer for
-  // short chunks, which have to reach all SMs (8 x 32K tokens of tiers: 178 us with 32, 203 with 4; 333 int8
-  // tokens: 7.8 us with 32, 3.1 with 4)
+  // rows of a block: 32 from 600 blocks on (four an SM, of the six that are resident), fewer for
+  // short chunks, which have to reach all SMs (eight sequences of 9K to 32K tokens of tiers: 178 us with 32, 203
+  // with 4; 333 int8 tokens: 7.8 us with 32, 3.1 with 4)
   int per = 32;
   while (per > 4 && num_rows < per * 600) per >>= 1;
   const unsigned blocks = static_cast<unsigned>((static_cast<long long>(num_rows) + per - 1) / per);

@@ -17,8 +17,8 @@
 
 namespace cfr {
 
-// In tiles.  Items of 256 rows end with 64 KiB to write (16 ragged sequences, 64 drafts: 377 us with 0, 343 with
-// 2, 330 with 6, 342 with 10); smaller ones end sooner (5 drafts: 254 us with 2, 259 with 6).
+// In tiles.  Items of 256 rows end with 64 KiB to write (16 ragged sequences, 64 drafts, in bursts: 377 us with 0, 343
+// with 2, 330 with 6, 342 with 10); smaller ones end sooner (5 drafts: 254 us with 2, 259 with 6).
 template <int RB>
 constexpr int tree_item_cost = RB == 256 ? 6 : 2;
 

@@ -44,14 +44,17 @@
 //    become zeros, and non-finite values of drafts are taken out (they would reach, as 0 * NaN, rows that do
 //    not see the draft) and added back at the end to the rows that see it.
 //
-// What bounds it.  64 rows of a kv head over 1M bf16 tokens: HBM (654 us, the copy
-// rate; sustained, the power cap lowers SM clocks to 1.44 GHz and it takes 716).  256 rows (64 drafts, 16 ragged sequences): the softmax, one exponential a
-// score at 16 a clock and SM with its TMEM reads and writes around it (330 us, of 171 for
-// the bytes and 131 for the MMAs).  Quantised pages: instruction fetch and issue, since
-// the expansion, the softmax and the copies together fill the instruction cache, so hot loops are
-// kept rolled and what is rare stands out of line (64 rows, 8 x 32K tokens of tiers, capped: 279 us, of
-// 92 for the bytes).  One short sequence: the latency of one tile's way through the
-// roles (28 rows over 1K tokens: 19 us).
+// What bounds it.  64 rows of a kv head over 1M bf16 tokens: HBM in bursts of ten passes (670 us, 0.98 of the copy
+// rate); sustained, the power cap lowers SM clocks to 1.4 GHz and it takes 800 to 840.  256 rows (64 drafts, 16
+// ragged sequences): 331 us in bursts and 378 to 391 sustained, of 171 for the bytes and 131 for the MMAs, and no
+// unit is full (tensor pipe 39 %, special functions 36 %, issue 38 %): two softmax warps a scheduler each go through
+// wait, loads, exponentials and stores in turn.  Few rows over 16-token pages (5 drafts, the same batch): 258 us in
+// bursts of 169, memory at half its rate and most stalls on loads; which role they belong to was not traced.
+// Quantised pages: one softmax warp a scheduler, whose chain of steps takes 3.5K of the 4.9K
+// clocks of a tile and is lengthened by instruction fetch, since the expansion, the softmax and the copies
+// together fill the instruction cache (so hot loops are kept rolled and what is rare stands out of line; 64 rows,
+// 8 x 32K tokens of tiers: 260 us, capped 280, of 92 for the bytes).  One short sequence: the latency of one
+// tile's way through the roles (28 rows over 1K tokens: 18 us).
 #include <cuda_bf16.h>
 
 #include <climits>
@@ -76,7 +79,7 @@ constexpr float RESCALE_STEP = 8.f;
 // one number, with no maximum and a single pass over the scores: 2^(s - 10) of |s| <= 80 (in units of log2 e,
 // caps up to 55) is between 2^-90 and 2^70, which leaves normal numbers for V, or the V scales of quantised
 // pages, between 2^-36 and 2^28 (of 2^20 tokens that all stand at the cap).  (Eight
-// sequences of 32K tiered tokens, capped at 50: 279 us, and 360 in two passes.)
+// sequences of 32K tiered tokens, capped at 50: 280 us, and 360 in two passes.)
 enum TtMode { PLAIN, GENERAL_SCORES, FIXED_REFERENCE };
 constexpr float TT_FIXED_CAP = 80.f, TT_FIXED_REF = 10.f;
 
@@ -984,7 +987,7 @@ __device__ __forceinline__ void tt_put(const TreeParams &p, bool part, long long
 
 // Caps: c2 tanh(u) of u = s / cap, c2 = cap log2 e (scores are in units of log2 e from here on).
 // Up to |u| = 3/4 tanh(u) = u + u z q(z), z = u^2, q of degree 4 with the least greatest relative
-// error of the whole (2^-24.9, found by exchange): multiply-adds, where the closed form takes two of the 16
+// error of the whole (2^-24.7 with its coefficients in fp32, found by exchange): multiply-adds, where the closed form takes two of the 16
 // special functions a clock and SM, three with the exponential that follows (the ragged batch of 64 drafts,
 // capped at 50: 576 us with the closed form, 497 with this).
 constexpr float TT_CAP_NEAR = 0.75f;
