@@ -325,8 +325,11 @@ _HOT = (torch.float32, torch.bfloat16)
 
 
 def _device() -> int:
-    """The current CUDA device, -1 before CUDA is initialised (the device of host tensors)."""
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+    """The current CUDA device; -1, the device of host tensors, where there is none (the library's
+    own checks can be called there, and it launches nothing)."""
+    if torch.cuda.is_initialized():
+        return torch._C._cuda_getDevice()
+    return torch.cuda.current_device() if torch.cuda.is_available() else -1
 
 
 def _raw_stream(stream, dev: int) -> int:
