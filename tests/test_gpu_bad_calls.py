@@ -106,3 +106,15 @@ def test_bad_lengths_leave_the_other_sequences_right(form, Q):
     case.seq_lens.copy_(right)
     call.q_lens = [Q] * 5
     call.check(skip={(b, i, h) for b in (1, 2, 3) for i in range(Q) for h in range(4)})
+
+
+@pytest.mark.parametrize("Q", [3, 40], ids=["12rows", "160rows"])
+@pytest.mark.parametrize("form", [dict(), dict(fmt="i8", P=64), dict(fmt="f32", q_fmt="f32")], ids=["bf16", "i8", "f32"])
+def test_no_drafts_at_all(form, Q):
+    # nothing to do, whatever the lengths say
+    case = tree_case((200, 90), Q, Hq=4, Hkv=1, **form)
+    case.seq_lens[0], case.seq_lens[1] = -5, 2 ** 31 - 1
+    call = TreeCall(case, q_lens=[0, 0])
+    assert call.run() == 0
+    torch.cuda.synchronize()
+    assert (call.out == 7).all() and (call.lse == 7).all() and int(call.err.item()) == 0
